@@ -8,7 +8,9 @@ if it has not been built.
 from .api import (CapturedAttention, OvcError, Prepared, Repair, attention, attention_prepared, attention_probe,
                   attention_v_repair, attention_workspace_bytes, attn_flags, group_v, device_status, flops, prepare, prepare_v_repair,
                   prepare_workspace_bytes, repair_workspace_bytes, baseline_attention)
+from .paged import (KVCache, kv_cache, kv_cache_read, kv_cache_write, paged_attention, paged_attention_workspace_bytes)
 
 __all__ = ["CapturedAttention", "OvcError", "Prepared", "Repair", "attention", "attention_prepared", "attention_probe",
            "attention_v_repair", "attention_workspace_bytes", "attn_flags", "group_v", "device_status", "flops", "prepare", "prepare_v_repair",
-           "prepare_workspace_bytes", "repair_workspace_bytes", "baseline_attention"]
+           "prepare_workspace_bytes", "repair_workspace_bytes", "baseline_attention",
+           "KVCache", "kv_cache", "kv_cache_read", "kv_cache_write", "paged_attention", "paged_attention_workspace_bytes"]

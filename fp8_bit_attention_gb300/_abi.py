@@ -18,6 +18,7 @@ OVC_ERR_WORKSPACE_TOO_SMALL = 3
 OVC_ERR_CUDA = 4
 OVC_ERR_TIMEOUT = 5
 OVC_ERR_SCRATCH_LIMIT = 6
+OVC_ERR_BAD_INDEX = 7
 OVC_NOALLOC_MAX_HEADS = 4096
 OVC_PREPARE_SMOOTH_K = 1
 OVC_PREPARE_V_SMOOTH = 2
@@ -63,6 +64,20 @@ class OvcProbe(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class OvcKVCache(ctypes.Structure):
+    _fields_ = [("pages", c_i64), ("heads", c_i64), ("page", c_i64), ("k", c_ptr), ("v", c_ptr),
+                ("k_scale", c_ptr), ("v_scale", c_ptr)]
+
+
+class OvcRows(ctypes.Structure):
+    _fields_ = [("ptr", c_ptr), ("dtype", c_i32), ("T", c_i64), ("H", c_i64), ("stride_t", c_i64), ("stride_h", c_i64)]
+
+
+class OvcPagedBatch(ctypes.Structure):
+    _fields_ = [("B", c_i64), ("page_table", c_ptr), ("table_stride", c_i64), ("table_width", c_i32), ("kv_lens", c_ptr),
+                ("cu_q", c_ptr), ("max_q", c_i32), ("causal", c_i32), ("window", c_i32)]
+
+
 P = ctypes.POINTER
 SIGNATURES = {
     "ovc_prepare_workspace_bytes": (ctypes.c_size_t, [c_i64, c_i64, c_i64, c_i64]),
@@ -94,6 +109,11 @@ SIGNATURES = {
     "ovc_attention_host_workspace_bytes": (ctypes.c_size_t, [c_i64, c_i64, c_i64, c_i32, ctypes.c_uint32,
                                                              ctypes.c_float]),
     "ovc_host_chunk_plan": (c_i32, [c_i64, c_i64, c_i32, c_ptr, c_i32]),
+    "ovc_kv_write": (c_i32, [P(OvcKVCache), P(OvcRows), P(OvcRows), c_ptr, c_ptr]),
+    "ovc_kv_read": (c_i32, [P(OvcKVCache), c_ptr, P(OvcRows), P(OvcRows), c_ptr]),
+    "ovc_paged_attention_workspace_bytes": (ctypes.c_size_t, [P(OvcRows), P(OvcKVCache), P(OvcPagedBatch)]),
+    "ovc_paged_attention": (c_i32, [P(OvcRows), P(OvcKVCache), P(OvcPagedBatch), ctypes.c_float, P(OvcRows), c_ptr, c_ptr,
+                                    ctypes.c_size_t, c_ptr]),
 }
 
 _lock = threading.Lock()

@@ -16,13 +16,15 @@
 #include "ovc.h"
 #include "attention.cuh"
 #include "group.cuh"
+#include "host.cuh"
 #include "prepare.cuh"
 #include "repair.cuh"
 
 namespace ovc {
 
 // Device-side status word: kernels OR in kStatusTimeout when a bounded wait
-// expires.  Read and cleared by ovc_get_device_status().
+// expires, kStatusBadIndex when a paged call meets an index out of range.
+// Read and cleared by ovc_get_device_status().
 __device__ unsigned int g_status;
 
 namespace {
@@ -63,15 +65,10 @@ constexpr int kMaxDevices = 64;
 constexpr uint32_t kPrepareFlags = OVC_PREPARE_SMOOTH_K | OVC_PREPARE_V_SMOOTH | OVC_PREPARE_SMOOTH_Q;
 constexpr uint64_t kDefaultTimeoutNs = 4000000000ull;   // 4 s per wait
 
-struct DeviceState {
-  bool init = false;
-  bool supported = false;
-  int sms = 0;
-  unsigned int* status = nullptr;
-};
-
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
+
+}  // namespace
 
 ovc_status device_state(DeviceState** out) {
   int dev = 0;
@@ -98,6 +95,7 @@ ovc_status device_state(DeviceState** out) {
       if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return OVC_ERR_CUDA;
       d.status = static_cast<unsigned int*>(p);
     }
+    d.index = dev;
     d.init = true;
   }
   *out = &d;
@@ -117,6 +115,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+namespace {
 
 // 2-D byte tensor [rows][inner] (row pitch `pitch` bytes), 128x128 boxes,
 // 128-byte swizzle (the layout tcgen05 reads as K-major SW128).
@@ -703,7 +703,7 @@ ovc_status ovc_get_device_status(void* stream) {
   if (word != 0) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return OVC_ERR_CUDA;
-    return OVC_ERR_TIMEOUT;
+    return (word & kStatusTimeout) ? OVC_ERR_TIMEOUT : OVC_ERR_BAD_INDEX;
   }
   return OVC_OK;
 }
@@ -717,6 +717,7 @@ const char* ovc_status_string(ovc_status s) {
     case OVC_ERR_CUDA: return "CUDA runtime error";
     case OVC_ERR_TIMEOUT: return "a device-side wait timed out";
     case OVC_ERR_SCRATCH_LIMIT: return "B*H exceeds the fixed scratch of ovc_prepare_noalloc (OVC_NOALLOC_MAX_HEADS)";
+    case OVC_ERR_BAD_INDEX: return "a slot, page or length of a paged call lay outside its cache, page table or rows";
   }
   return "unknown status";
 }

@@ -1,0 +1,148 @@
+// paged.cu -- libovc's paged FP8 KV cache (see include/ovc.h): the entry
+// points that check arguments and launch on the caller's stream.  A
+// translation unit of its own, compiled beside ovc.cu.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "ovc.h"
+#include "host.cuh"
+#include "paged.cuh"
+#include "paged_simple.cuh"
+
+namespace ovc {
+namespace {
+
+static_assert(kPagedBadIndex == kStatusBadIndex, "status bits");
+
+bool at16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool at4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool cache_ok(const ovc_kv_cache* c) {
+  if (!c || c->pages < 1 || c->heads < 1 || c->page < 16 || c->page > 1024 || c->page % 16) return false;
+  if (!at16(c->k) || !at16(c->v) || !at16(c->k_scale) || !at16(c->v_scale)) return false;
+  constexpr int64_t kMost = (int64_t{1} << 31) - 1024;
+  return c->heads <= 65535 && c->pages <= kMost && c->pages * c->page <= kMost &&
+         c->pages * c->page * c->heads <= kMost;
+}
+
+ovc_status rows_ok(const ovc_rows* r) {
+  if (!r || r->T < 1 || r->H < 1 || r->T > 0x7FFFFFFF || r->H > 65535 * 256) return OVC_ERR_INVALID_ARG;
+  if (!at16(r->ptr) || r->stride_t % 8 || r->stride_h % 8 || r->stride_t < 0 || r->stride_h < 0) return OVC_ERR_INVALID_ARG;
+  return r->dtype == OVC_BF16 || r->dtype == OVC_FP16 ? OVC_OK : OVC_ERR_UNSUPPORTED;
+}
+
+CacheView view(const ovc_kv_cache* c) {
+  return {c->k, c->v, c->k_scale, c->v_scale, static_cast<int32_t>(c->pages), static_cast<int32_t>(c->heads),
+          static_cast<int32_t>(c->page)};
+}
+
+RowsView view(const ovc_rows* r) { return {r->ptr, r->stride_t, r->stride_h}; }
+
+ovc_status launched() { return cudaGetLastError() == cudaSuccess ? OVC_OK : OVC_ERR_CUDA; }
+
+// Arguments that ovc_kv_write and ovc_kv_read share.
+ovc_status cache_call_ok(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows* v, const int32_t* slots) {
+  if (!cache_ok(c) || !at4(slots)) return OVC_ERR_INVALID_ARG;
+  ovc_status st = rows_ok(k);
+  if (st != OVC_OK) return st;
+  st = rows_ok(v);
+  if (st != OVC_OK) return st;
+  if (k->T != v->T || k->H != c->heads || v->H != c->heads || k->dtype != v->dtype) return OVC_ERR_INVALID_ARG;
+  return (k->T * k->H + kCacheVecs - 1) / kCacheVecs <= 0x7FFFFFFF ? OVC_OK : OVC_ERR_INVALID_ARG;
+}
+
+bool batch_ok(const ovc_paged_batch* b) {
+  if (!b || b->B < 1 || b->B > 0x7FFFFFF || b->table_width < 1 || b->table_stride < b->table_width) return false;
+  if (!at4(b->page_table) || !at4(b->kv_lens) || (b->cu_q && !at4(b->cu_q))) return false;
+  return b->max_q >= 0 && (b->causal == 0 || b->causal == 1) && b->window >= 0 && (b->causal || b->window == 0);
+}
+
+ovc_status paged_ok(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b) {
+  if (!cache_ok(c) || !batch_ok(b)) return OVC_ERR_INVALID_ARG;
+  const ovc_status st = rows_ok(q);
+  if (st != OVC_OK) return st;
+  if (q->H % c->heads || (!b->cu_q && q->T != b->B)) return OVC_ERR_INVALID_ARG;
+  return q->T * q->H <= 0x7FFFFFFF ? OVC_OK : OVC_ERR_INVALID_ARG;
+}
+
+}  // namespace
+}  // namespace ovc
+
+using namespace ovc;
+
+extern "C" {
+
+ovc_status ovc_kv_write(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows* v, const int32_t* slots,
+                        void* stream) {
+  ovc_status st = cache_call_ok(c, k, v, slots);
+  if (st != OVC_OK) return st;
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != OVC_OK) return st;
+  const int64_t n = k->T * k->H;
+  const dim3 grid(static_cast<unsigned>((n + kCacheVecs - 1) / kCacheVecs), 2);
+  auto* fn = k->dtype == OVC_FP16 ? kv_write_kernel<true> : kv_write_kernel<false>;
+  fn<<<grid, kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(view(c), view(k), view(v), slots, n, dev->status);
+  return launched();
+}
+
+ovc_status ovc_kv_read(const ovc_kv_cache* c, const int32_t* slots, const ovc_rows* k, const ovc_rows* v,
+                       void* stream) {
+  ovc_status st = cache_call_ok(c, k, v, slots);
+  if (st != OVC_OK) return st;
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != OVC_OK) return st;
+  const int64_t n = k->T * k->H;
+  const dim3 grid(static_cast<unsigned>((n + kCacheVecs - 1) / kCacheVecs), 2);
+  auto* fn = k->dtype == OVC_FP16 ? kv_read_kernel<true> : kv_read_kernel<false>;
+  fn<<<grid, kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(view(c), view(k), view(v), slots, n, dev->status);
+  return launched();
+}
+
+size_t ovc_paged_attention_workspace_bytes(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b) {
+  return paged_ok(q, c, b) == OVC_OK ? 256 : 0;
+}
+
+ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b,
+                               float softmax_scale, const ovc_rows* o, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  ovc_status st = paged_ok(q, c, b);
+  if (st != OVC_OK) return st;
+  st = rows_ok(o);
+  if (st != OVC_OK) return st;
+  if (o->T != q->T || o->H != q->H || o->dtype != OVC_BF16 || (lse && !at4(lse))) return OVC_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return OVC_ERR_INVALID_ARG;
+  if (workspace_bytes < ovc_paged_attention_workspace_bytes(q, c, b)) return OVC_ERR_WORKSPACE_TOO_SMALL;
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != OVC_OK) return st;
+  PagedParams P{};
+  P.c = view(c);
+  P.q = view(q);
+  P.o = view(o);
+  P.lse = lse;
+  P.table = b->page_table;
+  P.table_stride = b->table_stride;
+  P.width = b->table_width;
+  P.kv_lens = b->kv_lens;
+  P.cu_q = b->cu_q;
+  P.B = static_cast<int32_t>(b->B);
+  P.T = static_cast<int32_t>(q->T);
+  P.Hq = static_cast<int32_t>(q->H);
+  P.group = static_cast<int32_t>(q->H / c->heads);
+  P.causal = b->causal;
+  P.window = b->window;
+  const double sm = softmax_scale > 0.0f ? static_cast<double>(softmax_scale) : 1.0 / std::sqrt(128.0);
+  P.c2 = static_cast<float>(1.4426950408889634074 * sm);
+  P.status = dev->status;
+  const int64_t warps = q->T * q->H;
+  auto* fn = q->dtype == OVC_FP16 ? paged_simple_kernel<true> : paged_simple_kernel<false>;
+  fn<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(P);
+  return launched();
+}
+
+}  // extern "C"

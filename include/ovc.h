@@ -20,8 +20,8 @@
  *     about 8*log2(v)+56; beta = -0.35.
  *
  * Conventions for every call:
- *   - All pointers inside ovc_tensor / ovc_output / ovc_prepared / ovc_repair
- *     are DEVICE pointers of the current CUDA device.  The caller owns every
+ *   - All pointers inside ovc_tensor / ovc_output / ovc_prepared / ovc_repair /
+ *     ovc_kv_cache / ovc_rows / ovc_paged_batch are DEVICE pointers of the current CUDA device.  The caller owns every
  *     buffer; the library never allocates or frees device memory.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Every
  *     call is asynchronous on it; argument errors are returned synchronously
@@ -50,7 +50,9 @@ typedef enum {
   OVC_ERR_WORKSPACE_TOO_SMALL = 3,  /* workspace_bytes below the *_workspace_bytes() figure */
   OVC_ERR_CUDA = 4,                 /* a CUDA runtime call failed */
   OVC_ERR_TIMEOUT = 5,              /* a device-side wait hit its limit */
-  OVC_ERR_SCRATCH_LIMIT = 6         /* ovc_prepare_noalloc: B*H above its fixed scratch */
+  OVC_ERR_SCRATCH_LIMIT = 6,        /* ovc_prepare_noalloc: B*H above its fixed scratch */
+  OVC_ERR_BAD_INDEX = 7             /* reported by ovc_get_device_status: a paged call met a slot, page or
+                                       length outside its cache, page table or rows */
 } ovc_status;
 
 enum { OVC_BF16 = 0, OVC_FP16 = 1 };
@@ -409,6 +411,106 @@ size_t ovc_attention_host_workspace_bytes(int64_t B, int64_t S, int64_t max_chun
  * for the attention kernel's pairs of 128-row query blocks (nb = ceil(S/128));
  * sms = the device's SM count. */
 int32_t ovc_host_chunk_plan(int64_t H, int64_t tiles_per_head, int32_t sms, int32_t* sizes, int32_t max_chunks);
+
+/* ---------------------------------------------------------------------------
+ * The paged FP8 KV cache: keys and values of growing sequences, quantised to
+ * E4M3 as they are written, read back, and attended by new tokens (chunked
+ * prefill, verification of drafted tokens, single-token decoding).  No
+ * counterpart in the pages, whose call takes whole sequences; head dim 128,
+ * BF16/FP16 inputs and BF16 output as there.
+ *
+ * A cache is `pages` pages of `page` tokens of each of `heads` KV heads:
+ *   k, v              [pages, heads, page, 128] E4M3 codes, 16-byte aligned
+ *   k_scale, v_scale  [pages, heads, page] one E8M0 byte e per vector, 16-byte
+ *                     aligned: scale 2^(e-127); 255 is NaN
+ * `page` is a multiple of 16, at most 1024, and pages*heads*page < 2^31 - 1024.
+ * Token slot s is row s % page of page s / page, in every head.
+ *
+ * Quantising a vector x: e is the least value in 0..254 with
+ * max|x| <= 448 * 2^(e-127) (127 for a zero vector), and code =
+ * E4M3(x * 2^(127-e)), to nearest even.  Scales are powers of two because a
+ * token is written once and never requantised: its scale is its own, the
+ * scaling is exact in every type, and a code times its scale is a BF16 value.
+ * A vector that holds a NaN or an infinity gets e = 255 and zero codes; it
+ * reads back as NaN, and attention gives NaN in the rows that see it and in no
+ * others.  Slots never written may hold anything: no call reads them as long
+ * as the lengths given stay within what was written. */
+typedef struct {
+  int64_t pages, heads, page;
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+} ovc_kv_cache;
+
+/* Rows of heads [T,H,128], BF16 or FP16; strides in elements, multiples of 8,
+ * unit channel stride, 16-byte aligned. */
+typedef struct {
+  void* ptr;
+  int32_t dtype;                    /* OVC_BF16 or OVC_FP16 */
+  int64_t T, H;
+  int64_t stride_t, stride_h;
+} ovc_rows;
+
+/* Quantise the T tokens' keys and values (same T, H = c->heads and dtype) and
+ * write token t to slot slots[t] (device, int32).  A negative slot skips its
+ * token (padding); one beyond the cache is skipped too and reported as
+ * OVC_ERR_BAD_INDEX by ovc_get_device_status().  The slots of one call are
+ * distinct (a slot given twice holds parts of both tokens). */
+ovc_status ovc_kv_write(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows* v, const int32_t* slots,
+                        void* stream);
+
+/* Read tokens back: rows t of k and v become the values of slot slots[t] in
+ * the rows' dtype (exact in BF16 and FP16 within their ranges, otherwise to
+ * nearest even).  A negative slot gives zeros; so does one beyond the cache,
+ * which is reported as for ovc_kv_write. */
+ovc_status ovc_kv_read(const ovc_kv_cache* c, const int32_t* slots, const ovc_rows* k, const ovc_rows* v,
+                       void* stream);
+
+/* A batch of B sequences over a cache.  All arrays are int32 on the device.
+ *   page_table  [B, table_width], row stride table_stride: the pages of each
+ *               sequence in order; only its first ceil(kv_len/page) are read
+ *   kv_lens     [B] tokens in the cache, the new ones among them
+ *   cu_q        [B+1] first query row of each sequence (ascending, from 0 on),
+ *               or NULL: one row each.  Sequence b's rows are its last
+ *               cu_q[b+1] - cu_q[b] tokens: row i stands at position
+ *               kv_len - n + i.
+ *   max_q       the most rows of any sequence, as far as the host knows (0:
+ *               unknown); it chooses between kernels, the result holds for any
+ *   causal      1: a row sees keys at its own position and before; 0: all keys
+ *   window      with causal: the last `window` of those only; 0: no limit
+ * A row that sees no key (kv_len 0, or more rows than tokens) gives 0, and
+ * -inf as its log-sum.  Rows of no sequence (before cu_q[0], from cu_q[B] on)
+ * are left as they were.  Lengths beyond the page table, rows beyond q, and
+ * pages beyond the cache among those read are cut off, the affected sequences'
+ * rows unspecified, and reported as OVC_ERR_BAD_INDEX. */
+typedef struct {
+  int64_t B;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int32_t table_width;
+  const int32_t* kv_lens;
+  const int32_t* cu_q;
+  int32_t max_q;
+  int32_t causal;
+  int32_t window;
+} ovc_paged_batch;
+
+/* Device bytes ovc_paged_attention needs (0 for invalid arguments). */
+size_t ovc_paged_attention_workspace_bytes(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b);
+
+/* o[t,h] = softmax(q[t,h] . K * softmax_scale) V over the keys that row t sees,
+ * KV head h / (q->H / c->heads); q->H is a multiple of c->heads.  o is BF16,
+ * shaped like q.  lse, if not NULL, receives the natural log-sum-exp of the
+ * scaled scores, FP32 [T, H] contiguous.  softmax_scale <= 0 selects
+ * 1/sqrt(128).  A query row that holds a NaN or an infinity gives NaN.
+ * Long sequences are split over the GPU and joined from the workspace
+ * (256-byte aligned); calls that share it must not overlap.  The way of
+ * splitting depends on all lengths of the batch: the last bits of a sequence's
+ * rows may differ between batches. */
+ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b,
+                               float softmax_scale, const ovc_rows* o, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,7 +10,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in ("ovc.cu", "paged.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("ptx.cuh", "prepare.cuh", "attention.cuh", "repair.cuh", "group.cuh",
-                                           "host_stream.cuh", "host.cuh", "paged.cuh", "paged_simple.cuh")]
+                                           "host_stream.cuh", "host.cuh", "paged.cuh", "paged_plan.cuh",
+                                           "paged_decode.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libovc.so")

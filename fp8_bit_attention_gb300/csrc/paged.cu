@@ -6,11 +6,12 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "ovc.h"
 #include "host.cuh"
 #include "paged.cuh"
-#include "paged_simple.cuh"
+#include "paged_decode.cuh"
 
 namespace ovc {
 namespace {
@@ -65,7 +66,85 @@ ovc_status paged_ok(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_ba
   const ovc_status st = rows_ok(q);
   if (st != OVC_OK) return st;
   if (q->H % c->heads || (!b->cu_q && q->T != b->B)) return OVC_ERR_INVALID_ARG;
-  return q->T * q->H <= 0x7FFFFFFF ? OVC_OK : OVC_ERR_INVALID_ARG;
+  return q->T * q->H <= 0x7FFFFC00 ? OVC_OK : OVC_ERR_INVALID_ARG;
+}
+
+// Cache codes as rows of 128 bytes, boxes of `box` rows, 128-byte swizzle.
+bool make_cache_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int common_divisor(int a, int b) { return b ? common_divisor(b, a % b) : a; }
+
+constexpr uint64_t kTimeoutNs = 4000000000ull;    // 4 s per wait
+constexpr int kMaxCtas = 160;                     // of a persistent grid: one per SM
+constexpr int kDecodeMinShare = 8;                // blocks: one for each warp
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Query rows of a tile: the smallest of the kernels' that holds a sequence's
+// rows of one KV head.
+int tile_rows(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b) {
+  const int64_t group = q->H / c->heads;
+  const int64_t most = (b->cu_q ? (b->max_q > 0 ? b->max_q : q->T) : 1) * group;
+  return most <= 8 ? 8 : most <= 16 ? 16 : 32;
+}
+
+size_t work_bytes(int R, PagedWork* w, void* base) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  const size_t o = up256(static_cast<size_t>(kMaxCtas) * 2 * R * 512), l = up256(static_cast<size_t>(kMaxCtas) * 2 * R * 4);
+  if (w) {
+    w->o = reinterpret_cast<float*>(p);
+    w->lse = reinterpret_cast<float*>(p + o);
+    w->cut = reinterpret_cast<CutTile*>(p + o + l);
+  }
+  return o + l + up256(kMaxCtas * sizeof(CutTile));
+}
+
+using DecodeFn = decltype(&paged_decode_kernel<false, 1>);
+
+DecodeFn decode_fn(bool half, int R) {
+  if (R == 8) return half ? paged_decode_kernel<true, 1> : paged_decode_kernel<false, 1>;
+  if (R == 16) return half ? paged_decode_kernel<true, 2> : paged_decode_kernel<false, 2>;
+  return half ? paged_decode_kernel<true, 4> : paged_decode_kernel<false, 4>;
+}
+
+std::mutex g_paged_mu;
+bool g_paged_init[64];
+
+// Shared memory limits of the attention kernels, once per device.
+ovc_status paged_init(int device) {
+  std::lock_guard<std::mutex> lock(g_paged_mu);
+  if (g_paged_init[device]) return OVC_OK;
+  for (int R = 8; R <= 32; R *= 2)
+    for (int half = 0; half < 2; ++half)
+      if (cudaFuncSetAttribute(decode_fn(half, R), cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(DecodeSmem)) != cudaSuccess)
+        return OVC_ERR_CUDA;
+  g_paged_init[device] = true;
+  return OVC_OK;
+}
+
+// The join, launched while the attention kernel before it still runs.
+template <int R, int kWarps>
+cudaError_t launch_join(const PagedParams& P, const PagedWork& w, int ctas, cudaStream_t s) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, R / (kJoinThreads / 32 / kWarps));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<R, kWarps>, P, w);
 }
 
 }  // namespace
@@ -104,7 +183,7 @@ ovc_status ovc_kv_read(const ovc_kv_cache* c, const int32_t* slots, const ovc_ro
 }
 
 size_t ovc_paged_attention_workspace_bytes(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b) {
-  return paged_ok(q, c, b) == OVC_OK ? 256 : 0;
+  return paged_ok(q, c, b) == OVC_OK ? work_bytes(tile_rows(q, c, b), nullptr, nullptr) : 0;
 }
 
 ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b,
@@ -139,9 +218,25 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
   const double sm = softmax_scale > 0.0f ? static_cast<double>(softmax_scale) : 1.0 / std::sqrt(128.0);
   P.c2 = static_cast<float>(1.4426950408889634074 * sm);
   P.status = dev->status;
-  const int64_t warps = q->T * q->H;
-  auto* fn = q->dtype == OVC_FP16 ? paged_simple_kernel<true> : paged_simple_kernel<false>;
-  fn<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(P);
+  PagedMaps M{};
+  M.rows = static_cast<int32_t>(c->pages * c->heads * c->page);
+  M.box = common_divisor(static_cast<int>(c->page), kDecKeys);
+  M.min_share = kDecodeMinShare;
+  M.timeout_ns = kTimeoutNs;
+  if (!make_cache_map(&M.k, c->k, M.rows, M.box) || !make_cache_map(&M.v, c->v, M.rows, M.box)) return OVC_ERR_CUDA;
+  st = paged_init(dev->index);
+  if (st != OVC_OK) return st;
+  const int R = tile_rows(q, c, b);
+  PagedWork w;
+  work_bytes(R, &w, workspace);
+  const int ctas = dev->sms < kMaxCtas ? dev->sms : kMaxCtas;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  decode_fn(q->dtype == OVC_FP16, R)<<<ctas, kDecThreads, sizeof(DecodeSmem), s>>>(P, M, w);
+  st = launched();
+  if (st != OVC_OK) return st;
+  const cudaError_t err = R == 8 ? launch_join<8, 4>(P, w, ctas, s) : R == 16 ? launch_join<16, 4>(P, w, ctas, s)
+                                                                            : launch_join<32, 4>(P, w, ctas, s);
+  if (err != cudaSuccess) return OVC_ERR_CUDA;
   return launched();
 }
 

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -82,11 +83,9 @@ bool make_cache_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int common_divisor(int a, int b) { return b ? common_divisor(b, a % b) : a; }
-
 constexpr uint64_t kTimeoutNs = 4000000000ull;    // 4 s per wait
-constexpr int kMaxCtas = 160;                     // of a persistent grid: one per SM
-constexpr int kDecodeMinShare = 8;                // blocks: one for each warp
+constexpr int kMaxSms = 160;                      // that a persistent grid uses
+constexpr int kDecodeMinShare = 16;               // blocks
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -98,15 +97,29 @@ int tile_rows(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b
   return most <= 8 ? 8 : most <= 16 ? 16 : 32;
 }
 
+// CTAs per SM of the kernel with tiles of R rows.
+int ctas_per_sm(int R) { return R == 8 ? kDecodeCtas<1> : R == 16 ? kDecodeCtas<2> : kDecodeCtas<4>; }
+
 size_t work_bytes(int R, PagedWork* w, void* base) {
   uint8_t* p = static_cast<uint8_t*>(base);
-  const size_t o = up256(static_cast<size_t>(kMaxCtas) * 2 * R * 512), l = up256(static_cast<size_t>(kMaxCtas) * 2 * R * 4);
+  const size_t ctas = static_cast<size_t>(kMaxSms) * ctas_per_sm(R);
+  const size_t o = up256(ctas * 2 * R * 512), l = up256(ctas * 2 * R * 4);
   if (w) {
     w->o = reinterpret_cast<float*>(p);
     w->lse = reinterpret_cast<float*>(p + o);
     w->cut = reinterpret_cast<CutTile*>(p + o + l);
   }
-  return o + l + up256(kMaxCtas * sizeof(CutTile));
+  return o + l + up256(ctas * sizeof(CutTile));
+}
+
+// The unit of paged_plan.cuh's line: the least with which all tiles' places are
+// sure to fit 31 bits, whatever the lengths.
+int line_unit(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b, int R, int BK, int cost) {
+  const double tiles = (static_cast<double>(q->T) * (q->H / c->heads) / R + b->B) * c->heads;
+  const double blocks = static_cast<double>(b->table_width) * c->page / BK + cost + 1;
+  int unit = 0;
+  while (tiles * (std::ldexp(blocks, -unit) + 1) > 2.0e9 && unit < 27) ++unit;
+  return unit;
 }
 
 using DecodeFn = decltype(&paged_decode_kernel<false, 1>);
@@ -206,13 +219,15 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
   P.lse = lse;
   P.table = b->page_table;
   P.table_stride = b->table_stride;
-  P.width = b->table_width;
+  P.most = static_cast<int32_t>(std::min<int64_t>(b->table_width * c->page, 0x7FFFFF00));
   P.kv_lens = b->kv_lens;
   P.cu_q = b->cu_q;
   P.B = static_cast<int32_t>(b->B);
   P.T = static_cast<int32_t>(q->T);
   P.Hq = static_cast<int32_t>(q->H);
   P.group = static_cast<int32_t>(q->H / c->heads);
+  P.by_group = fast_div(P.group);
+  P.by_page = fast_div(P.c.page);
   P.causal = b->causal;
   P.window = b->window;
   const double sm = softmax_scale > 0.0f ? static_cast<double>(softmax_scale) : 1.0 / std::sqrt(128.0);
@@ -220,16 +235,16 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
   P.status = dev->status;
   PagedMaps M{};
   M.rows = static_cast<int32_t>(c->pages * c->heads * c->page);
-  M.box = common_divisor(static_cast<int>(c->page), kDecKeys);
   M.min_share = kDecodeMinShare;
   M.timeout_ns = kTimeoutNs;
-  if (!make_cache_map(&M.k, c->k, M.rows, M.box) || !make_cache_map(&M.v, c->v, M.rows, M.box)) return OVC_ERR_CUDA;
+  if (!make_cache_map(&M.k, c->k, M.rows, kDecKeys) || !make_cache_map(&M.v, c->v, M.rows, kDecKeys)) return OVC_ERR_CUDA;
   st = paged_init(dev->index);
   if (st != OVC_OK) return st;
   const int R = tile_rows(q, c, b);
+  P.unit = line_unit(q, c, b, R, kDecKeys, kTileCost<kDecKeys>);
   PagedWork w;
   work_bytes(R, &w, workspace);
-  const int ctas = dev->sms < kMaxCtas ? dev->sms : kMaxCtas;
+  const int ctas = (dev->sms < kMaxSms ? dev->sms : kMaxSms) * ctas_per_sm(R);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   decode_fn(q->dtype == OVC_FP16, R)<<<ctas, kDecThreads, sizeof(DecodeSmem), s>>>(P, M, w);
   st = launched();

@@ -158,17 +158,39 @@ __global__ void __launch_bounds__(kCacheThreads)
 // ---------------------------------------------------------------------------
 // Attention: parameters and the sequences of a batch
 // ---------------------------------------------------------------------------
+// Division of 0 <= n < 2^31 by a number known at the launch: with 2^(s-1) < d <=
+// 2^s and m = floor(2^32 (2^s - d) / d) + 1, n / d = (m n / 2^32 + n) >> s.  (A
+// division by a register is about 20 dependent instructions, and a CTA does a
+// dozen of them before its first load.)
+struct FastDiv {
+  uint32_t m, s;
+  int32_t d;
+};
+
+__host__ inline FastDiv fast_div(int32_t d) {
+  FastDiv f{0, 0, d};
+  while ((int64_t{1} << f.s) < d) ++f.s;
+  f.m = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << f.s) - d)) / d + 1);
+  return f;
+}
+
+__device__ __forceinline__ int operator/(int n, const FastDiv& f) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), f.m) + static_cast<uint32_t>(n)) >> f.s);
+}
+
 struct PagedParams {
   CacheView c;
   RowsView q, o;
   float* lse;
   const int32_t* table;
   int64_t table_stride;
-  int32_t width;
   const int32_t* kv_lens;
   const int32_t* cu_q;
   int32_t B, T, Hq, group;
+  FastDiv by_group, by_page;
   int32_t causal, window;
+  int32_t most;             // tokens that a page table row holds
+  int32_t unit;             // log2 of the key blocks between the places where work may be cut
   float c2;                 // softmax_scale * log2(e)
   unsigned int* status;
 };
@@ -188,11 +210,10 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& P, int b) {
     e = __ldg(P.cu_q + b + 1);
   }
   const int kv = __ldg(P.kv_lens + b);
-  const int most = static_cast<int>(min(static_cast<int64_t>(P.width) * P.c.page, static_cast<int64_t>(0x7FFFFF00)));
-  s.bad = a < 0 || e < a || e > P.T || kv < 0 || kv > most;
+  s.bad = a < 0 || e < a || e > P.T || kv < 0 || kv > P.most;
   s.q0 = min(max(a, 0), P.T);
   s.ql = min(max(e, s.q0), P.T) - s.q0;
-  s.kv = min(max(kv, 0), most);
+  s.kv = min(max(kv, 0), P.most);
   return s;
 }
 

@@ -25,7 +25,8 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 
 // A cut tile, written by the second CTA that works on it (c0 + 1).
 struct CutTile {
-  int32_t b, h, i, c0, c1;    // c1 < 0: none
+  int32_t c0, c1;             // the CTAs that work on it; c1 < 0: none
+  int32_t q0, p0, rows, h;    // its first row is packed row p0 of the sequence whose rows start at q0
 };
 
 // Workspace of one call.
@@ -41,8 +42,8 @@ template <int R, int BK>
 __device__ __forceinline__ void tile_blocks(const PagedParams& P, const Seq& s, int i, int& k0, int& k1) {
   const int rows = s.ql * P.group;
   int lo, hi, x;
-  row_range(P, s, i * R / P.group, lo, x);
-  row_range(P, s, (min(rows, i * R + R) - 1) / P.group, x, hi);
+  row_range(P, s, i * R / P.by_group, lo, x);
+  row_range(P, s, (min(rows, i * R + R) - 1) / P.by_group, x, hi);
   k0 = 0;
   k1 = 1;
   if (hi >= lo) {
@@ -60,148 +61,178 @@ __device__ __forceinline__ int tiles_of(const PagedParams& P, const Seq& s) {
 // out), in blocks: each tile stands for so many more blocks on the line, behind
 // its own, where there is nothing to do.
 template <int BK>
-constexpr int kTileCost = BK == 32 ? 8 : 2;
+constexpr int kTileCost = BK < 128 ? 8 : 2;
 
-constexpr int kPlanSeqs = 256;
+// The line is cut at places 2^unit blocks apart; the host takes unit = 0 unless
+// the line could then pass 31 bits.
+template <int BK>
+__device__ __forceinline__ int tile_places(const PagedParams& P, int t0, int t1) {
+  return (t1 - t0 + kTileCost<BK> - 1 >> P.unit) + 1;
+}
+
+// A CTA's share: it starts at place `off` of tile (b, i, h), whose key blocks
+// are [t0, t1), and is `len` places of the line long.
+struct Share {
+  Seq s;
+  int b, h, i, off, t0, t1;
+  int len, at, share;
+};
 
 struct PlanSmem {
-  long long blocks[kPlanSeqs];     // of each sequence of a chunk, one head
-  long long sums[kPlanSeqs / 32];
-  long long total;
-  int b, h, i, off;
+  int places[160];           // of each sequence of a chunk, one head
+  int sums[8];
+  int rem;
+  Share found;
 };
 
-// A CTA's share: it starts at place `off` of tile (b, i, h) and is `len` places
-// of the line long.
-struct Share {
-  int b, h, i, off;
-  long long len, at, share;
-};
+// Inclusive sum of w over threads 0 .. N - 1 of the CTA, and all of it.
+template <int N>
+__device__ __forceinline__ int cta_scan(int w, PlanSmem& sm, int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int v = w;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += u;
+  }
+  if (lane == 31 && warp < N / 32) sm.sums[warp] = v;
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) {
+    const int x = sm.sums[k];
+    if (k < warp) v += x;
+    all += x;
+  }
+  __syncthreads();
+  return v;
+}
 
-// Computed by the whole CTA (kThreads >= kPlanSeqs); kLanes threads add up one
+// Computed by the whole CTA, N sequences at a time; kLanes threads add up one
 // sequence's tiles (1 where sequences have a tile or two, 32 where many).
 // min_share: the least places worth a CTA.
 template <int R, int BK, int kThreads, int kLanes>
 __device__ Share plan_share(const PagedParams& P, PlanSmem& sm, int min_share) {
+  constexpr int N = kThreads < 160 ? kThreads : 160;
   const int tid = threadIdx.x, lane = tid & 31;
-  Share out{};
-  long long base = 0;
-  // Pass 0 adds up the line; pass 1 finds the share's start.  A batch of one
-  // chunk keeps its sums between the passes.
+  // Places of sequence b0 + tid, all heads.
+  auto places = [&](int b0, bool first) {
+    const int n = min(N, P.B - b0);
+    int w = 0;
+    if (kLanes == 1) {
+      if (tid < n) {
+        const Seq s = load_seq(P, b0 + tid);
+        if (s.bad && first && blockIdx.x == 0) atomicOr(P.status, kPagedBadIndex);
+        const int nt = tiles_of<R>(P, s);
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    base = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < P.B; b0 += kPlanSeqs) {
-      const int n = min(kPlanSeqs, P.B - b0);
-      if (pass == 0 || P.B > kPlanSeqs) {
-        __syncthreads();
-        for (int j = tid / kLanes; j < n; j += kThreads / kLanes) {
-          const Seq s = load_seq(P, b0 + j);
-          const int nt = tiles_of<R>(P, s);
-          long long w = 0;
-          for (int i = tid % kLanes; i < nt; i += kLanes) {
-            int k0, k1;
-            tile_blocks<R, BK>(P, s, i, k0, k1);
-            w += k1 - k0 + kTileCost<BK>;
-          }
-          if (kLanes == 32) {
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
-          }
-          if (tid % kLanes == 0) {
-            sm.blocks[j] = w;
-            if (s.bad && pass == 0 && blockIdx.x == 0) atomicOr(P.status, kPagedBadIndex);
-          }
+        for (int i = 0; i < nt; ++i) {
+          int t0, t1;
+          tile_blocks<R, BK>(P, s, i, t0, t1);
+          w += tile_places<BK>(P, t0, t1);
         }
-        __syncthreads();
       }
-      // Inclusive sums over the chunk's sequences (all heads).
-      long long w = 0, v = 0;
-      if (tid < kPlanSeqs) {
-        w = tid < n ? sm.blocks[tid] * P.c.heads : 0;
-        v = w;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const long long u = __shfl_up_sync(0xFFFFFFFFu, v, d);
-          if (lane >= d) v += u;
+    } else {
+#pragma unroll 1
+      for (int j = tid / 32; j < n; j += kThreads / 32) {
+        const Seq s = load_seq(P, b0 + j);
+        if (s.bad && first && blockIdx.x == 0 && lane == 0) atomicOr(P.status, kPagedBadIndex);
+        const int nt = tiles_of<R>(P, s);
+        int x = 0;
+#pragma unroll 1
+        for (int i = lane; i < nt; i += 32) {
+          int t0, t1;
+          tile_blocks<R, BK>(P, s, i, t0, t1);
+          x += tile_places<BK>(P, t0, t1);
         }
-        if (lane == 31) sm.sums[tid >> 5] = v;
+        x = __reduce_add_sync(0xFFFFFFFFu, x);
+        if (lane == 0) sm.places[j] = x;
       }
       __syncthreads();
-      if (tid < kPlanSeqs) {
-        for (int k = 0; k < (tid >> 5); ++k) v += sm.sums[k];
-        if (pass == 1) {
-          const long long lo = base + v - w;
-          if (out.at >= lo && out.at < lo + w) {       // one thread of one chunk
-            sm.b = b0 + tid;
-            sm.total = out.at - lo;                    // place within the sequence
-          }
-        }
-        if (pass == 0 && tid == n - 1) sm.total = base + v;
-      }
-      __syncthreads();
-      if (pass == 0) base = sm.total;
-      else if (P.B > kPlanSeqs) {
-        long long all = 0;
-        for (int k = 0; k < n; ++k) all += sm.blocks[k] * P.c.heads;
-        base += all;
-      }
+      if (tid < n) w = sm.places[tid];
+      // the next chunk's sums are written behind cta_scan's barriers
     }
-    if (pass == 0) {
-      const long long total = base;
-      out.share = max(static_cast<long long>(min_share), (total + gridDim.x - 1) / gridDim.x);
-      out.at = out.share * blockIdx.x;
-      out.len = min(out.share, total - out.at);
-      if (out.len <= 0) {
-        out.len = 0;
-        return out;                                    // the whole CTA
-      }
-    }
+    return w * P.c.heads;
+  };
+
+  int total = 0, w = 0, v = 0, all = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < P.B; b0 += N) {
+    w = places(b0, true);
+    v = cta_scan<N>(w, sm, all);
+    total += all;
   }
-  // The tile and head within the sequence, 32 tiles at a time.
-  if (tid < 32) {
-    const Seq s = load_seq(P, sm.b);
-    const int nt = tiles_of<R>(P, s);
-    long long rem = sm.total;
-    for (int i0 = 0; i0 < nt; i0 += 32) {
-      int len = 0;
-      if (i0 + lane < nt) {
-        int k0, k1;
-        tile_blocks<R, BK>(P, s, i0 + lane, k0, k1);
-        len = k1 - k0 + kTileCost<BK>;
-      }
-      const long long w = static_cast<long long>(len) * P.c.heads;
-      long long v = w;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long u = __shfl_up_sync(0xFFFFFFFFu, v, d);
-        if (lane >= d) v += u;
-      }
-      const unsigned past = __ballot_sync(0xFFFFFFFFu, v > rem);
-      if (past) {
-        if (lane == __ffs(past) - 1) {
-          const long long r = rem - (v - w);
-          sm.i = i0 + lane;
-          sm.h = static_cast<int>(r / len);
-          sm.off = static_cast<int>(r - static_cast<long long>(sm.h) * len);
-        }
-        break;
-      }
-      rem -= __shfl_sync(0xFFFFFFFFu, v, 31);
+  const int share = max(min_share, static_cast<int>((static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x));
+  const long long at = static_cast<long long>(share) * blockIdx.x;
+  if (at >= total) {
+    Share none{};
+    return none;                                       // the whole CTA
+  }
+  // The sequence that the share starts in: a batch of one chunk has its sums at
+  // hand, a longer one adds them up again.
+  auto found = [&](const Seq& s, int b, int i, int rem, int t0, int t1) {
+    const int n = tile_places<BK>(P, t0, t1), h = static_cast<unsigned>(rem) / static_cast<unsigned>(n);
+    sm.found = Share{s, b, h, i, rem - h * n, t0, t1, min(share, total - static_cast<int>(at)), static_cast<int>(at), share};
+  };
+  int base = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < P.B; b0 += N) {
+    if (P.B > N) {
+      w = places(b0, false);
+      v = cta_scan<N>(w, sm, all);
     }
+    const int rem = static_cast<int>(at) - (base + v - w);
+    if (tid < N && rem >= 0 && rem < w) {              // one thread of one chunk
+      const Seq s = load_seq(P, b0 + tid);
+      sm.found.b = b0 + tid;
+      sm.rem = -1;
+      if (tiles_of<R>(P, s) == 1) {
+        int t0, t1;
+        tile_blocks<R, BK>(P, s, 0, t0, t1);
+        found(s, b0 + tid, 0, rem, t0, t1);
+      } else {
+        sm.rem = rem;
+      }
+    }
+    base += all;
   }
   __syncthreads();
-  out.b = sm.b;
-  out.h = sm.h;
-  out.i = sm.i;
-  out.off = sm.off;
-  return out;
+  if (sm.rem >= 0) {
+    // A sequence of several tiles: 32 tiles at a time.
+    const int b = sm.found.b;
+    int rem = sm.rem;
+    __syncthreads();
+    if (tid < 32) {
+      const Seq s = load_seq(P, b);
+      const int nt = tiles_of<R>(P, s);
+#pragma unroll 1
+      for (int i0 = 0; i0 < nt; i0 += 32) {
+        int t0 = 0, t1 = 0, x = 0;
+        if (i0 + lane < nt) {
+          tile_blocks<R, BK>(P, s, i0 + lane, t0, t1);
+          x = tile_places<BK>(P, t0, t1) * P.c.heads;
+        }
+        int y = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int u = __shfl_up_sync(0xFFFFFFFFu, y, d);
+          if (lane >= d) y += u;
+        }
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, y > rem);
+        if (past) {
+          if (lane == __ffs(past) - 1) found(s, b, i0 + lane, rem - (y - x), t0, t1);
+          break;
+        }
+        rem -= __shfl_sync(0xFFFFFFFFu, y, 31);
+      }
+    }
+    __syncthreads();
+  }
+  return sm.found;
 }
 
 // The parts of tiles in a share, one after another: heads fastest, so that
 // what depends on the sequence and the tile alone is computed once for all
-// heads.  Every role of a CTA walks its own.
+// heads.
 template <int R, int BK>
 struct Walk {
   Seq s;
@@ -212,12 +243,12 @@ struct Walk {
   bool whole;        // the tile lies in this share alone
   int slot;          // else: which of the CTA's two partial results
   int nt;
-  long long len;     // places left
+  int len;           // places left
 
-  __device__ __forceinline__ void part(int off) {
-    const int places = t1 - t0 + kTileCost<BK>;
-    k0 = min(t0 + off, t1);
-    k1 = static_cast<int>(min(static_cast<long long>(t1), t0 + off + len));
+  __device__ __forceinline__ void part(const PagedParams& P, int off) {
+    const int places = tile_places<BK>(P, t0, t1);
+    k0 = min(t0 + (off << P.unit), t1);
+    k1 = off + len < places ? min(t0 + (off + len << P.unit), t1) : t1;
     whole = k0 == t0 && k1 == t1;
     slot = off > 0 ? 0 : 1;
     len -= places - off;
@@ -229,10 +260,11 @@ struct Walk {
     i = sh.i;
     h = sh.h;
     len = sh.len;
-    s = load_seq(P, b);
+    s = sh.s;
     nt = tiles_of<R>(P, s);
-    tile_blocks<R, BK>(P, s, i, t0, t1);
-    part(sh.off);
+    t0 = sh.t0;
+    t1 = sh.t1;
+    part(P, sh.off);
     if (k0 >= k1 && !step(P)) return false;
     fresh = true;
     return true;
@@ -254,7 +286,7 @@ struct Walk {
       }
       tile_blocks<R, BK>(P, s, i, t0, t1);
     }
-    part(0);
+    part(P, 0);
     return true;                                       // at least one block: places begin with them
   }
 };
@@ -263,13 +295,17 @@ struct Walk {
 // its share starts within, unless an earlier CTA's does too.
 template <int R, int BK>
 __device__ __forceinline__ void write_cut(const PagedParams& P, const Share& sh, const PagedWork& w) {
-  CutTile c{0, 0, 0, 0, -1};
-  if (sh.len > 0 && sh.off > 0) {
-    int k0, k1;
-    tile_blocks<R, BK>(P, load_seq(P, sh.b), sh.i, k0, k1);
-    const long long a = sh.at - sh.off;
-    const int c0 = static_cast<int>(a / sh.share), c1 = static_cast<int>((a + (k1 - k0) - 1) / sh.share);
-    if (sh.off < k1 - k0 && c0 + 1 == static_cast<int>(blockIdx.x)) c = CutTile{sh.b, sh.h, sh.i, c0, c1};
+  CutTile c{0, -1, 0, 0, 0, 0};
+  if (sh.len > 0 && sh.off > 0 && (sh.off << P.unit) < sh.t1 - sh.t0) {
+    const unsigned a = sh.at - sh.off, last = (sh.t1 - sh.t0 - 1) >> P.unit;     // place of the tile's last block
+    c.c0 = a / static_cast<unsigned>(sh.share);
+    if (c.c0 + 1 == static_cast<int>(blockIdx.x)) {
+      c.c1 = (a + last) / static_cast<unsigned>(sh.share);
+      c.q0 = sh.s.q0;
+      c.p0 = sh.i * R;
+      c.rows = min(R, sh.s.ql * P.group - c.p0);
+      c.h = sh.h;
+    }
   }
   w.cut[blockIdx.x] = c;
 }
@@ -289,9 +325,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   grid_dependency_wait();
   const CutTile c = w.cut[blockIdx.x];
   if (c.c1 < 0) return;
-  const Seq s = load_seq(P, c.b);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kWarps;
-  const int rows = min(R, s.ql * P.group - c.i * R);
+  const int rows = c.rows;
   for (int r0 = blockIdx.y * kRows; r0 < rows; r0 += gridDim.y * kRows) {
     const int r = r0 + warp / kWarps;
     const bool here = r < rows;
@@ -335,7 +370,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     }
     if (here && sub == 0) {
       const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-      const int p = c.i * R + r, t = s.q0 + p / P.group, hq = c.h * P.group + p % P.group;
+      const int p = c.p0 + r, tok = p / P.by_group, t = c.q0 + tok, hq = c.h * P.group + p - tok * P.group;
       reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o.ptr) + t * P.o.st + hq * P.o.sh)[lane] =
           make_uint2(pack2<false>(acc.x * inv, acc.y * inv), pack2<false>(acc.z * inv, acc.w * inv));
       if (P.lse && lane == 0)

@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in ("ovc.cu", "paged.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("ptx.cuh", "prepare.cuh", "attention.cuh", "repair.cuh", "group.cuh",
                                            "host_stream.cuh", "host.cuh", "paged.cuh", "paged_plan.cuh",
-                                           "paged_decode.cuh")]
+                                           "paged_decode.cuh", "paged_chunk.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libovc.so")

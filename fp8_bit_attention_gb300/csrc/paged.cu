@@ -12,6 +12,7 @@
 #include "ovc.h"
 #include "host.cuh"
 #include "paged.cuh"
+#include "paged_chunk.cuh"
 #include "paged_decode.cuh"
 
 namespace ovc {
@@ -83,9 +84,12 @@ bool make_cache_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int common_divisor(int a, int b) { return b ? common_divisor(b, a % b) : a; }
+
 constexpr uint64_t kTimeoutNs = 4000000000ull;    // 4 s per wait
 constexpr int kMaxSms = 160;                      // that a persistent grid uses
-constexpr int kDecodeMinShare = 16;               // blocks
+constexpr int kDecodeMinShare = 16;               // blocks of 16 keys
+constexpr int kChunkMinShare = 4;                 // blocks of 128 keys
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -94,11 +98,11 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int tile_rows(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b) {
   const int64_t group = q->H / c->heads;
   const int64_t most = (b->cu_q ? (b->max_q > 0 ? b->max_q : q->T) : 1) * group;
-  return most <= 8 ? 8 : most <= 16 ? 16 : 32;
+  return most <= 8 ? 8 : most <= 16 ? 16 : kChRows;
 }
 
 // CTAs per SM of the kernel with tiles of R rows.
-int ctas_per_sm(int R) { return R == 8 ? kDecodeCtas<1> : R == 16 ? kDecodeCtas<2> : kDecodeCtas<4>; }
+int ctas_per_sm(int R) { return R == 8 ? kDecodeCtas<1> : R == 16 ? kDecodeCtas<2> : 1; }
 
 size_t work_bytes(int R, PagedWork* w, void* base) {
   uint8_t* p = static_cast<uint8_t*>(base);
@@ -114,20 +118,26 @@ size_t work_bytes(int R, PagedWork* w, void* base) {
 
 // The unit of paged_plan.cuh's line: the least with which all tiles' places are
 // sure to fit 31 bits, whatever the lengths.
-int line_unit(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b, int R, int BK, int cost) {
+int line_unit(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b, int R, int BK) {
   const double tiles = (static_cast<double>(q->T) * (q->H / c->heads) / R + b->B) * c->heads;
-  const double blocks = static_cast<double>(b->table_width) * c->page / BK + cost + 1;
+  const double blocks = static_cast<double>(b->table_width) * c->page / BK + kTileCost<kDecKeys> + 1;
   int unit = 0;
   while (tiles * (std::ldexp(blocks, -unit) + 1) > 2.0e9 && unit < 27) ++unit;
   return unit;
 }
 
-using DecodeFn = decltype(&paged_decode_kernel<false, 1>);
+using PagedFn = decltype(&paged_decode_kernel<false, 1>);
 
-DecodeFn decode_fn(bool half, int R) {
-  if (R == 8) return half ? paged_decode_kernel<true, 1> : paged_decode_kernel<false, 1>;
-  if (R == 16) return half ? paged_decode_kernel<true, 2> : paged_decode_kernel<false, 2>;
-  return half ? paged_decode_kernel<true, 4> : paged_decode_kernel<false, 4>;
+struct PagedKernel {
+  PagedFn fn;
+  int threads, smem;
+};
+
+PagedKernel kernel_for(bool half, int R) {
+  if (R == 8) return {half ? paged_decode_kernel<true, 1> : paged_decode_kernel<false, 1>, kDecThreads, sizeof(DecodeSmem)};
+  if (R == 16) return {half ? paged_decode_kernel<true, 2> : paged_decode_kernel<false, 2>, kDecThreads, sizeof(DecodeSmem)};
+  if (half) return {paged_chunk_kernel<true>, kChThreads, sizeof(ChunkSmem<true>)};
+  return {paged_chunk_kernel<false>, kChThreads, sizeof(ChunkSmem<false>)};
 }
 
 std::mutex g_paged_mu;
@@ -137,22 +147,23 @@ bool g_paged_init[64];
 ovc_status paged_init(int device) {
   std::lock_guard<std::mutex> lock(g_paged_mu);
   if (g_paged_init[device]) return OVC_OK;
-  for (int R = 8; R <= 32; R *= 2)
-    for (int half = 0; half < 2; ++half)
-      if (cudaFuncSetAttribute(decode_fn(half, R), cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(DecodeSmem)) != cudaSuccess)
-        return OVC_ERR_CUDA;
+  for (const int R : {8, 16, kChRows})
+    for (int half = 0; half < 2; ++half) {
+      const PagedKernel k = kernel_for(half, R);
+      if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) return OVC_ERR_CUDA;
+    }
   g_paged_init[device] = true;
   return OVC_OK;
 }
 
 // The join, launched while the attention kernel before it still runs.
 template <int R, int kWarps>
-cudaError_t launch_join(const PagedParams& P, const PagedWork& w, int ctas, cudaStream_t s) {
+cudaError_t launch_join(const PagedParams& P, const PagedWork& w, int ctas, int groups, cudaStream_t s) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, R / (kJoinThreads / 32 / kWarps));
+  cfg.gridDim = dim3(ctas, groups);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cfg.attrs = &attr;
@@ -235,22 +246,25 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
   P.status = dev->status;
   PagedMaps M{};
   M.rows = static_cast<int32_t>(c->pages * c->heads * c->page);
-  M.min_share = kDecodeMinShare;
+  const int R = tile_rows(q, c, b), BK = R == kChRows ? kChKeys : kDecKeys;
+  M.box = common_divisor(static_cast<int>(c->page), BK);
+  M.min_share = R == kChRows ? kChunkMinShare : kDecodeMinShare;
   M.timeout_ns = kTimeoutNs;
-  if (!make_cache_map(&M.k, c->k, M.rows, kDecKeys) || !make_cache_map(&M.v, c->v, M.rows, kDecKeys)) return OVC_ERR_CUDA;
+  if (!make_cache_map(&M.k, c->k, M.rows, M.box) || !make_cache_map(&M.v, c->v, M.rows, M.box)) return OVC_ERR_CUDA;
   st = paged_init(dev->index);
   if (st != OVC_OK) return st;
-  const int R = tile_rows(q, c, b);
-  P.unit = line_unit(q, c, b, R, kDecKeys, kTileCost<kDecKeys>);
+  P.unit = line_unit(q, c, b, R, BK);
   PagedWork w;
   work_bytes(R, &w, workspace);
   const int ctas = (dev->sms < kMaxSms ? dev->sms : kMaxSms) * ctas_per_sm(R);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  decode_fn(q->dtype == OVC_FP16, R)<<<ctas, kDecThreads, sizeof(DecodeSmem), s>>>(P, M, w);
+  const PagedKernel k = kernel_for(q->dtype == OVC_FP16, R);
+  k.fn<<<ctas, k.threads, k.smem, s>>>(P, M, w);
   st = launched();
   if (st != OVC_OK) return st;
-  const cudaError_t err = R == 8 ? launch_join<8, 4>(P, w, ctas, s) : R == 16 ? launch_join<16, 4>(P, w, ctas, s)
-                                                                            : launch_join<32, 4>(P, w, ctas, s);
+  const cudaError_t err = R == 8    ? launch_join<8, 4>(P, w, ctas, 4, s)
+                          : R == 16 ? launch_join<16, 4>(P, w, ctas, 8, s)
+                                    : launch_join<kChRows, 1>(P, w, ctas, 8, s);
   if (err != cudaSuccess) return OVC_ERR_CUDA;
   return launched();
 }

@@ -1,0 +1,793 @@
+// paged_chunk.cuh -- attention over the paged cache for many query rows per KV
+// head: chunks of new tokens, on the tensor cores (tcgen05).
+//
+// A tile is 256 query rows (tokens times query heads of one KV head) in two
+// halves of 128, a step is one half's products with one block of 128 keys:
+//   S_t = Q_t K^T          kind::f8f6f4.  K's codes go in as they lie in the
+//                          cache (TMA tiles, K-major); Q enters as a sum of
+//                          E4M3 parts, each the rounding error of the ones
+//                          before it: two parts hold a BF16 row (8 bits), three
+//                          an FP16 row (11 bits), but for what lies below 2^-18
+//                          of the row's largest element.  Two 8-bit products
+//                          cost what one 16-bit product costs, and K needs no
+//                          conversion.
+//   O_t += P_t V           kind::f16.  P is FP16 and read from tensor memory,
+//                          where it overwrites S_t; V's codes are converted to
+//                          FP16 (exactly) by four warps, once per block for all
+//                          256 rows, with the token's scale: V 2^(e - E + 7), E
+//                          the largest scale so far.
+// While one half's softmax runs, the tensor core works on the other half.  A tile
+// of at most 128 rows keeps that overlap by giving the blocks to the halves in
+// turn, both on the same rows, and joining the two results at the end ("solo").
+//
+// Warps: 0-3 and 4-7 softmax of the halves, a thread per row; 8-11 convert V; 12
+// walks the share, looks up pages and loads K and V; 13 issues the products; 14
+// loads the scales; 15 idles.  All waits are bounded.
+//
+// Numbers: scores, maxima, sums and outputs are FP32.  Weights are 2^8 p relative
+// to a reference that follows the row's maximum only when that passes it by
+// 2^7 (then O is rescaled in tensor memory), so they lie below FP16's largest
+// value and are flushed below 2^-32.  V's values are flushed below 2^-31 of the
+// largest token's.
+#pragma once
+
+#include "paged_decode.cuh"
+
+namespace ovc {
+
+constexpr int kChRows = 256;
+constexpr int kChKeys = 128;
+constexpr int kChThreads = 512;
+// Registers: 512 threads of 128 at launch; 256 x 184 + 256 x 72 = 512 x 128.
+constexpr int kChSoftmaxRegs = 184;
+constexpr int kChOtherRegs = 72;
+static_assert(256 * kChSoftmaxRegs + 256 * kChOtherRegs <= kChThreads * 128, "register split");
+constexpr uint32_t kChTile = 128 * 128;            // bytes of an E4M3 tile
+constexpr uint32_t kChTile16 = 2 * kChTile;        // bytes of V in FP16
+constexpr float kChPBias = 8.0f;                   // log2 of the weight at the reference
+constexpr float kChLazy = 7.0f;                    // how far a maximum may pass the reference
+constexpr int kChVBias = 7;
+constexpr int kChParts = 4;
+
+template <bool kHalf>
+struct ChunkShape {
+  static constexpr int kQParts = kHalf ? 3 : 2;
+  static constexpr int kK = kHalf ? 2 : 3;         // stages of K
+  static constexpr int kV = kHalf ? 1 : 2;         // stages of V's codes
+  static constexpr int kScales = 2;
+};
+
+// A block's scales: those of K as values, those of V as FP16 pairs 2^(e-E+7).
+struct alignas(16) ChunkScales {
+  float k[kChKeys];
+  uint32_t v[kChKeys];
+  uint8_t nan[32];                                 // bit j of byte i: V's scale of key 4 i + j is NaN
+  int e;                                           // E
+  int poison;                                      // any such bit
+};
+
+// A tile's part.
+struct ChunkPart {
+  int more;
+  int b, q0, ql, kv;
+  int p0, rows, h;
+  int k0, nblk;
+  int all_lo, all_hi;
+  int slot;                                        // negative: the tile is whole
+};
+
+template <bool kHalf>
+struct ChunkSmem {
+  using Sh = ChunkShape<kHalf>;
+  uint8_t q[Sh::kQParts][2][kChTile];
+  uint8_t k[Sh::kK][kChTile];
+  uint8_t v8[Sh::kV][kChTile];
+  uint8_t v16[2][kChTile16];                       // [64-channel half][key][128 bytes]
+  union {
+    ChunkScales sc[Sh::kScales];
+    PlanSmem plan;
+  };
+  float2 ml[128];                                  // solo: the second half's reference and sum
+  int e1;                                          // and its E
+  ChunkPart part[kChParts];
+  uint64_t k_full[Sh::kK], k_empty[Sh::kK];
+  uint64_t v8_full[Sh::kV], v8_empty[Sh::kV];
+  uint64_t v16_full[2], v16_empty[2];
+  uint64_t sc_full[Sh::kScales], sc_empty[Sh::kScales];
+  uint64_t s_full[2], p_full[2], o_full[2], q_full, x_full, x_empty;
+  uint64_t part_full[kChParts], part_empty[kChParts];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int zero;
+};
+static_assert(sizeof(ChunkSmem<false>) <= 232448 && sizeof(ChunkSmem<true>) <= 232448, "shared memory per CTA");
+
+// Descriptor of V in FP16: MN-major (channels contiguous), 128-byte swizzle;
+// 64-channel halves 16 KB apart, groups of 8 keys 1024 bytes apart.
+__device__ __forceinline__ uint64_t v16_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kChTile >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// kind::f16 with FP16 operands, FP32 result, A K-major, B MN-major (bit 16).
+constexpr uint32_t kChIdescPV = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kChIdescQK = idesc_e4m3_f32(128, 128);
+
+// D[tmem] (+)= A[tmem] B[smem], 16-bit operands, by a converged warp.
+__device__ __forceinline__ void mma_16_ts_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// 2^x as an FP16 pair, x <= 15.
+__device__ __forceinline__ uint32_t exp2h2(int x) {
+  const uint32_t h = x >= -14 ? static_cast<uint32_t>(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
+  return h | (h << 16);
+}
+
+// E4M3 pair -> the values as floats.
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t pair) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(h) : "r"(pair));
+  return unpack2<true>(h);
+}
+
+template <bool kHalf>
+__global__ void __launch_bounds__(kChThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ PagedParams P, const __grid_constant__ PagedMaps M, PagedWork work) {
+  using Sh = ChunkShape<kHalf>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  ChunkSmem<kHalf>& sm = *reinterpret_cast<ChunkSmem<kHalf>*>(raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* const abort_flag = &sm.abort;
+  constexpr int kReaders = 4 + 1 + 1 + 8;          // warps that read a part's description: V, products, scales, softmax
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    sm.zero = 0;
+    for (int i = 0; i < Sh::kK; ++i) {
+      mbar_init(smem_addr(&sm.k_full[i]), 1);
+      mbar_init(smem_addr(&sm.k_empty[i]), 1);
+    }
+    for (int i = 0; i < Sh::kV; ++i) {
+      mbar_init(smem_addr(&sm.v8_full[i]), 1);
+      mbar_init(smem_addr(&sm.v8_empty[i]), 4);
+    }
+    for (int i = 0; i < Sh::kScales; ++i) {
+      mbar_init(smem_addr(&sm.sc_full[i]), 1);
+      mbar_init(smem_addr(&sm.sc_empty[i]), 12);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sm.v16_full[i]), 128);
+      mbar_init(smem_addr(&sm.v16_empty[i]), 1);
+      mbar_init(smem_addr(&sm.s_full[i]), 1);
+      mbar_init(smem_addr(&sm.p_full[i]), 128);
+      mbar_init(smem_addr(&sm.o_full[i]), 1);
+    }
+    for (int i = 0; i < kChParts; ++i) {
+      mbar_init(smem_addr(&sm.part_full[i]), 1);
+      mbar_init(smem_addr(&sm.part_empty[i]), kReaders);
+    }
+    mbar_init(smem_addr(&sm.q_full), 256);
+    mbar_init(smem_addr(&sm.x_full), 128);
+    mbar_init(smem_addr(&sm.x_empty), 128);
+    mbar_init(smem_addr(&sm.drain), 1);
+    fence_mbar_init();
+    tma_prefetch_map(&M.k);
+    tma_prefetch_map(&M.v);
+  }
+  grid_dependency_allow();
+  __syncthreads();
+  const Share share = plan_share<kChRows, kChKeys, kChThreads, 32>(P, sm.plan, M.min_share);
+  if (share.len == 0) {
+    if (threadIdx.x == 0) write_cut<kChRows, kChKeys>(P, share, work);
+    return;
+  }
+  if (warp == 13) {
+    tmem_alloc(smem_addr(&sm.tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();                                 // also: the plan's memory is free
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return mbar_wait(smem_addr(&bar), parity, M.timeout_ns, abort_flag); };
+  auto give_up = [&]() {
+    if (!*abort_flag) atomicOr(P.status, 1u);
+    *abort_flag = 1;
+  };
+
+  if (warp >= 8) {
+    regs_dec<kChOtherRegs>();
+    if (warp == 12) {
+      // -------------------------------------------------- the share, K and V
+      Walk<kChRows, kChKeys> w;
+      uint32_t parts = 0, n = 0, nv = 0;           // blocks whose K, V were loaded
+      bool ok = true;
+      const int boxes = kChKeys / M.box;
+      for (bool more = w.start(P, share);; more = w.step(P)) {
+        const uint32_t d = parts % kChParts;
+        if (parts >= kChParts) ok = __all_sync(0xFFFFFFFFu, wait(sm.part_empty[d], (parts / kChParts - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) {
+          ChunkPart& x = sm.part[d];
+          x.more = more;
+          if (more) {
+            int y;
+            x.b = w.b;
+            x.q0 = w.s.q0;
+            x.ql = w.s.ql;
+            x.kv = w.s.kv;
+            x.p0 = w.i * kChRows;
+            x.rows = min(kChRows, w.s.ql * P.group - x.p0);
+            x.h = w.h;
+            x.k0 = w.k0;
+            x.nblk = w.k1 - w.k0;
+            x.slot = w.whole ? -1 : w.slot;
+            row_range(P, w.s, (x.p0 + x.rows - 1) / P.by_group, x.all_lo, y);
+            row_range(P, w.s, x.p0 / P.by_group, y, x.all_hi);
+          }
+          mbar_arrive(smem_addr(&sm.part_full[d]));
+        }
+        ++parts;
+        if (!more) break;
+        auto lookup = [&](int kb) {
+          const int key = kb * kChKeys + lane * M.box;
+          int row = M.rows;                        // past the cache's end: reads zeros
+          if (lane < boxes && kb < w.k1 && key < w.s.kv) {
+            const int i = key / P.by_page;
+            const int p = __ldg(P.table + w.b * P.table_stride + i);
+            if (p >= 0 && p < P.c.pages) row = (p * P.c.heads + w.h) * P.c.page + key - i * P.c.page;
+            else atomicOr(P.status, kPagedBadIndex);
+          }
+          return row;
+        };
+        int row = lookup(w.k0);
+        for (int kb = w.k0; kb < w.k1; ++kb) {
+          const int next = lookup(kb + 1);
+          const uint32_t ks = n % Sh::kK, vs = nv % Sh::kV;
+          if (n >= Sh::kK) ok = __all_sync(0xFFFFFFFFu, wait(sm.k_empty[ks], (n / Sh::kK - 1) & 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sm.k_full[ks]), kChTile);
+          __syncwarp();
+          if (lane < boxes) tma_load_2d(smem_addr(sm.k[ks]) + lane * M.box * 128, &M.k, smem_addr(&sm.k_full[ks]), 0, row);
+          ++n;
+          if (nv >= Sh::kV) ok = __all_sync(0xFFFFFFFFu, wait(sm.v8_empty[vs], (nv / Sh::kV - 1) & 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sm.v8_full[vs]), kChTile);
+          __syncwarp();
+          if (lane < boxes) tma_load_2d(smem_addr(sm.v8[vs]) + lane * M.box * 128, &M.v, smem_addr(&sm.v8_full[vs]), 0, row);
+          ++nv;
+          row = next;
+        }
+        if (!ok) break;
+      }
+      if (lane == 0) write_cut<kChRows, kChKeys>(P, share, work);
+      if (!ok) {
+        give_up();
+        // The copies in flight end by themselves; shared memory must outlive them.
+        for (uint32_t i = n > Sh::kK ? n - Sh::kK : 0; i < n; ++i)
+          mbar_wait(smem_addr(&sm.k_full[i % Sh::kK]), (i / Sh::kK) & 1, 4000000000ull, &sm.zero);
+        for (uint32_t i = nv > Sh::kV ? nv - Sh::kV : 0; i < nv; ++i)
+          mbar_wait(smem_addr(&sm.v8_full[i % Sh::kV]), (i / Sh::kV) & 1, 4000000000ull, &sm.zero);
+      }
+    } else if (warp == 13) {
+      // --------------------------------------------------------- the products
+      uint32_t parts = 0, n = 0, steps[2] = {0, 0};
+      bool ok = true, issued = false;
+      const uint64_t qd = sw128_desc(smem_addr(sm.q[0][0]));
+      while (true) {
+        const uint32_t d = parts % kChParts;
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.part_full[d], (parts / kChParts) & 1));
+        if (!ok || !sm.part[d].more) break;
+        const int nblk = sm.part[d].nblk;
+        const bool solo = sm.part[d].rows <= 128;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[d]));
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.q_full, parts & 1));
+        if (!ok) break;
+        ++parts;
+        tc_fence_after();
+        const int total = solo ? nblk : 2 * nblk;
+        auto scores = [&](int i) {
+          const int t = i & 1;
+          const uint32_t blk = n + (solo ? i : i >> 1), ks = blk % Sh::kK;
+          ok = __all_sync(0xFFFFFFFFu, wait(sm.k_full[ks], (blk / Sh::kK) & 1));
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t kd = sw128_desc(smem_addr(sm.k[ks]));
+#pragma unroll
+          for (int part = 0; part < Sh::kQParts; ++part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f8_ss_w(tmem + t * 128, qd + (part * 2 + (solo ? 0 : t)) * (kChTile >> 4) + 2 * kk, kd + 2 * kk, kChIdescQK,
+                          part > 0 || kk > 0);
+          tc_commit_w(smem_addr(&sm.s_full[t]));
+          if (solo || t == 1) tc_commit_w(smem_addr(&sm.k_empty[ks]));
+          issued = true;
+        };
+        scores(0);
+        if (ok && total > 1) scores(1);
+        for (int i = 0; i < total && ok; ++i) {
+          const int t = i & 1;
+          const uint32_t blk = n + (solo ? i : i >> 1), vs = blk & 1;
+          ok = __all_sync(0xFFFFFFFFu, wait(sm.v16_full[vs], (blk >> 1) & 1) && wait(sm.p_full[t], steps[t] & 1));
+          if (!ok) break;
+          ++steps[t];
+          tc_fence_after();
+          const uint64_t vd = v16_desc(smem_addr(sm.v16[vs]));
+          const bool first = i < 2;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_16_ts_w(tmem + 256 + t * 128, tmem + t * 128 + 8 * kk, vd + kk * (2048 >> 4), kChIdescPV, !first || kk > 0);
+          if (solo || t == 1) tc_commit_w(smem_addr(&sm.v16_empty[vs]));
+          if (i + 2 < total) scores(i + 2);
+          else tc_commit_w(smem_addr(&sm.o_full[t]));
+        }
+        if (!ok) break;
+        n += nblk;
+      }
+      if (!ok) give_up();
+      if (issued) {
+        // Every product issued so far has completed once this barrier flips.
+        tc_commit_w(smem_addr(&sm.drain));
+        mbar_wait(smem_addr(&sm.drain), 0, 4000000000ull, &sm.zero);
+      }
+    } else if (warp == 14) {
+      // ----------------------------------------------------------- the scales
+      uint32_t parts = 0, n = 0;
+      bool ok = true;
+      while (true) {
+        const uint32_t d = parts % kChParts;
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.part_full[d], (parts / kChParts) & 1));
+        if (!ok || !sm.part[d].more) break;
+        const ChunkPart x = sm.part[d];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[d]));
+        ++parts;
+        // Lane i takes keys 4 i .. 4 i + 3 (one page holds them).
+        auto load = [&](int i, uint32_t& kw, uint32_t& vw) {
+          const int key = (x.k0 + i) * kChKeys + 4 * lane;
+          kw = vw = 0;
+          if (i < x.nblk && key < x.kv) {
+            const int j = key / P.by_page;
+            const int p = __ldg(P.table + x.b * P.table_stride + j);
+            if (p >= 0 && p < P.c.pages) {
+              const int64_t row = static_cast<int64_t>((p * P.c.heads + x.h) * P.c.page + key - j * P.c.page);
+              kw = *reinterpret_cast<const uint32_t*>(P.c.ks + row);
+              vw = *reinterpret_cast<const uint32_t*>(P.c.vs + row);
+            }
+          }
+        };
+        uint32_t kw, vw;
+        load(0, kw, vw);
+        int E = 0;
+        for (int i = 0; i < x.nblk; ++i, ++n) {
+          uint32_t kn, vn;
+          load(i + 1, kn, vn);
+          const uint32_t s = n % Sh::kScales;
+          const int left = x.kv - ((x.k0 + i) * kChKeys + 4 * lane);
+          int e = 0;
+          uint32_t nan = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t ev = (vw >> (8 * j)) & 255u;
+            if (j < left) {
+              if (ev == 255u) nan |= 1u << j;
+              else e = max(e, static_cast<int>(ev));
+            }
+          }
+          E = max(E, __reduce_max_sync(0xFFFFFFFFu, e));
+          if (n >= Sh::kScales) ok = __all_sync(0xFFFFFFFFu, wait(sm.sc_empty[s], (n / Sh::kScales - 1) & 1));
+          if (!ok) break;
+          ChunkScales& sc = sm.sc[s];
+          float4 f;
+          uint4 h;
+          f.x = scale_value(kw & 255u);
+          f.y = scale_value((kw >> 8) & 255u);
+          f.z = scale_value((kw >> 16) & 255u);
+          f.w = scale_value(kw >> 24);
+          auto vscale = [&](uint32_t ev) { return ev == 255u ? 0u : exp2h2(min(static_cast<int>(ev) - E, 0) + kChVBias); };
+          h.x = vscale(vw & 255u);
+          h.y = vscale((vw >> 8) & 255u);
+          h.z = vscale((vw >> 16) & 255u);
+          h.w = vscale(vw >> 24);
+          reinterpret_cast<float4*>(sc.k)[lane] = f;
+          reinterpret_cast<uint4*>(sc.v)[lane] = h;
+          sc.nan[lane] = static_cast<uint8_t>(nan);
+          const bool any = __any_sync(0xFFFFFFFFu, nan != 0);
+          if (lane == 0) {
+            sc.e = E;
+            sc.poison = any;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[s]));
+          kw = kn;
+          vw = vn;
+        }
+        if (!ok) break;
+      }
+      if (!ok) give_up();
+    } else if (warp < 12) {
+      // ------------------------------------------------- V's codes to FP16
+      const int w = warp - 8;
+      uint32_t parts = 0, n = 0;
+      bool ok = true;
+      while (true) {
+        const uint32_t d = parts % kChParts;
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.part_full[d], (parts / kChParts) & 1));
+        if (!ok || !sm.part[d].more) break;
+        const int nblk = sm.part[d].nblk, k0 = sm.part[d].k0, kv = sm.part[d].kv;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[d]));
+        ++parts;
+        for (int i = 0; i < nblk; ++i, ++n) {
+          const uint32_t vs = n % Sh::kV, ss = n % Sh::kScales, os = n & 1;
+          ok = wait(sm.v8_full[vs], (n / Sh::kV) & 1) && wait(sm.sc_full[ss], (n / Sh::kScales) & 1);
+          if (ok && n >= 2) ok = wait(sm.v16_empty[os], ((n >> 1) - 1) & 1);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          // Eight lanes take a key's 128 channels, 16 each: 16 bytes in, 2 x 16
+          // out.  Lanes of the upper 64 channels write their second 16 bytes
+          // first, so that the eight lanes of a store meet different banks.
+          const int c = lane & 7, half = c >> 2;
+          const int left = kv - (k0 + i) * kChKeys;
+          const uint8_t* src = sm.v8[vs];
+          uint8_t* dst = sm.v16[os] + half * kChTile;
+#pragma unroll 4
+          for (int j = 0; j < 8; ++j) {
+            const int r = 32 * w + 4 * j + (lane >> 3);
+            uint4 x = lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
+            if (r >= left) x = make_uint4(0u, 0u, 0u, 0u);     // behind the sequence's end: anything
+            const uint32_t f = sm.sc[ss].v[r];
+            uint4 a, b;
+            cvt_e4m3x4_to_f16x2x2(x.x, a.x, a.y);
+            cvt_e4m3x4_to_f16x2x2(x.y, a.z, a.w);
+            cvt_e4m3x4_to_f16x2x2(x.z, b.x, b.y);
+            cvt_e4m3x4_to_f16x2x2(x.w, b.z, b.w);
+            a = make_uint4(hmul2(a.x, f), hmul2(a.y, f), hmul2(a.z, f), hmul2(a.w, f));
+            b = make_uint4(hmul2(b.x, f), hmul2(b.y, f), hmul2(b.z, f), hmul2(b.w, f));
+            const int c0 = 2 * (c & 3);
+            uint8_t* row = dst + r * 128;
+            *reinterpret_cast<uint4*>(row + (((c0 + half) ^ (r & 7)) << 4)) = half ? b : a;
+            *reinterpret_cast<uint4*>(row + (((c0 + 1 - half) ^ (r & 7)) << 4)) = half ? a : b;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(smem_addr(&sm.v16_full[os]));
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&sm.v8_empty[vs]));
+            mbar_arrive(smem_addr(&sm.sc_empty[ss]));
+          }
+        }
+        if (!ok) break;
+      }
+      if (!ok) give_up();
+    }
+  } else {
+    regs_inc<kChSoftmaxRegs>();
+    // -------------------------------------------------------------- softmax
+    const int t = warp >> 2;                       // the half
+    const int r = threadIdx.x & 127;               // the row in it
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + 256 + t * 128;
+    uint32_t parts = 0, n = 0, steps = 0, ends = 0, solos = 0;
+    bool ok = true;
+    while (true) {
+      const uint32_t d = parts % kChParts;
+      ok = __all_sync(0xFFFFFFFFu, wait(sm.part_full[d], (parts / kChParts) & 1));
+      if (!ok || !sm.part[d].more) break;
+      const ChunkPart x = sm.part[d];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[d]));
+      ++parts;
+      const bool solo = x.rows <= 128;
+      const int row = solo ? r : t * 128 + r;      // of the tile
+      const bool here = row < x.rows;
+      const int p = x.p0 + row, tok = p / P.by_group, hq = x.h * P.group + p - tok * P.group;
+      Seq s;
+      s.q0 = x.q0;
+      s.ql = x.ql;
+      s.kv = x.kv;
+      int lo = 0, hi = -1;
+      if (here) row_range(P, s, tok, lo, hi);
+
+      // Q's row in E4M3 parts, scaled by a power of two to at most 448.
+      float rowf = P.c2;
+      if (!solo || t == 0) {
+        uint4 q[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (here) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q.ptr) + (s.q0 + tok) * P.q.st + hq * P.q.sh);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) q[i] = __ldg(src + i);
+        }
+        float amax = 0.0f;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const float2 a = unpack2<kHalf>(w[i]);
+          amax = fmaxf(amax, fmaxf(a.x == a.x ? fabsf(a.x) : INFINITY, a.y == a.y ? fabsf(a.y) : INFINITY));
+        }
+        const uint32_t e = scale_byte(amax);
+        const float mul = e == 255u ? 0.0f : inverse_scale(e);
+        rowf *= scale_value(e);                    // NaN for a row that is not finite: so are its results
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t out[Sh::kQParts][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 a = unpack2<kHalf>(w[8 * c + 2 * i]), b = unpack2<kHalf>(w[8 * c + 2 * i + 1]);
+            a = make_float2(a.x * mul, a.y * mul);
+            b = make_float2(b.x * mul, b.y * mul);
+#pragma unroll
+            for (int k = 0; k < Sh::kQParts; ++k) {
+              const uint32_t ca = cvt_e4m3x2(a.x, a.y), cb = cvt_e4m3x2(b.x, b.y);
+              out[k][i] = ca | (cb << 16);
+              if (k + 1 < Sh::kQParts) {
+                const float2 va = e4m3x2_values(ca), vb = e4m3x2_values(cb);
+                a = make_float2(a.x - va.x, a.y - va.y);
+                b = make_float2(b.x - vb.x, b.y - vb.y);
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < Sh::kQParts; ++k)
+            *reinterpret_cast<uint4*>(sm.q[k][t] + r * 128 + ((c ^ (r & 7)) << 4)) = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+        }
+        if (solo) sm.ml[r] = make_float2(rowf, 0.0f);
+        fence_proxy_async_smem();
+      }
+      mbar_arrive(smem_addr(&sm.q_full));
+      if (solo && t == 1) {
+        // The rows' factor comes from the first half's threads.
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.q_full, (parts - 1) & 1));
+        if (!ok) break;
+        rowf = sm.ml[r].x;
+      }
+
+      float m = kNegInf, l = 0.0f;
+      int E = 0;
+      bool begun = false;
+      for (int i = 0; i < x.nblk; ++i) {
+        const uint32_t blk = n + i, ss = blk % Sh::kScales;
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.sc_full[ss], (blk / Sh::kScales) & 1));
+        if (!ok) break;
+        if (solo && (i & 1) != t) {                // the other half's block
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[ss]));
+          continue;
+        }
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.s_full[t], steps & 1));
+        if (!ok) break;
+        ++steps;
+        tc_fence_after();
+        const ChunkScales& sc = sm.sc[ss];
+        uint32_t z[128];
+        tmem_ld32(tS, z);
+        tmem_ld32(tS + 32, z + 32);
+        tmem_ld32(tS + 64, z + 64);
+        tmem_ld32(tS + 96, z + 96);
+        tmem_wait_ld32(z);
+        tmem_wait_ld32(z + 32);
+        tmem_wait_ld32(z + 64);
+        tmem_wait_ld32(z + 96);
+        float m0 = kNegInf, m1 = kNegInf;
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+          const float4 k4 = *reinterpret_cast<const float4*>(sc.k + c);
+          const float2 a = unpack_f2(mul_f2(pack_f2(__uint_as_float(z[c]), __uint_as_float(z[c + 1])), pack_f2(k4.x, k4.y)));
+          const float2 b = unpack_f2(mul_f2(pack_f2(__uint_as_float(z[c + 2]), __uint_as_float(z[c + 3])), pack_f2(k4.z, k4.w)));
+          z[c] = __float_as_uint(a.x);
+          z[c + 1] = __float_as_uint(a.y);
+          z[c + 2] = __float_as_uint(b.x);
+          z[c + 3] = __float_as_uint(b.y);
+          m0 = fmax3(m0, a.x, a.y);
+          m1 = fmax3(m1, b.x, b.y);
+        }
+        const int key0 = (x.k0 + i) * kChKeys;
+        if (key0 < x.all_lo || key0 + kChKeys - 1 > x.all_hi) {
+          const int a = lo - key0, b = hi - key0;
+          m0 = m1 = kNegInf;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            if (c < a || c > b) z[c] = 0xFF800000u;
+            m0 = fmaxf(m0, __uint_as_float(z[c]));
+          }
+        }
+        const int Eb = sc.e;
+        const float top = fmaxf(m0, m1) * rowf;
+        const bool need = top > m + kChLazy;
+        if (__any_sync(0xFFFFFFFFu, need) || Eb != E) {
+          const float mn = need ? top : m;
+          float f = m == kNegInf ? 0.0f : ex2(m - mn);
+          m = mn;
+          l *= f;
+          f *= exp2i(E - Eb);
+          E = Eb;
+          if (begun) {
+            // O is at rest: the scores' commit came after all earlier products.
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + c, o);
+              tmem_wait_ld32(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32(tO + c, o);
+            }
+          }
+        }
+        begun = true;
+        const float shift = kChPBias - (m == kNegInf ? 0.0f : m);
+        const uint64_t f2 = pack_f2(rowf, rowf), s2 = pack_f2(shift, shift);
+        uint64_t l2 = pack_f2(l, 0.0f);
+        const bool poison = sc.poison;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const int k = 64 * q + c;
+            float2 a = unpack_f2(fma_f2(pack_f2(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), f2, s2));
+            a = make_float2(ex2(a.x), ex2(a.y));
+            l2 = add_f2(l2, pack_f2(a.x, a.y));
+            w[c / 2] = pack2<true>(a.x, a.y);
+          }
+          if (poison) {
+            // Tokens whose V is NaN: their weight is NaN in the rows that see them.
+#pragma unroll 1
+            for (int c = 0; c < 64; ++c) {
+              const int k = 64 * q + c;
+              if ((sc.nan[k >> 2] >> (k & 3)) & 1) {
+                const bool sees = key0 + k >= lo && key0 + k <= hi;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (j == c / 2 && sees) w[j] |= c & 1 ? 0x7FFF0000u : 0x7FFFu;
+              }
+            }
+          }
+          tmem_st32(tS + 32 * q, w);
+        }
+        {
+          const float2 a = unpack_f2(l2);
+          l = a.x + a.y;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_addr(&sm.p_full[t]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[ss]));
+      }
+      if (!ok) break;
+      n += x.nblk;
+
+      // The end of the part: O / l, and the halves' results joined in solo.
+      if (begun) {
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.o_full[t], ends & 1));
+        if (!ok) break;
+        ++ends;
+        tc_fence_after();
+      }
+      if (solo && t == 1) {
+        sm.ml[r] = make_float2(m, l);
+        if (r == 0) sm.e1 = E;
+        mbar_arrive(smem_addr(&sm.x_full));
+        // The first half reads this half's O.
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.x_empty, solos & 1));
+        ++solos;
+        if (!ok) break;
+        continue;
+      }
+      float f0 = 1.0f, f1 = 0.0f;
+      if (solo) {
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.x_full, solos & 1));
+        ++solos;
+        if (!ok) break;
+        tc_fence_after();
+        const float2 y = sm.ml[r];
+        const int e1 = sm.e1;
+        const float mj = fmaxf(m, y.x), ref = mj == kNegInf ? 0.0f : mj;
+        const int Ej = max(E, e1);
+        f0 = ex2(m - ref);
+        f1 = ex2(y.x - ref);
+        l = l * f0 + y.y * f1;
+        f0 *= exp2i(E - Ej);
+        f1 = x.nblk > 1 ? f1 * exp2i(e1 - Ej) : 0.0f;
+        m = mj;
+        E = Ej;
+      }
+      // 2^(E-127) and V's 2^7; the weights' 2^8 is in l.
+      const float inv = l == 0.0f ? 0.0f : exp2i(-kChVBias) / l, se = scale_value(E);
+      f0 *= inv;
+      f1 *= inv;
+      const float L = l == 0.0f ? kNegInf : m + log2f(l) - kChPBias;
+      uint16_t* orow = static_cast<uint16_t*>(P.o.ptr) + (s.q0 + tok) * P.o.st + hq * P.o.sh;
+      const int64_t place = (static_cast<int64_t>(blockIdx.x) * 2 + x.slot) * kChRows + row;
+      const bool two = solo && x.nblk > 1;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        float y[32];
+        tmem_ld32(tO + c, o);
+        tmem_wait_ld32(o);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * f0;
+        if (two) {
+          tmem_ld32(tO + 128 + c, o);
+          tmem_wait_ld32(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) y[k] += __uint_as_float(o[k]) * f1;
+        }
+        if (here) {
+          if (x.slot < 0) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(orow + c + k) =
+                  make_uint4(pack2<false>(y[k] * se, y[k + 1] * se), pack2<false>(y[k + 2] * se, y[k + 3] * se),
+                             pack2<false>(y[k + 4] * se, y[k + 5] * se), pack2<false>(y[k + 6] * se, y[k + 7] * se));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(work.o + place * 128 + c + k) = make_float4(y[k] * se, y[k + 1] * se, y[k + 2] * se, y[k + 3] * se);
+          }
+        }
+      }
+      tc_fence_before();
+      if (here) {
+        if (x.slot >= 0) work.lse[place] = L;
+        else if (P.lse) P.lse[static_cast<int64_t>(s.q0 + tok) * P.Hq + hq] = L * 0.69314718055994531f;
+      }
+      if (solo) mbar_arrive(smem_addr(&sm.x_empty));
+    }
+    if (!ok) give_up();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace ovc

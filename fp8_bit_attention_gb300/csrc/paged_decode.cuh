@@ -79,7 +79,8 @@ constexpr int kDecodeCtas = kTiles == 1 ? 3 : 2;
 static_assert((sizeof(DecodeSmem) + 1024) * 3 <= 233472, "shared memory per SM");
 
 struct PagedMaps {
-  CUtensorMap k, v;
+  CUtensorMap k, v;     // boxes of `box` rows, which divides the page and the key block
+  int32_t box;
   int32_t rows;         // rows of the cache: a box from there on reads zeros
   int32_t min_share;
   uint64_t timeout_ns;

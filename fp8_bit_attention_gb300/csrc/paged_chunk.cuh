@@ -24,10 +24,11 @@
 // walks the share, looks up pages and loads K and V; 13 issues the products; 14
 // loads the scales; 15 idles.  All waits are bounded.
 //
-// Numbers: scores, maxima, sums and outputs are FP32.  Weights are 2^8 p relative
-// to a reference that follows the row's maximum only when that passes it by
-// 2^7 (then O is rescaled in tensor memory), so they lie below FP16's largest
-// value and are flushed below 2^-32.  V's values are flushed below 2^-31 of the
+// Numbers: scores, references, sums and outputs are FP32.  Weights are 2^7 p
+// relative to a reference, the row's maximum when it was last looked for: that is
+// when the weights of a block add up to 2^15.5, so that none passes FP16's
+// largest value (O is then rescaled in tensor memory).  Weights are flushed below
+// 2^-32 of the one at the reference.  V's values are flushed below 2^-31 of the
 // largest token's.
 #pragma once
 
@@ -44,8 +45,8 @@ constexpr int kChOtherRegs = 72;
 static_assert(256 * kChSoftmaxRegs + 256 * kChOtherRegs <= kChThreads * 128, "register split");
 constexpr uint32_t kChTile = 128 * 128;            // bytes of an E4M3 tile
 constexpr uint32_t kChTile16 = 2 * kChTile;        // bytes of V in FP16
-constexpr float kChPBias = 8.0f;                   // log2 of the weight at the reference
-constexpr float kChLazy = 7.0f;                    // how far a maximum may pass the reference
+constexpr float kChPBias = 7.0f;                   // log2 of the weight at the reference
+constexpr float kChSumLimit = 46341.0f;            // 2^15.5: a row's weights in a block stay below FP16's largest value
 constexpr int kChVBias = 7;
 constexpr int kChParts = 4;
 
@@ -54,16 +55,16 @@ struct ChunkShape {
   static constexpr int kQParts = kHalf ? 3 : 2;
   static constexpr int kK = kHalf ? 2 : 3;         // stages of K
   static constexpr int kV = kHalf ? 1 : 2;         // stages of V's codes
-  static constexpr int kScales = 2;
+  static constexpr int kScales = 4;
 };
 
 // A block's scales: those of K as values, those of V as FP16 pairs 2^(e-E+7).
 struct alignas(16) ChunkScales {
   float k[kChKeys];
   uint32_t v[kChKeys];
-  uint8_t nan[32];                                 // bit j of byte i: V's scale of key 4 i + j is NaN
+  uint8_t nan[kChKeys];                            // 1: K's scale is NaN, 2: V's (their values above are 1 and 0)
   int e;                                           // E
-  int poison;                                      // any such bit
+  int poison;                                      // any such token
 };
 
 // A tile's part.
@@ -154,6 +155,18 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+
+// One column of this thread's lane of tensor memory.
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t x;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x)
+      : "r"(taddr)
+      : "memory");
+  return x;
 }
 
 // 2^x as an FP16 pair, x <= 15.
@@ -410,8 +423,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
           for (int j = 0; j < 4; ++j) {
             const uint32_t ev = (vw >> (8 * j)) & 255u;
             if (j < left) {
-              if (ev == 255u) nan |= 1u << j;
+              if (ev == 255u) nan |= 2u << (8 * j);
               else e = max(e, static_cast<int>(ev));
+              if (((kw >> (8 * j)) & 255u) == 255u) nan |= 1u << (8 * j);
             }
           }
           E = max(E, __reduce_max_sync(0xFFFFFFFFu, e));
@@ -420,10 +434,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
           ChunkScales& sc = sm.sc[s];
           float4 f;
           uint4 h;
-          f.x = scale_value(kw & 255u);
-          f.y = scale_value((kw >> 8) & 255u);
-          f.z = scale_value((kw >> 16) & 255u);
-          f.w = scale_value(kw >> 24);
+          auto kscale = [&](uint32_t ek) { return ek == 255u ? 1.0f : scale_value(ek); };
+          f.x = kscale(kw & 255u);
+          f.y = kscale((kw >> 8) & 255u);
+          f.z = kscale((kw >> 16) & 255u);
+          f.w = kscale(kw >> 24);
           auto vscale = [&](uint32_t ev) { return ev == 255u ? 0u : exp2h2(min(static_cast<int>(ev) - E, 0) + kChVBias); };
           h.x = vscale(vw & 255u);
           h.y = vscale((vw >> 8) & 255u);
@@ -431,7 +446,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           h.w = vscale(vw >> 24);
           reinterpret_cast<float4*>(sc.k)[lane] = f;
           reinterpret_cast<uint4*>(sc.v)[lane] = h;
-          sc.nan[lane] = static_cast<uint8_t>(nan);
+          reinterpret_cast<uint32_t*>(sc.nan)[lane] = nan;
           const bool any = __any_sync(0xFFFFFFFFu, nan != 0);
           if (lane == 0) {
             sc.e = E;
@@ -601,46 +616,77 @@ __global__ void __launch_bounds__(kChThreads, 1)
         ++steps;
         tc_fence_after();
         const ChunkScales& sc = sm.sc[ss];
-        uint32_t z[128];
-        tmem_ld32(tS, z);
-        tmem_ld32(tS + 32, z + 32);
-        tmem_ld32(tS + 64, z + 64);
-        tmem_ld32(tS + 96, z + 96);
-        tmem_wait_ld32(z);
-        tmem_wait_ld32(z + 32);
-        tmem_wait_ld32(z + 64);
-        tmem_wait_ld32(z + 96);
-        float m0 = kNegInf, m1 = kNegInf;
+        const int key0 = (x.k0 + i) * kChKeys, a = lo - key0, b = hi - key0;
+        const bool masked = key0 < x.all_lo || key0 + kChKeys - 1 > x.all_hi;
+        if (masked) {
+          // Keys that the row does not see: -inf in tensor memory, before the
+          // scores are read, by a loop that stays out of the common path.
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t y[32];
+            tmem_ld32(tS + c, y);
+            tmem_wait_ld32(y);
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          const float4 k4 = *reinterpret_cast<const float4*>(sc.k + c);
-          const float2 a = unpack_f2(mul_f2(pack_f2(__uint_as_float(z[c]), __uint_as_float(z[c + 1])), pack_f2(k4.x, k4.y)));
-          const float2 b = unpack_f2(mul_f2(pack_f2(__uint_as_float(z[c + 2]), __uint_as_float(z[c + 3])), pack_f2(k4.z, k4.w)));
-          z[c] = __float_as_uint(a.x);
-          z[c + 1] = __float_as_uint(a.y);
-          z[c + 2] = __float_as_uint(b.x);
-          z[c + 3] = __float_as_uint(b.y);
-          m0 = fmax3(m0, a.x, a.y);
-          m1 = fmax3(m1, b.x, b.y);
-        }
-        const int key0 = (x.k0 + i) * kChKeys;
-        if (key0 < x.all_lo || key0 + kChKeys - 1 > x.all_hi) {
-          const int a = lo - key0, b = hi - key0;
-          m0 = m1 = kNegInf;
-#pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            if (c < a || c > b) z[c] = 0xFF800000u;
-            m0 = fmaxf(m0, __uint_as_float(z[c]));
+            for (int k = 0; k < 32; ++k)
+              if (c + k < a || c + k > b) y[k] = 0xFF800000u;
+            tmem_st32(tS + c, y);
           }
+          tmem_wait_st();
         }
+        // Weights against the reference at hand.  Their sum tells whether it is
+        // still good: only when that reaches kChSumLimit (and in the first
+        // blocks, without a reference) is the maximum looked for and are the
+        // weights computed again.  P stays in registers until then, since it
+        // overwrites S.
+        const uint64_t f2 = pack_f2(rowf, rowf);
         const int Eb = sc.e;
-        const float top = fmaxf(m0, m1) * rowf;
-        const bool need = top > m + kChLazy;
-        if (__any_sync(0xFFFFFFFFu, need) || Eb != E) {
-          const float mn = need ? top : m;
-          float f = m == kNegInf ? 0.0f : ex2(m - mn);
-          m = mn;
-          l *= f;
+        uint32_t w[64];
+        float sum;
+#pragma unroll 1
+        for (int attempt = 0; attempt < 2; ++attempt) {
+          const float shift = kChPBias - (m == kNegInf ? 0.0f : m);
+          const uint64_t s2 = pack_f2(shift, shift);
+          uint64_t la = 0, lb = 0;
+          uint32_t z[128];
+          tmem_ld32(tS, z);
+          tmem_ld32(tS + 32, z + 32);
+          tmem_ld32(tS + 64, z + 64);
+          tmem_ld32(tS + 96, z + 96);
+          tmem_wait_ld32(z);
+          tmem_wait_ld32(z + 32);
+          tmem_wait_ld32(z + 64);
+          tmem_wait_ld32(z + 96);
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(sc.k + c);
+            const uint64_t u = mul_f2(pack_f2(__uint_as_float(z[c]), __uint_as_float(z[c + 1])), pack_f2(k4.x, k4.y));
+            const uint64_t v = mul_f2(pack_f2(__uint_as_float(z[c + 2]), __uint_as_float(z[c + 3])), pack_f2(k4.z, k4.w));
+            const float2 e = unpack_f2(fma_f2(u, f2, s2)), f = unpack_f2(fma_f2(v, f2, s2));
+            const float p0 = ex2(e.x), p1 = ex2(e.y), p2 = ex2(f.x), p3 = ex2(f.y);
+            la = add_f2(la, pack_f2(p0, p1));
+            lb = add_f2(lb, pack_f2(p2, p3));
+            w[c / 2] = pack2<true>(p0, p1);
+            w[c / 2 + 1] = pack2<true>(p2, p3);
+          }
+          const float2 y = unpack_f2(add_f2(la, lb));
+          sum = y.x + y.y;
+          const bool again = attempt == 0 && __any_sync(0xFFFFFFFFu, m == kNegInf || sum >= kChSumLimit);
+          if (!again && Eb == E) break;
+          float f = 1.0f;
+          if (again) {
+            float top = kNegInf;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              tmem_ld32(tS + c, z);
+              tmem_wait_ld32(z);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(z[k]) * sc.k[c + k]);
+            }
+            const float mn = fmaxf(m, top * rowf);
+            f = m == kNegInf ? 0.0f : ex2(m - mn);
+            m = mn;
+            l *= f;
+          }
           f *= exp2i(E - Eb);
           E = Eb;
           if (begun) {
@@ -655,41 +701,29 @@ __global__ void __launch_bounds__(kChThreads, 1)
               tmem_st32(tO + c, o);
             }
           }
+          if (!again) break;
         }
+        l += sum;
         begun = true;
-        const float shift = kChPBias - (m == kNegInf ? 0.0f : m);
-        const uint64_t f2 = pack_f2(rowf, rowf), s2 = pack_f2(shift, shift);
-        uint64_t l2 = pack_f2(l, 0.0f);
-        const bool poison = sc.poison;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t w[32];
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const int k = 64 * q + c;
-            float2 a = unpack_f2(fma_f2(pack_f2(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), f2, s2));
-            a = make_float2(ex2(a.x), ex2(a.y));
-            l2 = add_f2(l2, pack_f2(a.x, a.y));
-            w[c / 2] = pack2<true>(a.x, a.y);
-          }
-          if (poison) {
-            // Tokens whose V is NaN: their weight is NaN in the rows that see them.
+        tmem_st32(tS, w);
+        tmem_st32(tS + 32, w + 32);
+        if (sc.poison) {
+          // Tokens whose K or V is NaN: a NaN weight in the rows that see them,
+          // and for K a NaN sum.  (In tensor memory: picked out of registers by
+          // a loop, the weights would live in local memory.)
+          tmem_wait_st();
 #pragma unroll 1
-            for (int c = 0; c < 64; ++c) {
-              const int k = 64 * q + c;
-              if ((sc.nan[k >> 2] >> (k & 3)) & 1) {
-                const bool sees = key0 + k >= lo && key0 + k <= hi;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (j == c / 2 && sees) w[j] |= c & 1 ? 0x7FFF0000u : 0x7FFFu;
-              }
+          for (int c = 0; c < 128; c += 2) {
+            const uint32_t bad0 = sc.nan[c], bad1 = sc.nan[c + 1];
+            if (bad0 | bad1) {
+              uint32_t y = tmem_ld1(tS + c / 2);
+              const uint32_t see0 = c >= a && c <= b ? bad0 : 0u, see1 = c + 1 >= a && c + 1 <= b ? bad1 : 0u;
+              if (see0) y |= 0x7FFFu;
+              if (see1) y |= 0x7FFF0000u;
+              if ((see0 | see1) & 1u) l = __uint_as_float(0x7FFFFFFFu);
+              tmem_st1(tS + c / 2, y);
             }
           }
-          tmem_st32(tS + 32 * q, w);
-        }
-        {
-          const float2 a = unpack_f2(l2);
-          l = a.x + a.y;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -735,7 +769,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         m = mj;
         E = Ej;
       }
-      // 2^(E-127) and V's 2^7; the weights' 2^8 is in l.
+      // 2^(E-127) and V's 2^7; the weights' 2^7 is in l.
       const float inv = l == 0.0f ? 0.0f : exp2i(-kChVBias) / l, se = scale_value(E);
       f0 *= inv;
       f1 *= inv;

@@ -55,6 +55,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A value that is the same in all lanes, by a shuffle: the compiler then keeps it,
+// and what is computed from it alone, in uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
 struct CacheView {
   uint8_t* k;
   uint8_t* v;

@@ -2,7 +2,7 @@
 // head: chunks of new tokens, on the tensor cores (tcgen05).
 //
 // A tile is 256 query rows (tokens times query heads of one KV head) in two
-// halves of 128, a step is one half's products with one block of 128 keys:
+// halves of 128, a step is one half's work on a block of 128 keys:
 //   S_t = Q_t K^T          kind::f8f6f4.  K's codes go in as they lie in the
 //                          cache (TMA tiles, K-major); Q enters as a sum of
 //                          E4M3 parts, each the rounding error of the ones
@@ -16,9 +16,11 @@
 //                          FP16 (exactly) by four warps, once per block for all
 //                          256 rows, with the token's scale: V 2^(e - E + 7), E
 //                          the largest scale so far.
-// While one half's softmax runs, the tensor core works on the other half.  A tile
-// of at most 128 rows keeps that overlap by giving the blocks to the halves in
-// turn, both on the same rows, and joining the two results at the end ("solo").
+// While one half's softmax runs, the tensor core works on the other half.  The
+// softmax hands over P in two parts of 64 keys, so that the first part's product
+// runs beside the second part's softmax.  A tile of at most 128 rows keeps the
+// overlap by giving the blocks to the halves in turn, both on the same rows, and
+// joining the two results at the end ("solo").
 //
 // Warps: 0-3 and 4-7 softmax of the halves, a thread per row; 8-11 convert V; 12
 // walks the share, looks up pages and loads K and V; 13 issues the products; 14
@@ -38,6 +40,7 @@ namespace ovc {
 
 constexpr int kChRows = 256;
 constexpr int kChKeys = 128;
+constexpr int kChStep = 64;                        // keys of a step
 constexpr int kChThreads = 512;
 // Registers: 512 threads of 128 at launch; 256 x 184 + 256 x 72 = 512 x 128.
 constexpr int kChSoftmaxRegs = 184;
@@ -95,7 +98,9 @@ struct ChunkSmem {
   uint64_t v8_full[Sh::kV], v8_empty[Sh::kV];
   uint64_t v16_full[2], v16_empty[2];
   uint64_t sc_full[Sh::kScales], sc_empty[Sh::kScales];
-  uint64_t s_full[2], p_full[2], o_full[2], q_full, x_full, x_empty;
+  uint64_t s_full[2], p_full[2][2];                // [half], [half][step of a block]
+  uint64_t o_done[2], o_full[2];                   // the products of a block's first step, of a part are complete
+  uint64_t q_full, x_full, x_empty;
   uint64_t part_full[kChParts], part_empty[kChParts];
   uint64_t drain;
   uint32_t tmem_base;
@@ -182,13 +187,18 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t pair) {
   return unpack2<true>(h);
 }
 
+__device__ __forceinline__ ChunkPart uniform(const ChunkPart& x) {
+  return {uniform(x.more), uniform(x.b),    uniform(x.q0),   uniform(x.ql),     uniform(x.kv),     uniform(x.p0),  uniform(x.rows),
+          uniform(x.h),    uniform(x.k0),   uniform(x.nblk), uniform(x.all_lo), uniform(x.all_hi), uniform(x.slot)};
+}
+
 template <bool kHalf>
 __global__ void __launch_bounds__(kChThreads, 1)
     paged_chunk_kernel(const __grid_constant__ PagedParams P, const __grid_constant__ PagedMaps M, PagedWork work) {
   using Sh = ChunkShape<kHalf>;
   extern __shared__ __align__(1024) uint8_t raw[];
   ChunkSmem<kHalf>& sm = *reinterpret_cast<ChunkSmem<kHalf>*>(raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int* const abort_flag = &sm.abort;
   constexpr int kReaders = 4 + 1 + 1 + 8;          // warps that read a part's description: V, products, scales, softmax
   if (threadIdx.x == 0) {
@@ -210,7 +220,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
       mbar_init(smem_addr(&sm.v16_full[i]), 128);
       mbar_init(smem_addr(&sm.v16_empty[i]), 1);
       mbar_init(smem_addr(&sm.s_full[i]), 1);
-      mbar_init(smem_addr(&sm.p_full[i]), 128);
+      for (int j = 0; j < 2; ++j) mbar_init(smem_addr(&sm.p_full[i][j]), 128);
+      mbar_init(smem_addr(&sm.o_done[i]), 1);
       mbar_init(smem_addr(&sm.o_full[i]), 1);
     }
     for (int i = 0; i < kChParts; ++i) {
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   tc_fence_before();
   __syncthreads();                                 // also: the plan's memory is free
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = uniform(sm.tmem_base);
 
   auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return mbar_wait(smem_addr(&bar), parity, M.timeout_ns, abort_flag); };
   auto give_up = [&]() {
@@ -323,6 +334,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
       }
     } else if (warp == 13) {
       // --------------------------------------------------------- the products
+      // By one warp, the halves in turn: with a warp for each the two fall into
+      // step, and both softmaxes wait for both halves' products (3.9 against 3.1
+      // ms for 4096 tokens x 32 heads over 65536 keys).  What the products are
+      // told must be in uniform registers: computed per lane, each costs the warp
+      // several times its 64 cycles (3.7 ms).
       uint32_t parts = 0, n = 0, steps[2] = {0, 0};
       bool ok = true, issued = false;
       const uint64_t qd = sw128_desc(smem_addr(sm.q[0][0]));
@@ -330,21 +346,23 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const uint32_t d = parts % kChParts;
         ok = __all_sync(0xFFFFFFFFu, wait(sm.part_full[d], (parts / kChParts) & 1));
         if (!ok || !sm.part[d].more) break;
-        const int nblk = sm.part[d].nblk;
-        const bool solo = sm.part[d].rows <= 128;
+        const int nblk = uniform(sm.part[d].nblk);
+        const bool solo = uniform(sm.part[d].rows) <= 128;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[d]));
         ok = __all_sync(0xFFFFFFFFu, wait(sm.q_full, parts & 1));
         if (!ok) break;
         ++parts;
         tc_fence_after();
+        // Turn i: half i & 1 on block i / 2, in solo on block i.
         const int total = solo ? nblk : 2 * nblk;
+        auto wait_k = [&](int i) {
+          const uint32_t blk = n + (solo ? i : i >> 1);
+          ok = __all_sync(0xFFFFFFFFu, wait(sm.k_full[blk % Sh::kK], (blk / Sh::kK) & 1));
+        };
         auto scores = [&](int i) {
           const int t = i & 1;
           const uint32_t blk = n + (solo ? i : i >> 1), ks = blk % Sh::kK;
-          ok = __all_sync(0xFFFFFFFFu, wait(sm.k_full[ks], (blk / Sh::kK) & 1));
-          if (!ok) return;
-          tc_fence_after();
           const uint64_t kd = sw128_desc(smem_addr(sm.k[ks]));
 #pragma unroll
           for (int part = 0; part < Sh::kQParts; ++part)
@@ -356,20 +374,33 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (solo || t == 1) tc_commit_w(smem_addr(&sm.k_empty[ks]));
           issued = true;
         };
-        scores(0);
-        if (ok && total > 1) scores(1);
+        for (int i = 0; i < 2 && i < total; ++i) {
+          wait_k(i);
+          if (!ok) break;
+          tc_fence_after();
+          scores(i);
+        }
         for (int i = 0; i < total && ok; ++i) {
           const int t = i & 1;
           const uint32_t blk = n + (solo ? i : i >> 1), vs = blk & 1;
-          ok = __all_sync(0xFFFFFFFFu, wait(sm.v16_full[vs], (blk >> 1) & 1) && wait(sm.p_full[t], steps[t] & 1));
+          const uint64_t vd = v16_desc(smem_addr(sm.v16[vs]));
+          // The waits for what has long been there come first: even a wait for a
+          // completed barrier takes a round trip.
+          if (i + 2 < total && (solo || t == 0)) wait_k(i + 2);
+          if (ok && (solo || t == 0)) ok = __all_sync(0xFFFFFFFFu, wait(sm.v16_full[vs], (blk >> 1) & 1));
+          if (!ok) break;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = __all_sync(0xFFFFFFFFu, wait(sm.p_full[t][half], steps[t] & 1));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              mma_16_ts_w(tmem + 256 + t * 128, tmem + t * 128 + 8 * kk, vd + kk * (2048 >> 4), kChIdescPV, i > 1 || kk > 0);
+            if (half == 0) tc_commit_w(smem_addr(&sm.o_done[t]));
+          }
           if (!ok) break;
           ++steps[t];
-          tc_fence_after();
-          const uint64_t vd = v16_desc(smem_addr(sm.v16[vs]));
-          const bool first = i < 2;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_16_ts_w(tmem + 256 + t * 128, tmem + t * 128 + 8 * kk, vd + kk * (2048 >> 4), kChIdescPV, !first || kk > 0);
           if (solo || t == 1) tc_commit_w(smem_addr(&sm.v16_empty[vs]));
           if (i + 2 < total) scores(i + 2);
           else tc_commit_w(smem_addr(&sm.o_full[t]));
@@ -391,7 +422,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const uint32_t d = parts % kChParts;
         ok = __all_sync(0xFFFFFFFFu, wait(sm.part_full[d], (parts / kChParts) & 1));
         if (!ok || !sm.part[d].more) break;
-        const ChunkPart x = sm.part[d];
+        const ChunkPart x = uniform(sm.part[d]);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[d]));
         ++parts;
@@ -469,7 +500,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const uint32_t d = parts % kChParts;
         ok = __all_sync(0xFFFFFFFFu, wait(sm.part_full[d], (parts / kChParts) & 1));
         if (!ok || !sm.part[d].more) break;
-        const int nblk = sm.part[d].nblk, k0 = sm.part[d].k0, kv = sm.part[d].kv;
+        const int nblk = uniform(sm.part[d].nblk), k0 = uniform(sm.part[d].k0), kv = uniform(sm.part[d].kv);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[d]));
         ++parts;
@@ -522,14 +553,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
     const int t = warp >> 2;                       // the half
     const int r = threadIdx.x & 127;               // the row in it
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + 256 + t * 128;
+    const uint32_t tO = tmem + lanes + 256 + t * 128;
     uint32_t parts = 0, n = 0, steps = 0, ends = 0, solos = 0;
     bool ok = true;
     while (true) {
       const uint32_t d = parts % kChParts;
       ok = __all_sync(0xFFFFFFFFu, wait(sm.part_full[d], (parts / kChParts) & 1));
       if (!ok || !sm.part[d].more) break;
-      const ChunkPart x = sm.part[d];
+      const ChunkPart x = uniform(sm.part[d]);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[d]));
       ++parts;
@@ -611,18 +642,24 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[ss]));
           continue;
         }
-        ok = __all_sync(0xFFFFFFFFu, wait(sm.s_full[t], steps & 1));
-        if (!ok) break;
-        ++steps;
-        tc_fence_after();
         const ChunkScales& sc = sm.sc[ss];
-        const int key0 = (x.k0 + i) * kChKeys, a = lo - key0, b = hi - key0;
-        const bool masked = key0 < x.all_lo || key0 + kChKeys - 1 > x.all_hi;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+        // Two steps a block: scores in columns 64 half .., weights in 32 half ..
+        const uint32_t tS = tmem + lanes + t * 128 + half * kChStep, tP = tmem + lanes + t * 128 + half * (kChStep / 2);
+        if (half == 0) {
+          ok = __all_sync(0xFFFFFFFFu, wait(sm.s_full[t], steps & 1));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const float* sk = sc.k + half * kChStep;
+        const int key0 = (x.k0 + i) * kChKeys + half * kChStep, a = lo - key0, b = hi - key0;
+        const bool masked = key0 < x.all_lo || key0 + kChStep - 1 > x.all_hi;
         if (masked) {
           // Keys that the row does not see: -inf in tensor memory, before the
           // scores are read, by a loop that stays out of the common path.
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < kChStep; c += 32) {
             uint32_t y[32];
             tmem_ld32(tS + c, y);
             tmem_wait_ld32(y);
@@ -640,25 +677,21 @@ __global__ void __launch_bounds__(kChThreads, 1)
         // overwrites S.
         const uint64_t f2 = pack_f2(rowf, rowf);
         const int Eb = sc.e;
-        uint32_t w[64];
+        uint32_t w[32];
         float sum;
 #pragma unroll 1
         for (int attempt = 0; attempt < 2; ++attempt) {
           const float shift = kChPBias - (m == kNegInf ? 0.0f : m);
           const uint64_t s2 = pack_f2(shift, shift);
           uint64_t la = 0, lb = 0;
-          uint32_t z[128];
+          uint32_t z[kChStep];
           tmem_ld32(tS, z);
           tmem_ld32(tS + 32, z + 32);
-          tmem_ld32(tS + 64, z + 64);
-          tmem_ld32(tS + 96, z + 96);
           tmem_wait_ld32(z);
           tmem_wait_ld32(z + 32);
-          tmem_wait_ld32(z + 64);
-          tmem_wait_ld32(z + 96);
 #pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            const float4 k4 = *reinterpret_cast<const float4*>(sc.k + c);
+          for (int c = 0; c < kChStep; c += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(sk + c);
             const uint64_t u = mul_f2(pack_f2(__uint_as_float(z[c]), __uint_as_float(z[c + 1])), pack_f2(k4.x, k4.y));
             const uint64_t v = mul_f2(pack_f2(__uint_as_float(z[c + 2]), __uint_as_float(z[c + 3])), pack_f2(k4.z, k4.w));
             const float2 e = unpack_f2(fma_f2(u, f2, s2)), f = unpack_f2(fma_f2(v, f2, s2));
@@ -676,11 +709,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (again) {
             float top = kNegInf;
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
+            for (int c = 0; c < kChStep; c += 32) {
               tmem_ld32(tS + c, z);
               tmem_wait_ld32(z);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(z[k]) * sc.k[c + k]);
+              for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(z[k]) * sk[c + k]);
             }
             const float mn = fmaxf(m, top * rowf);
             f = m == kNegInf ? 0.0f : ex2(m - mn);
@@ -689,8 +722,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
           f *= exp2i(E - Eb);
           E = Eb;
-          if (begun) {
-            // O is at rest: the scores' commit came after all earlier products.
+          if (begun || half == 1) {
+            // O is at rest in a block's first step (its scores came after all
+            // earlier products), in the second once the first one's are complete.
+            if (half == 1) ok = __all_sync(0xFFFFFFFFu, wait(sm.o_done[t], steps & 1));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
               uint32_t o[32];
@@ -703,31 +740,34 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
           if (!again) break;
         }
+        if (!ok) break;
         l += sum;
-        begun = true;
-        tmem_st32(tS, w);
-        tmem_st32(tS + 32, w + 32);
+        tmem_st32(tP, w);
         if (sc.poison) {
           // Tokens whose K or V is NaN: a NaN weight in the rows that see them,
           // and for K a NaN sum.  (In tensor memory: picked out of registers by
           // a loop, the weights would live in local memory.)
           tmem_wait_st();
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 2) {
-            const uint32_t bad0 = sc.nan[c], bad1 = sc.nan[c + 1];
+          for (int c = 0; c < kChStep; c += 2) {
+            const uint32_t bad0 = sc.nan[half * kChStep + c], bad1 = sc.nan[half * kChStep + c + 1];
             if (bad0 | bad1) {
-              uint32_t y = tmem_ld1(tS + c / 2);
+              uint32_t y = tmem_ld1(tP + c / 2);
               const uint32_t see0 = c >= a && c <= b ? bad0 : 0u, see1 = c + 1 >= a && c + 1 <= b ? bad1 : 0u;
               if (see0) y |= 0x7FFFu;
               if (see1) y |= 0x7FFF0000u;
               if ((see0 | see1) & 1u) l = __uint_as_float(0x7FFFFFFFu);
-              tmem_st1(tS + c / 2, y);
+              tmem_st1(tP + c / 2, y);
             }
           }
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_addr(&sm.p_full[t]));
+        mbar_arrive(smem_addr(&sm.p_full[t][half]));
+        }
+        if (!ok) break;
+        ++steps;
+        begun = true;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[ss]));
       }

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
   constexpr int R = 8 * kTiles;
   extern __shared__ __align__(1024) uint8_t raw[];
   DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>(raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     sm.abort = 0;
     sm.zero = 0;

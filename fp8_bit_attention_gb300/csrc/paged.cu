@@ -32,7 +32,7 @@ bool cache_ok(const ovc_kv_cache* c) {
 }
 
 ovc_status rows_ok(const ovc_rows* r) {
-  if (!r || r->T < 1 || r->H < 1 || r->T > 0x7FFFFFFF || r->H > 65535 * 256) return OVC_ERR_INVALID_ARG;
+  if (!r || r->T < 1 || r->H < 1 || r->T > 0x7FFFFC00 || r->H > 65535 * 256) return OVC_ERR_INVALID_ARG;
   if (!at16(r->ptr) || r->stride_t % 8 || r->stride_h % 8 || r->stride_t < 0 || r->stride_h < 0) return OVC_ERR_INVALID_ARG;
   return r->dtype == OVC_BF16 || r->dtype == OVC_FP16 ? OVC_OK : OVC_ERR_UNSUPPORTED;
 }
@@ -54,7 +54,17 @@ ovc_status cache_call_ok(const ovc_kv_cache* c, const ovc_rows* k, const ovc_row
   st = rows_ok(v);
   if (st != OVC_OK) return st;
   if (k->T != v->T || k->H != c->heads || v->H != c->heads || k->dtype != v->dtype) return OVC_ERR_INVALID_ARG;
-  return (k->T * k->H + kCacheVecs - 1) / kCacheVecs <= 0x7FFFFFFF ? OVC_OK : OVC_ERR_INVALID_ARG;
+  return OVC_OK;
+}
+
+// Whether four tokens a lane would leave less than two CTAs an SM.
+bool few_tokens(const ovc_rows* r, const DeviceState* dev) {
+  return (r->T + 4 * kCacheGroups - 1) / (4 * kCacheGroups) * r->H * 2 < 2 * dev->sms;
+}
+
+dim3 cache_grid(const ovc_rows* r, bool few) {
+  const int64_t tokens = kCacheGroups * (few ? 1 : 4);
+  return dim3(static_cast<unsigned>((r->T + tokens - 1) / tokens), static_cast<unsigned>(r->H), 2);
 }
 
 bool batch_ok(const ovc_paged_batch* b) {
@@ -185,10 +195,11 @@ ovc_status ovc_kv_write(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows
   DeviceState* dev = nullptr;
   st = device_state(&dev);
   if (st != OVC_OK) return st;
-  const int64_t n = k->T * k->H;
-  const dim3 grid(static_cast<unsigned>((n + kCacheVecs - 1) / kCacheVecs), 2);
-  auto* fn = k->dtype == OVC_FP16 ? kv_write_kernel<true> : kv_write_kernel<false>;
-  fn<<<grid, kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(view(c), view(k), view(v), slots, n, dev->status);
+  const bool few = few_tokens(k, dev);
+  auto* fn = k->dtype == OVC_FP16 ? (few ? kv_write_kernel<true, 1> : kv_write_kernel<true, 4>)
+                                  : (few ? kv_write_kernel<false, 1> : kv_write_kernel<false, 4>);
+  fn<<<cache_grid(k, few), kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      view(c), fast_div(static_cast<int32_t>(c->page)), view(k), view(v), slots, static_cast<int32_t>(k->T), dev->status);
   return launched();
 }
 
@@ -199,10 +210,11 @@ ovc_status ovc_kv_read(const ovc_kv_cache* c, const int32_t* slots, const ovc_ro
   DeviceState* dev = nullptr;
   st = device_state(&dev);
   if (st != OVC_OK) return st;
-  const int64_t n = k->T * k->H;
-  const dim3 grid(static_cast<unsigned>((n + kCacheVecs - 1) / kCacheVecs), 2);
-  auto* fn = k->dtype == OVC_FP16 ? kv_read_kernel<true> : kv_read_kernel<false>;
-  fn<<<grid, kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(view(c), view(k), view(v), slots, n, dev->status);
+  const bool few = few_tokens(k, dev);
+  auto* fn = k->dtype == OVC_FP16 ? (few ? kv_read_kernel<true, 1> : kv_read_kernel<true, 4>)
+                                  : (few ? kv_read_kernel<false, 1> : kv_read_kernel<false, 4>);
+  fn<<<cache_grid(k, few), kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      view(c), fast_div(static_cast<int32_t>(c->page)), view(k), view(v), slots, static_cast<int32_t>(k->T), dev->status);
   return launched();
 }
 

@@ -54,7 +54,7 @@ class KVCache:
                 raise ValueError("a cache's tensors must be contiguous, 16-byte aligned uint8")
         desc = _abi.OvcKVCache(shape[0], shape[1], shape[2], self.k.data_ptr(), self.v.data_ptr(),
                                self.k_scale.data_ptr(), self.v_scale.data_ptr())
-        object.__setattr__(self, "_desc", desc)
+        object.__setattr__(self, "_ref", _byref(desc))     # the C struct, kept alive by its reference
 
     @property
     def pages(self) -> int:
@@ -95,27 +95,41 @@ def _on(dev: torch.device, stream):
 
 def _call(dev, stream, fn):
     """fn(stream handle) under the right device and stream; the usual case, the
-    current ones, without the context managers' cost."""
+    current ones, without the cost of the context managers and stream objects."""
     if stream is None and dev.index == torch.cuda.current_device():
-        return fn(torch.cuda.current_stream().cuda_stream)
+        return fn(torch._C._cuda_getCurrentRawStream(dev.index))
     with _on(dev, stream):
-        return fn(torch.cuda.current_stream().cuda_stream)
+        return fn(torch._C._cuda_getCurrentRawStream(dev.index))
+
+
+def _device(first: torch.Tensor, *others, stream=None) -> torch.device:
+    """The device of all of them (None entries skipped), as :func:`_device_of`."""
+    dev = first.device
+    if stream is None and dev.type == "cuda":
+        for x in others:
+            if x is not None and x.device != dev:
+                break
+        else:
+            return dev
+    return _device_of(first, *others, stream=stream)
 
 
 def _rows(x: torch.Tensor, what: str, heads: int | None = None) -> _abi.OvcRows:
-    if x.dim() != 3 or x.shape[2] != 128 or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{what} must be [tokens, {heads or 'heads'}, 128], got {tuple(x.shape)}")
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{what} must be [tokens, {heads or 'heads'}, 128], got {tuple(shape)}")
     code = _DTYPES.get(x.dtype)
     if code is None:
         raise TypeError(f"{what} must be bfloat16 or float16, got {x.dtype}")
     st, sh, sc = x.stride()
-    if sc != 1 or st % 8 or sh % 8 or x.data_ptr() % 16:
+    ptr = x.data_ptr()
+    if sc != 1 or st % 8 or sh % 8 or ptr % 16:
         raise ValueError(f"{what} needs unit channel stride, strides that are multiples of 8 and 16-byte alignment")
-    return _abi.OvcRows(x.data_ptr(), code, x.shape[0], x.shape[1], st, sh)
+    return _abi.OvcRows(ptr, code, shape[0], shape[1], st, sh)
 
 
 def _ints(x: torch.Tensor, shape: tuple, what: str) -> int:
-    if x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous():
+    if x.dtype != torch.int32 or x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor {list(shape)}, got {x.dtype} {list(x.shape)}")
     return x.data_ptr()
 
@@ -126,14 +140,14 @@ def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     [T]).  Negative slots are skipped (padding); slots beyond the cache are
     skipped and reported by :func:`device_status` (7).  A slot is given at most
     once per call.  See ``ovc_kv_write`` for the format."""
-    dev = _device_of(cache.k, k, v, slots, stream=stream)
+    dev = _device(cache.k, k, v, slots, stream=stream)
     rk, rv = _rows(k, "k", cache.heads), _rows(v, "v", cache.heads)
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have one shape and dtype")
     ps = _ints(slots, (k.shape[0],), "slots")
     if k.shape[0] == 0:
         return
-    check(_call(dev, stream, lambda s: lib().ovc_kv_write(_byref(cache._desc), _byref(rk), _byref(rv), ps, s)), "ovc_kv_write")
+    check(_call(dev, stream, lambda s: lib().ovc_kv_write(cache._ref, _byref(rk), _byref(rv), ps, s)), "ovc_kv_write")
 
 
 def kv_cache_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
@@ -141,7 +155,7 @@ def kv_cache_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype = t
     `dtype` (bfloat16 or float16) tensors [T, heads, 128], or in the pair `out`.
     Negative slots give zeros; so do slots beyond the cache, which
     :func:`device_status` reports (7)."""
-    dev = _device_of(cache.k, slots, *(out or ()), stream=stream)
+    dev = _device(cache.k, slots, *(out or ()), stream=stream)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
     if slots.dim() != 1:
@@ -158,7 +172,7 @@ def kv_cache_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype = t
             torch.empty((n, cache.heads, 128), dtype=dtype, device=dev) for _ in range(2))
         if n:
             rk, rv = (_rows(x, "out", cache.heads) for x in pair)
-            check(lib().ovc_kv_read(_byref(cache._desc), ps, _byref(rk), _byref(rv), s), "ovc_kv_read")
+            check(lib().ovc_kv_read(cache._ref, ps, _byref(rk), _byref(rv), s), "ovc_kv_read")
         return pair[0], pair[1]
 
     return _call(dev, stream, run)
@@ -194,7 +208,7 @@ def paged_attention_workspace_bytes(q: torch.Tensor, cache: KVCache, page_table:
     if q.shape[0] == 0:
         return 0
     b = _batch(q, cache, page_table, kv_lens, cu_q, max_q, True, None)
-    return int(lib().ovc_paged_attention_workspace_bytes(_byref(_rows(q, "q")), _byref(cache._desc), _byref(b)))
+    return int(lib().ovc_paged_attention_workspace_bytes(_byref(_rows(q, "q")), cache._ref, _byref(b)))
 
 
 def paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, *,
@@ -218,24 +232,23 @@ def paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, k
     gives 0 and -inf.  Rows of no sequence are left as they were (in a new
     output: unset).  Indices outside the cache, the table or q are cut off and
     reported by :func:`device_status` (7)."""
-    dev = _device_of(q, cache.k, page_table, kv_lens, cu_q, out, workspace, stream=stream)
+    dev = _device(q, cache.k, page_table, kv_lens, cu_q, out, workspace, stream=stream)
     rq = _rows(q, "q")
     b = _batch(q, cache, page_table, kv_lens, cu_q, max_q, causal, window)
     if out is not None and (out.shape != q.shape or out.dtype != torch.bfloat16):
         raise ValueError("out must be a bfloat16 tensor shaped like q")
 
     def run(s):
-        o = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        o = out if out is not None else torch.empty_like(q, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if return_lse else None
         if q.shape[0] and b.B:
             ro = _rows(o, "out")
-            ws = workspace
+            L, pq, pb, ws = lib(), _byref(rq), _byref(b), workspace
             if ws is None:
-                need = lib().ovc_paged_attention_workspace_bytes(_byref(rq), _byref(cache._desc), _byref(b))
-                ws = torch.empty(need, dtype=torch.uint8, device=dev)
-            check(lib().ovc_paged_attention(_byref(rq), _byref(cache._desc), _byref(b), float(softmax_scale or 0.0),
-                                            _byref(ro), lse.data_ptr() if lse is not None else None, ws.data_ptr(),
-                                            ws.numel(), s), "ovc_paged_attention")
+                ws = torch.empty(L.ovc_paged_attention_workspace_bytes(pq, cache._ref, pb), dtype=torch.uint8, device=dev)
+            check(L.ovc_paged_attention(pq, cache._ref, pb, float(softmax_scale or 0.0), _byref(ro),
+                                        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), s),
+                  "ovc_paged_attention")
         return (o, lse) if return_lse else o
 
     return _call(dev, stream, run)

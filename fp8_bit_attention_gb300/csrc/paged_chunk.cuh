@@ -187,6 +187,51 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t pair) {
   return unpack2<true>(h);
 }
 
+// 32 bytes in one store (a whole sector): the address is a multiple of 32.
+__device__ __forceinline__ void store8(float* to, const float* y) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(to)), "f"(y[0]), "f"(y[1]),
+               "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Two FP16 pairs -> four E4M3 bytes in order (nearest even, saturating).
+__device__ __forceinline__ uint32_t e4m3x4_of_f16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\t"
+      "mov.b32 %0, {x, y};\n\t}"
+      : "=r"(d)
+      : "r"(a), "r"(b));
+  return d;
+}
+
+// Largest magnitude of 64 BF16 or FP16 pairs, NaN if one is NaN.
+template <bool kHalf>
+__device__ __forceinline__ float row_amax(const uint32_t* w) {
+  uint32_t m[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 64; ++i) {
+    const uint32_t x = w[i] & 0x7FFF7FFFu;
+    if (kHalf) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m[i & 3]) : "r"(x));
+    else asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m[i & 3]) : "r"(x));
+  }
+  float best = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = unpack2<kHalf>(m[i]);
+    // (A NaN counts as an infinity: fmaxf would drop it.)
+    best = fmaxf(best, fmaxf(a.x == a.x ? a.x : INFINITY, a.y == a.y ? a.y : INFINITY));
+  }
+  return best;
+}
+
 __device__ __forceinline__ ChunkPart uniform(const ChunkPart& x) {
   return {uniform(x.more), uniform(x.b),    uniform(x.q0),   uniform(x.ql),     uniform(x.kv),     uniform(x.p0),  uniform(x.rows),
           uniform(x.h),    uniform(x.k0),   uniform(x.nblk), uniform(x.all_lo), uniform(x.all_hi), uniform(x.slot)};
@@ -586,32 +631,30 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) q[i] = __ldg(src + i);
         }
-        float amax = 0.0f;
         const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const float2 a = unpack2<kHalf>(w[i]);
-          amax = fmaxf(amax, fmaxf(a.x == a.x ? fabsf(a.x) : INFINITY, a.y == a.y ? fabsf(a.y) : INFINITY));
-        }
-        const uint32_t e = scale_byte(amax);
+        const uint32_t e = scale_byte(row_amax<kHalf>(w));
         const float mul = e == 255u ? 0.0f : inverse_scale(e);
+        const uint64_t mul2 = pack_f2(mul, mul);
         rowf *= scale_value(e);                    // NaN for a row that is not finite: so are its results
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t out[Sh::kQParts][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float2 a = unpack2<kHalf>(w[8 * c + 2 * i]), b = unpack2<kHalf>(w[8 * c + 2 * i + 1]);
-            a = make_float2(a.x * mul, a.y * mul);
-            b = make_float2(b.x * mul, b.y * mul);
+            // As FP16 pairs: exact where E4M3's range reaches, and so is what a
+            // part leaves over.
+            float2 f = unpack2<kHalf>(w[8 * c + 2 * i]), g = unpack2<kHalf>(w[8 * c + 2 * i + 1]);
+            f = unpack_f2(mul_f2(pack_f2(f.x, f.y), mul2));
+            g = unpack_f2(mul_f2(pack_f2(g.x, g.y), mul2));
+            uint32_t a = pack2<true>(f.x, f.y), b = pack2<true>(g.x, g.y);
 #pragma unroll
             for (int k = 0; k < Sh::kQParts; ++k) {
-              const uint32_t ca = cvt_e4m3x2(a.x, a.y), cb = cvt_e4m3x2(b.x, b.y);
-              out[k][i] = ca | (cb << 16);
+              out[k][i] = e4m3x4_of_f16(a, b);
               if (k + 1 < Sh::kQParts) {
-                const float2 va = e4m3x2_values(ca), vb = e4m3x2_values(cb);
-                a = make_float2(a.x - va.x, a.y - va.y);
-                b = make_float2(b.x - vb.x, b.y - vb.y);
+                uint32_t va, vb;
+                cvt_e4m3x4_to_f16x2x2(out[k][i], va, vb);
+                a = hsub2(a, va);
+                b = hsub2(b, vb);
               }
             }
           }
@@ -679,6 +722,24 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int Eb = sc.e;
         uint32_t w[32];
         float sum;
+        // The row's largest score of the step, in log2 units.
+        auto largest = [&]() {
+          float top = kNegInf;
+#pragma unroll 1
+          for (int c = 0; c < kChStep; c += 32) {
+            uint32_t y[32];
+            tmem_ld32(tS + c, y);
+            tmem_wait_ld32(y);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(sk + c + k);
+              top = fmax3(top, __uint_as_float(y[k]) * k4.x, __uint_as_float(y[k + 1]) * k4.y);
+              top = fmax3(top, __uint_as_float(y[k + 2]) * k4.z, __uint_as_float(y[k + 3]) * k4.w);
+            }
+          }
+          return top * rowf;
+        };
+        if (!begun && half == 0) m = largest();      // a part's first step has no reference to try
 #pragma unroll 1
         for (int attempt = 0; attempt < 2; ++attempt) {
           const float shift = kChPBias - (m == kNegInf ? 0.0f : m);
@@ -703,19 +764,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
           const float2 y = unpack_f2(add_f2(la, lb));
           sum = y.x + y.y;
-          const bool again = attempt == 0 && __any_sync(0xFFFFFFFFu, m == kNegInf || sum >= kChSumLimit);
+          const bool again = attempt == 0 && __any_sync(0xFFFFFFFFu, here && (m == kNegInf || sum >= kChSumLimit));
           if (!again && Eb == E) break;
           float f = 1.0f;
           if (again) {
-            float top = kNegInf;
-#pragma unroll 1
-            for (int c = 0; c < kChStep; c += 32) {
-              tmem_ld32(tS + c, z);
-              tmem_wait_ld32(z);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(z[k]) * sk[c + k]);
-            }
-            const float mn = fmaxf(m, top * rowf);
+            const float mn = fmaxf(m, largest());
             f = m == kNegInf ? 0.0f : ex2(m - mn);
             m = mn;
             l *= f;
@@ -840,8 +893,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
                              pack2<false>(y[k + 4] * se, y[k + 5] * se), pack2<false>(y[k + 6] * se, y[k + 7] * se));
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(work.o + place * 128 + c + k) = make_float4(y[k] * se, y[k + 1] * se, y[k + 2] * se, y[k + 3] * se);
+            for (int k = 0; k < 32; k += 8) {
+#pragma unroll
+              for (int j = k; j < k + 8; ++j) y[j] *= se;
+              store8(work.o + place * 128 + c + k, y + k);
+            }
           }
         }
       }

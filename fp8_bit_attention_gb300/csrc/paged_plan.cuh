@@ -61,7 +61,7 @@ __device__ __forceinline__ int tiles_of(const PagedParams& P, const Seq& s) {
 // out), in blocks: each tile stands for so many more blocks on the line, behind
 // its own, where there is nothing to do.
 template <int BK>
-constexpr int kTileCost = BK < 128 ? 8 : 2;
+constexpr int kTileCost = BK < 128 ? 8 : 4;
 
 // The line is cut at places 2^unit blocks apart; the host takes unit = 0 unless
 // the line could then pass 31 bits.

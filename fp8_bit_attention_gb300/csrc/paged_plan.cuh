@@ -63,6 +63,20 @@ __device__ __forceinline__ int tiles_of(const PagedParams& P, const Seq& s) {
 template <int BK>
 constexpr int kTileCost = BK < 128 ? 8 : 4;
 
+// A cut so near a tile's start or end is moved there: fewer blocks than this are
+// not worth a part of their own, with its partial results and their join.
+template <int BK>
+constexpr int kSnap = BK < 128 ? 4 : 3;
+
+// Where a cut behind `off` of a tile's n blocks falls.  The CTA that ends and
+// the one that begins there both ask.
+template <int BK>
+__device__ __forceinline__ int cut_at(const PagedParams& P, int off, int n) {
+  if (off <= 0) return 0;
+  if (off >= n || (P.unit == 0 && n - off <= kSnap<BK>)) return n;
+  return P.unit == 0 && off <= kSnap<BK> ? 0 : off;
+}
+
 // The line is cut at places 2^unit blocks apart; the host takes unit = 0 unless
 // the line could then pass 31 bits.
 template <int BK>
@@ -247,10 +261,10 @@ struct Walk {
 
   __device__ __forceinline__ void part(const PagedParams& P, int off) {
     const int places = tile_places<BK>(P, t0, t1);
-    k0 = min(t0 + (off << P.unit), t1);
-    k1 = off + len < places ? min(t0 + (off + len << P.unit), t1) : t1;
+    k0 = t0 + cut_at<BK>(P, off << P.unit, t1 - t0);
+    k1 = off + len < places ? t0 + cut_at<BK>(P, off + len << P.unit, t1 - t0) : t1;
     whole = k0 == t0 && k1 == t1;
-    slot = off > 0 ? 0 : 1;
+    slot = k0 > t0 ? 0 : 1;
     len -= places - off;
   }
 
@@ -271,23 +285,25 @@ struct Walk {
   }
 
   __device__ __forceinline__ bool step(const PagedParams& P) {
-    if (len <= 0) return false;
     fresh = false;
-    if (++h >= P.c.heads) {
-      h = 0;
-      fresh = true;
-      if (++i >= nt) {
-        i = 0;
-        do {
-          if (++b >= P.B) return false;                // not reached: len ends first
-          s = load_seq(P, b);
-          nt = tiles_of<R>(P, s);
-        } while (nt == 0);
+    do {
+      if (len <= 0) return false;
+      if (++h >= P.c.heads) {
+        h = 0;
+        fresh = true;
+        if (++i >= nt) {
+          i = 0;
+          do {
+            if (++b >= P.B) return false;              // not reached: len ends first
+            s = load_seq(P, b);
+            nt = tiles_of<R>(P, s);
+          } while (nt == 0);
+        }
+        tile_blocks<R, BK>(P, s, i, t0, t1);
       }
-      tile_blocks<R, BK>(P, s, i, t0, t1);
-    }
-    part(P, 0);
-    return true;                                       // at least one block: places begin with them
+      part(P, 0);
+    } while (k0 >= k1);                                // a last part too short to be one
+    return true;
   }
 };
 
@@ -296,16 +312,21 @@ struct Walk {
 template <int R, int BK>
 __device__ __forceinline__ void write_cut(const PagedParams& P, const Share& sh, const PagedWork& w) {
   CutTile c{0, -1, 0, 0, 0, 0};
-  if (sh.len > 0 && sh.off > 0 && (sh.off << P.unit) < sh.t1 - sh.t0) {
-    const unsigned a = sh.at - sh.off, last = (sh.t1 - sh.t0 - 1) >> P.unit;     // place of the tile's last block
-    c.c0 = a / static_cast<unsigned>(sh.share);
-    if (c.c0 + 1 == static_cast<int>(blockIdx.x)) {
-      c.c1 = (a + last) / static_cast<unsigned>(sh.share);
-      c.q0 = sh.s.q0;
-      c.p0 = sh.i * R;
-      c.rows = min(R, sh.s.ql * P.group - c.p0);
-      c.h = sh.h;
-    }
+  const int n = sh.t1 - sh.t0;
+  auto cut = [&](int off) {                            // is the tile cut behind place `off`?
+    const int k = cut_at<BK>(P, off << P.unit, n);
+    return k > 0 && k < n;
+  };
+  if (sh.len > 0 && sh.off > 0 && cut(sh.off) && !(sh.off > sh.share && cut(sh.off - sh.share))) {
+    c.c0 = blockIdx.x - 1;
+    c.c1 = blockIdx.x;
+    // The last cut: behind the last place that leaves more than kSnap blocks.
+    const int most = P.unit == 0 ? n - 1 - kSnap<BK> : (n - 1) >> P.unit;
+    c.c1 += static_cast<unsigned>(most - sh.off) / static_cast<unsigned>(sh.share);
+    c.q0 = sh.s.q0;
+    c.p0 = sh.i * R;
+    c.rows = min(R, sh.s.ql * P.group - c.p0);
+    c.h = sh.h;
   }
   w.cut[blockIdx.x] = c;
 }

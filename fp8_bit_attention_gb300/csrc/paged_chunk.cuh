@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       // ms for 4096 tokens x 32 heads over 65536 keys).  What the products are
       // told must be in uniform registers: computed per lane, each costs the warp
       // several times its 64 cycles (3.7 ms).
-      uint32_t parts = 0, n = 0, steps[2] = {0, 0};
+      uint32_t parts = 0, n = 0, phase = 0;          // bit t: parity of half t's weights
       bool ok = true, issued = false;
       const uint64_t qd = sw128_desc(smem_addr(sm.q[0][0]));
       while (true) {
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (!ok) break;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            ok = __all_sync(0xFFFFFFFFu, wait(sm.p_full[t][half], steps[t] & 1));
+            ok = __all_sync(0xFFFFFFFFu, wait(sm.p_full[t][half], phase >> t & 1));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             if (half == 0) tc_commit_w(smem_addr(&sm.o_done[t]));
           }
           if (!ok) break;
-          ++steps[t];
+          phase ^= 1u << t;
           if (solo || t == 1) tc_commit_w(smem_addr(&sm.v16_empty[vs]));
           if (i + 2 < total) scores(i + 2);
           else tc_commit_w(smem_addr(&sm.o_full[t]));
@@ -556,29 +556,27 @@ __global__ void __launch_bounds__(kChThreads, 1)
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           // Eight lanes take a key's 128 channels, 16 each: 16 bytes in, 2 x 16
-          // out.  Lanes of the upper 64 channels write their second 16 bytes
-          // first, so that the eight lanes of a store meet different banks.
-          const int c = lane & 7, half = c >> 2;
+          // out.  The lanes of the upper 64 channels work on the neighbouring key
+          // (r ^ 1), so that the eight lanes of a load or store meet all banks.
+          const int c = lane & 7, half = c >> 2, c0 = 2 * (c & 3);
           const int left = kv - (k0 + i) * kChKeys;
           const uint8_t* src = sm.v8[vs];
           uint8_t* dst = sm.v16[os] + half * kChTile;
+          const uint32_t* sv = sm.sc[ss].v;
 #pragma unroll 4
           for (int j = 0; j < 8; ++j) {
-            const int r = 32 * w + 4 * j + (lane >> 3);
-            uint4 x = lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
-            if (r >= left) x = make_uint4(0u, 0u, 0u, 0u);     // behind the sequence's end: anything
-            const uint32_t f = sm.sc[ss].v[r];
+            const int r = 32 * w + 4 * j + ((lane >> 3) ^ half), x7 = (4 * (j & 1) + ((lane >> 3) ^ half)) & 7;
+            uint4 x = lds128(src + r * 128 + ((c ^ x7) << 4));
+            if (left < kChKeys && r >= left) x = make_uint4(0u, 0u, 0u, 0u);     // behind the sequence's end: anything
+            const uint32_t f = sv[r];
             uint4 a, b;
             cvt_e4m3x4_to_f16x2x2(x.x, a.x, a.y);
             cvt_e4m3x4_to_f16x2x2(x.y, a.z, a.w);
             cvt_e4m3x4_to_f16x2x2(x.z, b.x, b.y);
             cvt_e4m3x4_to_f16x2x2(x.w, b.z, b.w);
-            a = make_uint4(hmul2(a.x, f), hmul2(a.y, f), hmul2(a.z, f), hmul2(a.w, f));
-            b = make_uint4(hmul2(b.x, f), hmul2(b.y, f), hmul2(b.z, f), hmul2(b.w, f));
-            const int c0 = 2 * (c & 3);
             uint8_t* row = dst + r * 128;
-            *reinterpret_cast<uint4*>(row + (((c0 + half) ^ (r & 7)) << 4)) = half ? b : a;
-            *reinterpret_cast<uint4*>(row + (((c0 + 1 - half) ^ (r & 7)) << 4)) = half ? a : b;
+            *reinterpret_cast<uint4*>(row + ((c0 ^ x7) << 4)) = make_uint4(hmul2(a.x, f), hmul2(a.y, f), hmul2(a.z, f), hmul2(a.w, f));
+            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ x7) << 4)) = make_uint4(hmul2(b.x, f), hmul2(b.y, f), hmul2(b.z, f), hmul2(b.w, f));
           }
           fence_proxy_async_smem();
           mbar_arrive(smem_addr(&sm.v16_full[os]));

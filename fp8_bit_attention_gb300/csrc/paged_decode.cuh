@@ -75,7 +75,7 @@ struct DecodeSmem {
 
 // CTAs per SM: what the registers of kTiles tiles leave room for.
 template <int kTiles>
-constexpr int kDecodeCtas = kTiles == 1 ? 3 : 2;
+constexpr int kDecodeCtas = kTiles == 1 ? 3 : 2;   // 1 or 2 tiles
 static_assert((sizeof(DecodeSmem) + 1024) * 3 <= 233472, "shared memory per SM");
 
 struct PagedMaps {

@@ -26,7 +26,7 @@ from .api import _DTYPES, _device_of
 _byref = ctypes.byref
 
 
-@dataclasses.dataclass(frozen=True)
+@dataclasses.dataclass(frozen=True, eq=False)
 class KVCache:
     """A cache's memory: E4M3 codes ``k``, ``v`` uint8 [pages, heads, page, 128]
     and E8M0 scale bytes ``k_scale``, ``v_scale`` uint8 [pages, heads, page]

@@ -252,7 +252,7 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
   P.by_group = fast_div(P.group);
   P.by_page = fast_div(P.c.page);
   P.causal = b->causal;
-  P.window = b->window;
+  P.window = b->window < P.most ? b->window : 0;
   const double sm = softmax_scale > 0.0f ? static_cast<double>(softmax_scale) : 1.0 / std::sqrt(128.0);
   P.c2 = static_cast<float>(1.4426950408889634074 * sm);
   P.status = dev->status;

@@ -55,6 +55,25 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Largest magnitude of N BF16 or FP16 pairs; infinity if one is a NaN.
+template <bool kHalf, int N>
+__device__ __forceinline__ float largest_of(const uint32_t* w) {
+  uint32_t m[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t x = w[i] & 0x7FFF7FFFu;
+    if (kHalf) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m[i & 3]) : "r"(x));
+    else asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m[i & 3]) : "r"(x));
+  }
+  float best = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = unpack2<kHalf>(m[i]);
+    best = fmaxf(best, fmaxf(a.x == a.x ? a.x : INFINITY, a.y == a.y ? a.y : INFINITY));
+  }
+  return best;
+}
+
 // A value that is the same in all lanes, by a shuffle: the compiler then keeps it,
 // and what is computed from it alone, in uniform registers.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
@@ -258,7 +277,7 @@ __device__ __forceinline__ void row_range(const PagedParams& P, const Seq& s, in
   hi = s.kv - 1;
   if (P.causal) {
     hi = s.kv - s.ql + i;
-    if (P.window > 0) lo = max(0, hi - P.window + 1);
+    if (P.window > 0 && hi >= P.window) lo = hi - P.window + 1;
   }
 }
 

@@ -212,26 +212,6 @@ __device__ __forceinline__ uint32_t e4m3x4_of_f16(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Largest magnitude of 64 BF16 or FP16 pairs, NaN if one is NaN.
-template <bool kHalf>
-__device__ __forceinline__ float row_amax(const uint32_t* w) {
-  uint32_t m[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 64; ++i) {
-    const uint32_t x = w[i] & 0x7FFF7FFFu;
-    if (kHalf) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m[i & 3]) : "r"(x));
-    else asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m[i & 3]) : "r"(x));
-  }
-  float best = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = unpack2<kHalf>(m[i]);
-    // (A NaN counts as an infinity: fmaxf would drop it.)
-    best = fmaxf(best, fmaxf(a.x == a.x ? a.x : INFINITY, a.y == a.y ? a.y : INFINITY));
-  }
-  return best;
-}
-
 __device__ __forceinline__ ChunkPart uniform(const ChunkPart& x) {
   return {uniform(x.more), uniform(x.b),    uniform(x.q0),   uniform(x.ql),     uniform(x.kv),     uniform(x.p0),  uniform(x.rows),
           uniform(x.h),    uniform(x.k0),   uniform(x.nblk), uniform(x.all_lo), uniform(x.all_hi), uniform(x.slot)};
@@ -630,7 +610,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           for (int i = 0; i < 16; ++i) q[i] = __ldg(src + i);
         }
         const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
-        const uint32_t e = scale_byte(row_amax<kHalf>(w));
+        const uint32_t e = scale_byte(largest_of<kHalf, 64>(w));
         const float mul = e == 255u ? 0.0f : inverse_scale(e);
         const uint64_t mul2 = pack_f2(mul, mul);
         rowf *= scale_value(e);                    // NaN for a row that is not finite: so are its results

@@ -299,16 +299,11 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
         qf[n][2 * i + 1][0] = x[n][i].z;
         qf[n][2 * i + 1][1] = x[n][i].w;
       }
+      float amax = largest_of<kHalf, 16>(&qf[n][0][0]);
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       if (!kHalf) {
         // BF16 to FP16: the row's largest magnitude goes to [2^14, 2^15).
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 a = unpack2<false>(qf[n][i / 2][i % 2]);
-          amax = fmaxf(amax, fmaxf(fabsf(a.x), fabsf(a.y)));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
         const uint32_t up = min(268u - (__float_as_uint(amax) >> 23), 254u);       // 2^(up - 127)
         const float mul = __uint_as_float(up << 23);
 #pragma unroll
@@ -318,6 +313,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
         }
         f *= inverse_scale(up);
       }
+      if (amax == INFINITY) f = __uint_as_float(0x7FFFFFFFu);      // a row that is not finite: NaN, whatever its scores
 #pragma unroll
       for (int j = 0; j < 2; ++j) rowf[n][j] = __shfl_sync(0xFFFFFFFFu, f, (2 * t + j) * 4);
     }

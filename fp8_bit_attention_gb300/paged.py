@@ -7,9 +7,11 @@ A serving loop writes each step's keys and values and attends with its queries::
     kv_cache_write(cache, k, v, slots)                  # k, v [T, heads, 128]
     o = paged_attention(q, cache, page_table, kv_lens, cu_q=cu_q, max_q=n)
 
-Every call is asynchronous on the current stream (or ``stream``), reads no
-device value on the host, and can be captured into a CUDA graph: lengths,
-slots and page tables may change between replays.
+Every call is asynchronous on the current stream (or ``stream``) and reads no
+device value on the host, so that a step can be captured into a CUDA graph
+(after one eager call, which loads the library and sets its per-device state)
+and lengths, slots and page tables may change between replays.  The calls have
+no gradient.
 """
 from __future__ import annotations
 
@@ -24,6 +26,7 @@ from ._abi import check, lib
 from .api import _DTYPES, _device_of
 
 _byref = ctypes.byref
+_INT32_MAX = 2 ** 31 - 1
 
 
 @dataclasses.dataclass(frozen=True, eq=False)
@@ -190,7 +193,7 @@ def _batch(q, cache, page_table, kv_lens, cu_q, max_q, causal, window):
             raise ValueError("max_q needs cu_q")
         cu, most = None, 1
     else:
-        cu, most = _ints(cu_q, (n + 1,), "cu_q"), int(max_q or 0)
+        cu, most = _ints(cu_q, (n + 1,), "cu_q"), min(int(max_q or 0), _INT32_MAX)
     if most < 0:
         raise ValueError("max_q must not be negative")
     if window is not None and (window < 1 or not causal):
@@ -199,7 +202,7 @@ def _batch(q, cache, page_table, kv_lens, cu_q, max_q, causal, window):
         raise ValueError(f"{q.shape[1]} query heads over {cache.heads} KV heads")
     stride = page_table.stride(0) if n > 1 else max(page_table.stride(0), page_table.shape[1])
     return _abi.OvcPagedBatch(n, page_table.data_ptr(), stride, page_table.shape[1], lens, cu, most, int(bool(causal)),
-                              int(window or 0))
+                              min(int(window or 0), _INT32_MAX))
 
 
 def paged_attention_workspace_bytes(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, *,

@@ -308,6 +308,67 @@ def test_nan_queries(q_len):
     assert torch.equal(torch.isnan(o).any(-1), want) and torch.equal(torch.isnan(o).all(-1), want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("q_len", [1, 100])
+def test_infinite_queries(q_len, dtype):
+    """Also where every score would be minus infinity."""
+    c = Case([q_len], [200], 1, 4, 16, dtype, seed=18)
+    c.k[:, :, 5] = -1.0
+    ovc.kv_cache_write(c.cache, c.k, c.v, c.slots)
+    c.q[0, 1, 5] = math.inf
+    c.q[q_len - 1, 2, 5] = -math.inf
+    o, lse = c.run(return_lse=True)
+    want = torch.zeros(o.shape[:2], dtype=torch.bool, device="cuda")
+    want[0, 1] = want[q_len - 1, 2] = True
+    assert torch.equal(torch.isnan(o).all(-1), want) and torch.equal(torch.isnan(o).any(-1), want)
+    assert torch.equal(torch.isnan(lse), want)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 10 ** 12])
+def test_windows_beyond_every_length(window):
+    c = Case([300, 2, 40], [250, 900, 40], 1, 2, 16, seed=19)     # the first: more rows than tokens
+    assert torch.equal(c.run(window=window), c.run())
+    c.check(c.run(window=window))
+
+
+@pytest.mark.parametrize("q_len", [1, 30])
+def test_many_short_sequences(q_len):
+    """More sequences than a CTA has threads, some without rows or tokens."""
+    n = 700
+    q_lens = [q_len if b % 7 else 0 for b in range(n)]
+    kv_lens = [0 if b % 11 == 0 else max(q_lens[b], (b * 37) % 150) for b in range(n)]
+    c = Case(q_lens, kv_lens, 2, 2, 16, seed=20)
+    o, lse = c.run(return_lse=True)
+    c.check(o, lse)
+
+
+@pytest.mark.parametrize("q_len", [1, 64])
+def test_page_tables_far_wider_than_the_sequences(q_len):
+    """2^31 tokens' worth of page table, of which the lengths use a little."""
+    c = Case([q_len] * 2, [3000, 500], 8, 2, 16, seed=21)
+    wide = torch.empty((2, 1 << 27), dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    o = ovc.paged_attention(c.q, c.cache, wide, c.lens, cu_q=c.cu, max_q=q_len)
+    c.check(o)
+
+
+def test_calls_on_two_streams_at_once():
+    cases = [Case([q] * 3, [900, 5000, 77], 2, 4, 32, seed=22 + q) for q in (1, 50)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                ovc.kv_cache_write(c.cache, c.k, c.v, c.slots)
+                got[i].append(c.run())
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(w, o) for o in outs)
+    assert ovc.device_status() == 0
+
+
 @pytest.mark.parametrize("q_len", [1, 90])
 def test_rows_of_no_sequence_keep_what_they_held(q_len):
     c = Case([q_len, q_len], [200, 60], 2, 2, 16, seed=8)

@@ -37,6 +37,17 @@ ovc_status rows_ok(const ovc_rows* r) {
   return r->dtype == OVC_BF16 || r->dtype == OVC_FP16 ? OVC_OK : OVC_ERR_UNSUPPORTED;
 }
 
+// An output's rows: as above, and no two of them overlap.
+ovc_status out_ok(const ovc_rows* r) {
+  const ovc_status st = rows_ok(r);
+  if (st != OVC_OK) return st;
+  const bool t_inner = r->T == 1 || (r->H > 1 && r->stride_t < r->stride_h);
+  const int64_t inner = t_inner ? r->stride_t : r->stride_h, outer = t_inner ? r->stride_h : r->stride_t;
+  const int64_t n = t_inner ? r->T : r->H, m = t_inner ? r->H : r->T;
+  if (n > 1 && inner < 128) return OVC_ERR_INVALID_ARG;
+  return m > 1 && (outer < 128 || (n > 1 && (outer - 128) / (n - 1) < inner)) ? OVC_ERR_INVALID_ARG : OVC_OK;
+}
+
 CacheView view(const ovc_kv_cache* c) {
   return {c->k, c->v, c->k_scale, c->v_scale, static_cast<int32_t>(c->pages), static_cast<int32_t>(c->heads),
           static_cast<int32_t>(c->page)};
@@ -46,12 +57,13 @@ RowsView view(const ovc_rows* r) { return {r->ptr, r->stride_t, r->stride_h}; }
 
 ovc_status launched() { return cudaGetLastError() == cudaSuccess ? OVC_OK : OVC_ERR_CUDA; }
 
-// Arguments that ovc_kv_write and ovc_kv_read share.
-ovc_status cache_call_ok(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows* v, const int32_t* slots) {
+// Arguments that ovc_kv_write and ovc_kv_read (with its check of the rows) share.
+ovc_status cache_call_ok(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows* v, const int32_t* slots,
+                         ovc_status (*ok)(const ovc_rows*)) {
   if (!cache_ok(c) || !at4(slots)) return OVC_ERR_INVALID_ARG;
-  ovc_status st = rows_ok(k);
+  ovc_status st = ok(k);
   if (st != OVC_OK) return st;
-  st = rows_ok(v);
+  st = ok(v);
   if (st != OVC_OK) return st;
   if (k->T != v->T || k->H != c->heads || v->H != c->heads || k->dtype != v->dtype) return OVC_ERR_INVALID_ARG;
   return OVC_OK;
@@ -190,7 +202,7 @@ extern "C" {
 
 ovc_status ovc_kv_write(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows* v, const int32_t* slots,
                         void* stream) {
-  ovc_status st = cache_call_ok(c, k, v, slots);
+  ovc_status st = cache_call_ok(c, k, v, slots, rows_ok);
   if (st != OVC_OK) return st;
   DeviceState* dev = nullptr;
   st = device_state(&dev);
@@ -205,7 +217,7 @@ ovc_status ovc_kv_write(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows
 
 ovc_status ovc_kv_read(const ovc_kv_cache* c, const int32_t* slots, const ovc_rows* k, const ovc_rows* v,
                        void* stream) {
-  ovc_status st = cache_call_ok(c, k, v, slots);
+  ovc_status st = cache_call_ok(c, k, v, slots, out_ok);
   if (st != OVC_OK) return st;
   DeviceState* dev = nullptr;
   st = device_state(&dev);
@@ -227,7 +239,7 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
                                size_t workspace_bytes, void* stream) {
   ovc_status st = paged_ok(q, c, b);
   if (st != OVC_OK) return st;
-  st = rows_ok(o);
+  st = out_ok(o);
   if (st != OVC_OK) return st;
   if (o->T != q->T || o->H != q->H || o->dtype != OVC_BF16 || (lse && !at4(lse))) return OVC_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return OVC_ERR_INVALID_ARG;

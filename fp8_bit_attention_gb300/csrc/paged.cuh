@@ -253,7 +253,7 @@ struct PagedParams {
 // arrays hold, the rows lie within q and the tokens within the page table.
 struct Seq {
   int q0, ql, kv;
-  bool bad;
+  int bad;                  // 1: something was cut off; 2: cu_q descends here
 };
 
 __device__ __forceinline__ Seq load_seq(const PagedParams& P, int b) {
@@ -264,7 +264,7 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& P, int b) {
     e = __ldg(P.cu_q + b + 1);
   }
   const int kv = __ldg(P.kv_lens + b);
-  s.bad = a < 0 || e < a || e > P.T || kv < 0 || kv > P.most;
+  s.bad = e < a ? 2 : a < 0 || e > P.T || kv < 0 || kv > P.most;
   s.q0 = min(max(a, 0), P.T);
   s.ql = min(max(e, s.q0), P.T) - s.q0;
   s.kv = min(max(kv, 0), P.most);

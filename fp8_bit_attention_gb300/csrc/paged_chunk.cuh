@@ -613,7 +613,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const uint32_t e = scale_byte(largest_of<kHalf, 64>(w));
         const float mul = e == 255u ? 0.0f : inverse_scale(e);
         const uint64_t mul2 = pack_f2(mul, mul);
-        rowf *= scale_value(e);                    // NaN for a row that is not finite: so are its results
+        // NaN for a row that is not finite: so are its results, if it sees a key.
+        if (e != 255u || lo <= hi) rowf *= scale_value(e);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t out[Sh::kQParts][4];

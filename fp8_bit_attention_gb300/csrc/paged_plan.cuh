@@ -99,9 +99,10 @@ struct PlanSmem {
   Share found;
 };
 
-// Inclusive sum of w over threads 0 .. N - 1 of the CTA, and all of it.
+// Inclusive sum of w over threads 0 .. N - 1 of the CTA, and all of it; `any`
+// becomes true if it is so in any thread.
 template <int N>
-__device__ __forceinline__ int cta_scan(int w, PlanSmem& sm, int& all) {
+__device__ __forceinline__ int cta_scan(int w, PlanSmem& sm, int& all, bool& any) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int v = w;
 #pragma unroll
@@ -118,7 +119,7 @@ __device__ __forceinline__ int cta_scan(int w, PlanSmem& sm, int& all) {
     if (k < warp) v += x;
     all += x;
   }
-  __syncthreads();
+  any = __syncthreads_or(any);
   return v;
 }
 
@@ -130,6 +131,7 @@ __device__ Share plan_share(const PagedParams& P, PlanSmem& sm, int min_share) {
   constexpr int N = kThreads < 160 ? kThreads : 160;
   const int tid = threadIdx.x, lane = tid & 31;
   // Places of sequence b0 + tid, all heads.
+  bool descends = false;
   auto places = [&](int b0, bool first) {
     const int n = min(N, P.B - b0);
     int w = 0;
@@ -137,6 +139,7 @@ __device__ Share plan_share(const PagedParams& P, PlanSmem& sm, int min_share) {
       if (tid < n) {
         const Seq s = load_seq(P, b0 + tid);
         if (s.bad && first && blockIdx.x == 0) atomicOr(P.status, kPagedBadIndex);
+        descends |= s.bad == 2;
         const int nt = tiles_of<R>(P, s);
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
@@ -150,6 +153,7 @@ __device__ Share plan_share(const PagedParams& P, PlanSmem& sm, int min_share) {
       for (int j = tid / 32; j < n; j += kThreads / 32) {
         const Seq s = load_seq(P, b0 + j);
         if (s.bad && first && blockIdx.x == 0 && lane == 0) atomicOr(P.status, kPagedBadIndex);
+        descends |= s.bad == 2;
         const int nt = tiles_of<R>(P, s);
         int x = 0;
 #pragma unroll 1
@@ -172,9 +176,12 @@ __device__ Share plan_share(const PagedParams& P, PlanSmem& sm, int min_share) {
 #pragma unroll 1
   for (int b0 = 0; b0 < P.B; b0 += N) {
     w = places(b0, true);
-    v = cta_scan<N>(w, sm, all);
+    v = cta_scan<N>(w, sm, all, descends);
     total += all;
   }
+  // Where cu_q descends its sequences overlap, and their places may pass the 31
+  // bits that the host saw to: nothing of the batch is done then.
+  if (descends) total = 0;
   const int share = max(min_share, static_cast<int>((static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x));
   const long long at = static_cast<long long>(share) * blockIdx.x;
   if (at >= total) {
@@ -192,7 +199,7 @@ __device__ Share plan_share(const PagedParams& P, PlanSmem& sm, int min_share) {
   for (int b0 = 0; b0 < P.B; b0 += N) {
     if (P.B > N) {
       w = places(b0, false);
-      v = cta_scan<N>(w, sm, all);
+      v = cta_scan<N>(w, sm, all, descends);
     }
     const int rem = static_cast<int>(at) - (base + v - w);
     if (tid < N && rem >= 0 && rem < w) {              // one thread of one chunk

@@ -234,12 +234,17 @@ def paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, k
     heads] natural log-sum-exp of the scaled scores).  A row that sees no key
     gives 0 and -inf.  Rows of no sequence are left as they were (in a new
     output: unset).  Indices outside the cache, the table or q are cut off and
-    reported by :func:`device_status` (7)."""
+    reported by :func:`device_status` (7); where ``cu_q`` descends, no row is
+    written.  ``out`` must not overlap q.  ``workspace`` (uint8, 256-byte aligned,
+    :func:`paged_attention_workspace_bytes`) is allocated if not given; calls,
+    or captured graphs, that share one must not run at the same time."""
     dev = _device(q, cache.k, page_table, kv_lens, cu_q, out, workspace, stream=stream)
     rq = _rows(q, "q")
     b = _batch(q, cache, page_table, kv_lens, cu_q, max_q, causal, window)
     if out is not None and (out.shape != q.shape or out.dtype != torch.bfloat16):
         raise ValueError("out must be a bfloat16 tensor shaped like q")
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor")
 
     def run(s):
         o = out if out is not None else torch.empty_like(q, dtype=torch.bfloat16, memory_format=torch.contiguous_format)

@@ -433,8 +433,9 @@ int32_t ovc_host_chunk_plan(int64_t H, int64_t tiles_per_head, int32_t sms, int3
  * scaling is exact in every type, and a code times its scale is a BF16 value.
  * A vector that holds a NaN or an infinity gets e = 255 and zero codes; it
  * reads back as NaN, and attention gives NaN in the rows that see it and in no
- * others.  Slots never written may hold anything: no call reads them as long
- * as the lengths given stay within what was written. */
+ * others.  Slots never written may hold anything: no call uses them as long
+ * as the lengths given stay within what was written.  A written slot holds no
+ * NaN code (0x7F, 0xFF): a cache filled by other means says NaN by its scale. */
 typedef struct {
   int64_t pages, heads, page;
   uint8_t* k;
@@ -462,14 +463,15 @@ ovc_status ovc_kv_write(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows
 
 /* Read tokens back: rows t of k and v become the values of slot slots[t] in
  * the rows' dtype (exact in BF16 and FP16 within their ranges, otherwise to
- * nearest even).  A negative slot gives zeros; so does one beyond the cache,
+ * nearest even).  No two rows written may overlap.  A negative slot gives zeros; so does one beyond the cache,
  * which is reported as for ovc_kv_write. */
 ovc_status ovc_kv_read(const ovc_kv_cache* c, const int32_t* slots, const ovc_rows* k, const ovc_rows* v,
                        void* stream);
 
 /* A batch of B sequences over a cache.  All arrays are int32 on the device.
- *   page_table  [B, table_width], row stride table_stride: the pages of each
- *               sequence in order; only its first ceil(kv_len/page) are read
+ *   page_table  [B, table_width], row stride table_stride >= table_width: the
+ *               pages of each sequence in order; only its first
+ *               ceil(kv_len/page) are read
  *   kv_lens     [B] tokens in the cache, the new ones among them
  *   cu_q        [B+1] first query row of each sequence (ascending, from 0 on),
  *               or NULL: one row each.  Sequence b's rows are its last
@@ -483,7 +485,8 @@ ovc_status ovc_kv_read(const ovc_kv_cache* c, const int32_t* slots, const ovc_ro
  * -inf as its log-sum.  Rows of no sequence (before cu_q[0], from cu_q[B] on)
  * are left as they were.  Lengths beyond the page table, rows beyond q, and
  * pages beyond the cache among those read are cut off, the affected sequences'
- * rows unspecified, and reported as OVC_ERR_BAD_INDEX. */
+ * rows unspecified, and reported as OVC_ERR_BAD_INDEX; where cu_q descends, no
+ * row of the batch is written. */
 typedef struct {
   int64_t B;
   const int32_t* page_table;
@@ -501,9 +504,10 @@ size_t ovc_paged_attention_workspace_bytes(const ovc_rows* q, const ovc_kv_cache
 
 /* o[t,h] = softmax(q[t,h] . K * softmax_scale) V over the keys that row t sees,
  * KV head h / (q->H / c->heads); q->H is a multiple of c->heads.  o is BF16,
- * shaped like q.  lse, if not NULL, receives the natural log-sum-exp of the
+ * shaped like q; its rows overlap neither each other nor q's.  lse, if not NULL, receives the natural log-sum-exp of the
  * scaled scores, FP32 [T, H] contiguous.  softmax_scale <= 0 selects
- * 1/sqrt(128).  A query row that holds a NaN or an infinity gives NaN.
+ * 1/sqrt(128).  A query row that holds a NaN or an infinity gives NaN, unless
+ * it sees no key.
  * Long sequences are split over the GPU and joined from the workspace
  * (256-byte aligned); calls that share it must not overlap.  The way of
  * splitting depends on all lengths of the batch: the last bits of a sequence's

@@ -324,6 +324,32 @@ def test_infinite_queries(q_len, dtype):
     assert torch.equal(torch.isnan(lse), want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("q_len", [4, 100])
+def test_rows_without_keys_are_zero_whatever_they_hold(q_len, dtype):
+    c = Case([q_len, q_len], [q_len - 3, 0], 1, 4, 16, dtype, seed=24)
+    c.q[:3] = math.nan
+    c.q[q_len:] = math.inf
+    o, lse = c.run(return_lse=True)
+    empty = torch.cat([torch.arange(3), torch.arange(q_len, 2 * q_len)]).cuda()
+    assert (o[empty] == 0).all() and (lse[empty] == -math.inf).all()
+    assert torch.isfinite(o[3:q_len]).all() and torch.isfinite(lse[3:q_len]).all()
+
+
+@pytest.mark.parametrize("max_q", [1, 64])
+def test_descending_row_starts_write_nothing(max_q):
+    """Taken one by one, such sequences have 200 times q's rows, and work beyond 2^31 places."""
+    c = Case([2000], [3000], 8, 8, 1024, seed=25)
+    n = 400
+    cu = _i32([2000 * (i % 2) for i in range(n + 1)])
+    table = torch.zeros((n, 2048), dtype=torch.int32, device="cuda")
+    out = torch.full(c.q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lens = _i32([2 ** 21] * n)
+    ovc.paged_attention(c.q, c.cache, table, lens, cu_q=cu, max_q=max_q, out=out)
+    assert ovc.device_status() == BAD_INDEX and ovc.device_status() == 0
+    assert (out == 7.0).all()
+
+
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 10 ** 12])
 def test_windows_beyond_every_length(window):
     c = Case([300, 2, 40], [250, 900, 40], 1, 2, 16, seed=19)     # the first: more rows than tokens
@@ -538,7 +564,8 @@ def test_refusals():
         dict(q=q.float()), dict(q=q[:, :3]), dict(q=q[..., :64]), dict(q=q[:, :, ::2]), dict(q=q.cpu()), dict(table=t.long()),
         dict(table=t[:1]), dict(n=n.long()), dict(n=n[:1]), dict(cu=cu[:2]), dict(cu=cu.long()), dict(cu=None), dict(window=0),
         dict(window=3, causal=False), dict(max_q=-1), dict(out=torch.empty_like(q[:2])), dict(out=torch.empty_like(q).half()),
-        dict(out=torch.empty_like(q, device="cpu")),
+        dict(out=torch.empty_like(q, device="cpu")), dict(workspace=torch.empty(1 << 20, device="cuda")),
+        dict(workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 28)),
     ]
     for kw in bad:
         a = dict(q=q, table=t, n=n, cu=cu) | kw
@@ -555,6 +582,10 @@ def test_refusals():
         ovc.kv_cache_read(c.cache, c.slots.view(1, -1))
     with pytest.raises(ValueError):
         ovc.kv_cache_read(c.cache, c.slots, out=(k, k[:2]))
+    with pytest.raises(ovc.OvcError):
+        ovc.kv_cache_read(c.cache, c.slots, out=(k.clone(), k[:1].clone().expand_as(k)))
+    with pytest.raises(ovc.OvcError):
+        ovc.paged_attention(q, c.cache, t, n, cu_q=cu, out=torch.empty_like(q[:1]).expand_as(q))
     for shape in ((2, 1, 24), (2, 1, 2048), (0, 1, 16), (1 << 27, 1, 16)):
         with pytest.raises((ValueError, RuntimeError)):
             ovc.KVCache(*(torch.empty(1, dtype=torch.uint8, device="cuda").expand(*s) for s in (shape + (128,), shape + (128,), shape, shape)))

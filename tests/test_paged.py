@@ -82,6 +82,21 @@ def test_bad_rows_are_refused(lib, bad):
         assert lib.ovc_paged_attention(R(q), R(c), R(b), 0.0, R(o), None, B(0x100000), 1 << 30, None) == _abi.OVC_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("strides, ok", [((0, 128), False), ((256, 0), False), ((128, 128), False), ((256, 128), True),
+                                         ((248, 128), False), ((256, 120), False), ((128, 5 * 128), True),
+                                         ((128, 4 * 128), False), ((1 << 40, 136), True), ((136, 1 << 40), True)], ids=str)
+def test_outputs_that_overlap_are_refused(lib, strides, ok):
+    """5 tokens, 2 heads; the same strides are fine to read from."""
+    c, r, o, b = _cache(), _rows(T=5), _rows(T=5, stride_t=strides[0], stride_h=strides[1]), _batch()
+    if not ok or not torch.cuda.is_available():
+        st = lib.ovc_kv_read(R(c), B(0x90000), R(o), R(o), None)
+        assert (st != _abi.OVC_ERR_INVALID_ARG) == ok
+        st = lib.ovc_paged_attention(R(r), R(c), R(b), 0.0, R(o), None, B(0x100000), 1 << 30, None)
+        assert (st != _abi.OVC_ERR_INVALID_ARG) == ok
+    if not torch.cuda.is_available():
+        assert lib.ovc_kv_write(R(c), R(o), R(o), B(0x90000), None) != _abi.OVC_ERR_INVALID_ARG
+
+
 def test_mismatched_arguments_are_refused(lib):
     c, r, b = _cache(), _rows(), _batch()
     bad = _abi.OVC_ERR_INVALID_ARG

@@ -48,6 +48,10 @@ ovc_status out_ok(const ovc_rows* r) {
   return m > 1 && (outer < 128 || (n > 1 && (outer - 128) / (n - 1) < inner)) ? OVC_ERR_INVALID_ARG : OVC_OK;
 }
 
+bool at32(const ovc_rows* r) {
+  return (reinterpret_cast<uintptr_t>(r->ptr) & 31u) == 0 && r->stride_t % 16 == 0 && r->stride_h % 16 == 0;
+}
+
 CacheView view(const ovc_kv_cache* c) {
   return {c->k, c->v, c->k_scale, c->v_scale, static_cast<int32_t>(c->pages), static_cast<int32_t>(c->heads),
           static_cast<int32_t>(c->page)};
@@ -251,6 +255,8 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
   P.c = view(c);
   P.q = view(q);
   P.o = view(o);
+  P.q32 = at32(q);
+  P.o32 = at32(o);
   P.lse = lse;
   P.table = b->page_table;
   P.table_stride = b->table_stride;

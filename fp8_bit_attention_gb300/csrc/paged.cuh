@@ -78,6 +78,18 @@ __device__ __forceinline__ float largest_of(const uint32_t* w) {
 // and what is computed from it alone, in uniform registers.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 
+// mbar_wait (ptx.cuh) in little code: the attention kernels wait in many places,
+// their warps run through different code at the same time, and what does not fit
+// the instruction caches is what they wait for most.
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int* abort) {
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if (*abort || globaltimer_ns() - t0 > timeout_ns) return false;
+  return true;
+}
+
 struct CacheView {
   uint8_t* k;
   uint8_t* v;
@@ -246,6 +258,7 @@ struct PagedParams {
   int32_t most;             // tokens that a page table row holds
   int32_t unit;             // log2 of the key blocks between the places where work may be cut
   float c2;                 // softmax_scale * log2(e)
+  int32_t q32, o32;         // rows of q, of o lie at multiples of 32 bytes
   unsigned int* status;
 };
 

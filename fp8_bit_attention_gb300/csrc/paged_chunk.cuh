@@ -187,13 +187,17 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t pair) {
   return unpack2<true>(h);
 }
 
-// 32 bytes in one store (a whole sector): the address is a multiple of 32.
-__device__ __forceinline__ void store8(float* to, const float* y) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(to)), "f"(y[0]), "f"(y[1]),
-               "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+// 32 bytes in one load or store (a whole sector): the address is a multiple of 32.
+__device__ __forceinline__ void load8(uint32_t* w, const void* from) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(__cvta_generic_to_global(from)));
+}
+__device__ __forceinline__ void store8(void* to, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(to)), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem_base);
 
-  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return mbar_wait(smem_addr(&bar), parity, M.timeout_ns, abort_flag); };
+  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return paged_wait(smem_addr(&bar), parity, M.timeout_ns, abort_flag); };
   auto give_up = [&]() {
     if (!*abort_flag) atomicOr(P.status, 1u);
     *abort_flag = 1;
@@ -287,11 +291,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
     regs_dec<kChOtherRegs>();
     if (warp == 12) {
       // -------------------------------------------------- the share, K and V
-      Walk<kChRows, kChKeys> w;
+      Walk<kChRows, kChKeys> w(P, share);
       uint32_t parts = 0, n = 0, nv = 0;           // blocks whose K, V were loaded
       bool ok = true;
       const int boxes = kChKeys / M.box;
-      for (bool more = w.start(P, share);; more = w.step(P)) {
+      while (true) {
+        const bool more = w.step(P);
         const uint32_t d = parts % kChParts;
         if (parts >= kChParts) ok = __all_sync(0xFFFFFFFFu, wait(sm.part_empty[d], (parts / kChParts - 1) & 1));
         if (!ok) break;
@@ -353,9 +358,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
         give_up();
         // The copies in flight end by themselves; shared memory must outlive them.
         for (uint32_t i = n > Sh::kK ? n - Sh::kK : 0; i < n; ++i)
-          mbar_wait(smem_addr(&sm.k_full[i % Sh::kK]), (i / Sh::kK) & 1, 4000000000ull, &sm.zero);
+          paged_wait(smem_addr(&sm.k_full[i % Sh::kK]), (i / Sh::kK) & 1, 4000000000ull, &sm.zero);
         for (uint32_t i = nv > Sh::kV ? nv - Sh::kV : 0; i < nv; ++i)
-          mbar_wait(smem_addr(&sm.v8_full[i % Sh::kV]), (i / Sh::kV) & 1, 4000000000ull, &sm.zero);
+          paged_wait(smem_addr(&sm.v8_full[i % Sh::kV]), (i / Sh::kV) & 1, 4000000000ull, &sm.zero);
       }
     } else if (warp == 13) {
       // --------------------------------------------------------- the products
@@ -399,6 +404,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (solo || t == 1) tc_commit_w(smem_addr(&sm.k_empty[ks]));
           issued = true;
         };
+#pragma unroll 1
         for (int i = 0; i < 2 && i < total; ++i) {
           wait_k(i);
           if (!ok) break;
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       if (issued) {
         // Every product issued so far has completed once this barrier flips.
         tc_commit_w(smem_addr(&sm.drain));
-        mbar_wait(smem_addr(&sm.drain), 0, 4000000000ull, &sm.zero);
+        paged_wait(smem_addr(&sm.drain), 0, 4000000000ull, &sm.zero);
       }
     } else if (warp == 14) {
       // ----------------------------------------------------------- the scales
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           const uint8_t* src = sm.v8[vs];
           uint8_t* dst = sm.v16[os] + half * kChTile;
           const uint32_t* sv = sm.sc[ss].v;
-#pragma unroll 4
+#pragma unroll 2
           for (int j = 0; j < 8; ++j) {
             const int r = 32 * w + 4 * j + ((lane >> 3) ^ half), x7 = (4 * (j & 1) + ((lane >> 3) ^ half)) & 7;
             uint4 x = lds128(src + r * 128 + ((c ^ x7) << 4));
@@ -601,15 +607,25 @@ __global__ void __launch_bounds__(kChThreads, 1)
       // Q's row in E4M3 parts, scaled by a power of two to at most 448.
       float rowf = P.c2;
       if (!solo || t == 0) {
-        uint4 q[16];
+        uint32_t w[64];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 64; ++i) w[i] = 0u;
         if (here) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q.ptr) + (s.q0 + tok) * P.q.st + hq * P.q.sh);
+          const uint16_t* src = static_cast<const uint16_t*>(P.q.ptr) + (s.q0 + tok) * P.q.st + hq * P.q.sh;
+          if (P.q32) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) q[i] = __ldg(src + i);
+            for (int i = 0; i < 8; ++i) load8(w + 8 * i, src + 16 * i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint4 y = __ldg(reinterpret_cast<const uint4*>(src) + i);
+              w[4 * i] = y.x;
+              w[4 * i + 1] = y.y;
+              w[4 * i + 2] = y.z;
+              w[4 * i + 3] = y.w;
+            }
+          }
         }
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
         const uint32_t e = scale_byte(largest_of<kHalf, 64>(w));
         const float mul = e == 255u ? 0.0f : inverse_scale(e);
         const uint64_t mul2 = pack_f2(mul, mul);
@@ -865,17 +881,22 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         if (here) {
           if (x.slot < 0) {
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 32; k += 8)
-              *reinterpret_cast<uint4*>(orow + c + k) =
-                  make_uint4(pack2<false>(y[k] * se, y[k + 1] * se), pack2<false>(y[k + 2] * se, y[k + 3] * se),
-                             pack2<false>(y[k + 4] * se, y[k + 5] * se), pack2<false>(y[k + 6] * se, y[k + 7] * se));
+            for (int k = 0; k < 16; ++k) w[k] = pack2<false>(y[2 * k] * se, y[2 * k + 1] * se);
+            if (P.o32) {
+              store8(orow + c, w);
+              store8(orow + c + 16, w + 8);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) *reinterpret_cast<uint4*>(orow + c + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+            }
           } else {
 #pragma unroll
             for (int k = 0; k < 32; k += 8) {
 #pragma unroll
-              for (int j = k; j < k + 8; ++j) y[j] *= se;
-              store8(work.o + place * 128 + c + k, y + k);
+              for (int j = 0; j < 8; ++j) o[k + j] = __float_as_uint(y[k + j] * se);
+              store8(work.o + place * 128 + c + k, o + k);
             }
           }
         }

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
   // A wait that ran out: every role goes on without waiting or loading, works on
   // whatever is there, and ends.
   auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
-    if (mbar_wait(smem_addr(&bar), parity, M.timeout_ns, abort_flag)) return true;
+    if (paged_wait(smem_addr(&bar), parity, M.timeout_ns, abort_flag)) return true;
     if (!*abort_flag) atomicOr(P.status, 1u);
     *abort_flag = 1;
     return false;
@@ -180,10 +180,11 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
 
   if (warp == kDecWarps) {
     // -------------------------------------------------------------- loading
-    Walk<R, kDecKeys> w;
+    Walk<R, kDecKeys> w(P, share);
     uint32_t parts = 0;
     uint32_t issued = 0;                           // blocks of lane's ring (lanes 0 .. kDecWarps - 1)
-    for (bool more = w.start(P, share);; more = w.step(P)) {
+    while (true) {
+      const bool more = w.step(P);
       // Describe the part.
       const uint32_t d = parts % kDecParts;
       if (parts >= kDecParts && !__all_sync(0xFFFFFFFFu, wait(sm.part_empty[d], (parts / kDecParts - 1) & 1))) break;
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
     // the CTA's shared memory must outlive them.
     if (*abort_flag && lane < kDecWarps)
       for (uint32_t n = issued > kDecStages ? issued - kDecStages : 0; n < issued; ++n)
-        mbar_wait(smem_addr(&sm.full[lane][n % kDecStages]), (n / kDecStages) & 1, 4000000000ull, &sm.zero);
+        paged_wait(smem_addr(&sm.full[lane][n % kDecStages]), (n / kDecStages) & 1, 4000000000ull, &sm.zero);
     return;
   }
 

@@ -260,7 +260,6 @@ struct Walk {
   int b, i, h;       // the tile
   int t0, t1;        // its key blocks
   int k0, k1;        // those in this share
-  bool fresh;        // b or i changed with the last step
   bool whole;        // the tile lies in this share alone
   int slot;          // else: which of the CTA's two partial results
   int nt;
@@ -275,40 +274,33 @@ struct Walk {
     len -= places - off;
   }
 
-  // Stands on the first part that has blocks; false if there is none.
-  __device__ __forceinline__ bool start(const PagedParams& P, const Share& sh) {
-    b = sh.b;
-    i = sh.i;
-    h = sh.h;
-    len = sh.len;
-    s = sh.s;
-    nt = tiles_of<R>(P, s);
-    t0 = sh.t0;
-    t1 = sh.t1;
-    part(P, sh.off);
-    if (k0 >= k1 && !step(P)) return false;
-    fresh = true;
-    return true;
-  }
+  int off;           // the place that the next part starts at; negative: in the next tile
 
+  __device__ __forceinline__ Walk(const PagedParams& P, const Share& sh)
+      : s(sh.s), b(sh.b), i(sh.i), h(sh.h), t0(sh.t0), t1(sh.t1), nt(tiles_of<R>(P, sh.s)), len(sh.len), off(sh.off) {}
+
+  // Goes to the next part (the first, after construction) that has blocks; false
+  // if there is none.
   __device__ __forceinline__ bool step(const PagedParams& P) {
-    fresh = false;
     do {
-      if (len <= 0) return false;
-      if (++h >= P.c.heads) {
-        h = 0;
-        fresh = true;
-        if (++i >= nt) {
-          i = 0;
-          do {
-            if (++b >= P.B) return false;              // not reached: len ends first
-            s = load_seq(P, b);
-            nt = tiles_of<R>(P, s);
-          } while (nt == 0);
+      if (off < 0) {
+        if (len <= 0) return false;
+        if (++h >= P.c.heads) {
+          h = 0;
+          if (++i >= nt) {
+            i = 0;
+            do {
+              if (++b >= P.B) return false;            // not reached: len ends first
+              s = load_seq(P, b);
+              nt = tiles_of<R>(P, s);
+            } while (nt == 0);
+          }
+          tile_blocks<R, BK>(P, s, i, t0, t1);
         }
-        tile_blocks<R, BK>(P, s, i, t0, t1);
+        off = 0;
       }
-      part(P, 0);
+      part(P, off);
+      off = -1;
     } while (k0 >= k1);                                // a last part too short to be one
     return true;
   }

@@ -198,6 +198,10 @@ __device__ __forceinline__ void store8(void* to, const uint32_t* w) {
                "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(__cvta_generic_to_global(p)));
+}
+
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -322,6 +326,16 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         ++parts;
         if (!more) break;
+        // Its query rows go to L2 while the part before it still runs.
+        if (parts > 1) {
+          const int p0 = w.i * kChRows, rows = min(kChRows, w.s.ql * P.group - p0);
+          for (int i = lane; i < rows; i += 32) {
+            const int tok = (p0 + i) / P.by_group;
+            const uint16_t* src = static_cast<const uint16_t*>(P.q.ptr) + (w.s.q0 + tok) * P.q.st + (w.h * P.group + p0 + i - tok * P.group) * P.q.sh;
+            prefetch_l2(src);
+            prefetch_l2(src + 64);
+          }
+        }
         auto lookup = [&](int kb) {
           const int key = kb * kChKeys + lane * M.box;
           int row = M.rows;                        // past the cache's end: reads zeros

@@ -120,7 +120,18 @@ constexpr int kChunkMinShare = 4;                 // blocks of 128 keys
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Query rows of a tile: the smallest of the kernels' that holds a sequence's
-// rows of one KV head.
+// rows of one KV head.  Tiles of 8, 16 and 256 (a call of at most 128 rows works
+// on 128), times in us:
+//                                        rows     8      16     256
+//   1 sequence of 1024 keys, 8 heads         8    12.4   14.4   16.6
+//   16 sequences of 8192, 8 heads            8    55     76     75
+//   256 sequences of 256, 8 heads           16    66     72     107
+//   16 sequences of 8192, 8 heads           16    94     80     75
+//   8 sequences of 65536, 8 heads           16    323    253    232
+//   1 sequence of 1024, 8 heads             32    14.4   16.4   18.2
+//   16 sequences of 8192, 8 heads           32    166    142    76
+// For 9 to 16 rows the middle one is never far off; which of the others is best
+// depends on lengths that the host does not know.
 int tile_rows(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b) {
   const int64_t group = q->H / c->heads;
   const int64_t most = (b->cu_q ? (b->max_q > 0 ? b->max_q : q->T) : 1) * group;

@@ -132,8 +132,9 @@ __device__ __forceinline__ int operator/(int n, const FastDiv& f) {
 // ---------------------------------------------------------------------------
 constexpr int kCacheThreads = 256;
 // Tokens a lane: four where the calls are long enough to fill the GPU, else one,
-// which spreads a short call over more SMs (64 tokens x 8 heads: 4.1 against
-// 4.8 us; 73397 tokens x 8 heads: 102 against 82 us).
+// which spreads a short call over more SMs.  One against four, writing x 8 heads:
+// 64 tokens 4.1 and 4.8 us, 8192 tokens 17.5 and 14.9 us, 73397 tokens 105 and
+// 81 us; reading 65536 tokens 86 and 65 us.
 constexpr int kCacheGroups = kCacheThreads / 16;
 
 template <bool kHalf, int kEach>

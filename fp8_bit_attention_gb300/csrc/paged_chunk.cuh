@@ -2,7 +2,8 @@
 // head: chunks of new tokens, on the tensor cores (tcgen05).
 //
 // A tile is 256 query rows (tokens times query heads of one KV head) in two
-// halves of 128, a step is one half's work on a block of 128 keys:
+// halves of 128; a turn is one half's work on a block of 128 keys, whose softmax
+// takes two steps of 64 keys.  Halves t = 0, 1:
 //   S_t = Q_t K^T          kind::f8f6f4.  K's codes go in as they lie in the
 //                          cache (TMA tiles, K-major); Q enters as a sum of
 //                          E4M3 parts, each the rounding error of the ones
@@ -17,10 +18,28 @@
 //                          256 rows, with the token's scale: V 2^(e - E + 7), E
 //                          the largest scale so far.
 // While one half's softmax runs, the tensor core works on the other half.  The
-// softmax hands over P in two parts of 64 keys, so that the first part's product
-// runs beside the second part's softmax.  A tile of at most 128 rows keeps the
-// overlap by giving the blocks to the halves in turn, both on the same rows, and
-// joining the two results at the end ("solo").
+// softmax hands over P one step at a time, so that the first step's product runs
+// beside the second step's softmax.  A tile of at most 128 rows keeps the overlap
+// by giving the blocks to the halves in turn, both on the same rows, and joining
+// the two results at the end ("solo").
+//
+// What bounds it: long calls, the softmax beside the products.  4096 tokens x 32
+// heads over 65536 keys take 3.05 ms, 1390 TFLOP/s, 72% of a library product's
+// rate; a turn's 16 MMA instructions take 1026 cycles of the tensor core, its
+// softmax 1500 to 1870 of its four warps while the others run (900 alone), and
+// two turns in step 2900.  Calls of many tiles with few keys, what a tile costs
+// beside its blocks: 8 us (Q's rows in, their conversion, the first scores, O's
+// rows out; one CTA fills the SM, so nothing covers them).  Few rows over many
+// keys ("solo"), V's conversion and the softmax: 8 x 65536 keys x 8 heads for 32
+// rows 232 us, 69% of a copy's rate.  Instructions are a resource: every warp role
+// runs its own code at once, and waiting for instructions was the second largest
+// stall, so what is not in the inner loop is kept in loops of little code.
+//
+// Measured and left out (ms for 4096 over 65536; the kernel of the time in
+// brackets): scores of 64 keys in two buffers a half 3.5 (3.1); 16 softmax warps,
+// two threads a row, 3.7 (3.1); a warp issuing products for each half 3.9 (3.1);
+// O through shared memory, for stores of whole rows, 3.6 (3.1); the next tile's Q
+// in registers before the end of the one before 3.35 (3.06).
 //
 // Warps: 0-3 and 4-7 softmax of the halves, a thread per row; 8-11 convert V; 12
 // walks the share, looks up pages and loads K and V; 13 issues the products; 14
@@ -28,7 +47,7 @@
 //
 // Numbers: scores, references, sums and outputs are FP32.  Weights are 2^7 p
 // relative to a reference, the row's maximum when it was last looked for: that is
-// when the weights of a block add up to 2^15.5, so that none passes FP16's
+// when the weights of a step add up to 2^15.5, so that none passes FP16's
 // largest value (O is then rescaled in tensor memory).  Weights are flushed below
 // 2^-32 of the one at the reference.  V's values are flushed below 2^-31 of the
 // largest token's.
@@ -40,7 +59,7 @@ namespace ovc {
 
 constexpr int kChRows = 256;
 constexpr int kChKeys = 128;
-constexpr int kChStep = 64;                        // keys of a step
+constexpr int kChStep = 64;                        // keys of a softmax step
 constexpr int kChThreads = 512;
 // Registers: 512 threads of 128 at launch; 256 x 184 + 256 x 72 = 512 x 128.
 constexpr int kChSoftmaxRegs = 184;
@@ -49,7 +68,7 @@ static_assert(256 * kChSoftmaxRegs + 256 * kChOtherRegs <= kChThreads * 128, "re
 constexpr uint32_t kChTile = 128 * 128;            // bytes of an E4M3 tile
 constexpr uint32_t kChTile16 = 2 * kChTile;        // bytes of V in FP16
 constexpr float kChPBias = 7.0f;                   // log2 of the weight at the reference
-constexpr float kChSumLimit = 46341.0f;            // 2^15.5: a row's weights in a block stay below FP16's largest value
+constexpr float kChSumLimit = 46341.0f;            // 2^15.5: a row's weights in a step stay below FP16's largest value
 constexpr int kChVBias = 7;
 constexpr int kChParts = 4;
 

@@ -422,6 +422,37 @@ def test_strided_queries_and_output(q_len):
     assert not big.any()
 
 
+@pytest.mark.parametrize("start, stride_t, stride_h", [(8, 0, 128), (0, 8, 128), (0, 0, 136)])
+@pytest.mark.parametrize("q_len", [1, 200])
+def test_rows_at_16_bytes(q_len, start, stride_t, stride_h):
+    """Rows of q, of the output, of both at odd multiples of 16 bytes."""
+    c = Case([q_len] * 2, [2100, 300], 2, 4, 32, seed=23)
+    want = c.run()
+    n, h = c.q.shape[:2]
+
+    def odd(x, fill):
+        flat = torch.full((start + n * (stride_h * h + stride_t),), fill, dtype=torch.bfloat16, device="cuda")
+        y = flat.as_strided((n, h, 128), (stride_h * h + stride_t, stride_h, 1), start)
+        return flat, y.copy_(x) if x is not None else y
+
+    _, q = odd(c.q, 0.0)
+    flat, out = odd(None, 7.0)
+    for args in (dict(), dict(out=out)):
+        got = ovc.paged_attention(q, c.cache, c.table, c.lens, cu_q=c.cu, max_q=q_len, **args)
+        assert torch.equal(got, want)
+    out.fill_(7.0)
+    assert (flat == 7.0).all()                       # nothing between the rows was touched
+    got = ovc.paged_attention(c.q, c.cache, c.table, c.lens, cu_q=c.cu, max_q=q_len, out=out)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("q_len, group", [(1, 8), (1, 16), (3, 8), (40, 8)])
+def test_one_long_sequence_over_all_sms(q_len, group):
+    c = Case([q_len], [70001], 1, group, 16, seed=26)
+    o, lse = c.run(return_lse=True)
+    c.check(o, lse)
+
+
 @pytest.mark.parametrize("q_len", [1, 100])
 def test_bad_pages_and_lengths_are_reported(q_len):
     c = Case([q_len, q_len], [400, 400], 2, 2, 16, seed=12)

@@ -39,7 +39,9 @@
 // brackets): scores of 64 keys in two buffers a half 3.5 (3.1); 16 softmax warps,
 // two threads a row, 3.7 (3.1); a warp issuing products for each half 3.9 (3.1);
 // O through shared memory, for stores of whole rows, 3.6 (3.1); the next tile's Q
-// in registers before the end of the one before 3.35 (3.06).
+// in registers before the end of the one before 3.35 (3.06); scores 32 at a time,
+// the next ones on their way, 3.22 (3.05); warps without a row hand over at once,
+// 1% slower where all have some, 3% faster for 32 rows.
 //
 // Warps: 0-3 and 4-7 softmax of the halves, a thread per row; 8-11 convert V; 12
 // walks the share, looks up pages and loads K and V; 13 issues the products; 14

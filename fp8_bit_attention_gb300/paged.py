@@ -58,18 +58,19 @@ class KVCache:
         desc = _abi.OvcKVCache(shape[0], shape[1], shape[2], self.k.data_ptr(), self.v.data_ptr(),
                                self.k_scale.data_ptr(), self.v_scale.data_ptr())
         object.__setattr__(self, "_ref", _byref(desc))     # the C struct, kept alive by its reference
+        object.__setattr__(self, "_shape", shape)
 
     @property
     def pages(self) -> int:
-        return self.k.shape[0]
+        return self._shape[0]
 
     @property
     def heads(self) -> int:
-        return self.k.shape[1]
+        return self._shape[1]
 
     @property
     def page(self) -> int:
-        return self.k.shape[2]
+        return self._shape[2]
 
     @property
     def device(self) -> torch.device:
@@ -182,13 +183,15 @@ def kv_cache_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype = t
 
 
 def _batch(q, cache, page_table, kv_lens, cu_q, max_q, causal, window):
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1 or page_table.shape[1] < 1:
+    shape, strides = page_table.shape, page_table.stride()
+    if len(shape) != 2 or page_table.dtype != torch.int32 or strides[1] != 1 or shape[1] < 1:
         raise ValueError("page_table must be int32 [sequences, pages] with unit column stride")
-    n = page_table.shape[0]
+    n, width = shape
+    tokens, heads, _ = q.shape
     lens = _ints(kv_lens, (n,), "kv_lens")
     if cu_q is None:
-        if q.shape[0] != n:
-            raise ValueError(f"without cu_q each of the {n} sequences has one query row, got {q.shape[0]}")
+        if tokens != n:
+            raise ValueError(f"without cu_q each of the {n} sequences has one query row, got {tokens}")
         if max_q not in (None, 1):
             raise ValueError("max_q needs cu_q")
         cu, most = None, 1
@@ -198,10 +201,10 @@ def _batch(q, cache, page_table, kv_lens, cu_q, max_q, causal, window):
         raise ValueError("max_q must not be negative")
     if window is not None and (window < 1 or not causal):
         raise ValueError("window must be positive and needs causal")
-    if q.shape[1] % cache.heads or q.shape[1] == 0:
-        raise ValueError(f"{q.shape[1]} query heads over {cache.heads} KV heads")
-    stride = page_table.stride(0) if n > 1 else max(page_table.stride(0), page_table.shape[1])
-    return _abi.OvcPagedBatch(n, page_table.data_ptr(), stride, page_table.shape[1], lens, cu, most, int(bool(causal)),
+    if heads % cache.heads or heads == 0:
+        raise ValueError(f"{heads} query heads over {cache.heads} KV heads")
+    stride = strides[0] if n > 1 else max(strides[0], width)
+    return _abi.OvcPagedBatch(n, page_table.data_ptr(), stride, width, lens, cu, most, int(bool(causal)),
                               min(int(window or 0), _INT32_MAX))
 
 
@@ -210,8 +213,9 @@ def paged_attention_workspace_bytes(q: torch.Tensor, cache: KVCache, page_table:
     """Bytes of :func:`paged_attention`'s workspace (0 for no rows)."""
     if q.shape[0] == 0:
         return 0
+    rq = _rows(q, "q")
     b = _batch(q, cache, page_table, kv_lens, cu_q, max_q, True, None)
-    return int(lib().ovc_paged_attention_workspace_bytes(_byref(_rows(q, "q")), cache._ref, _byref(b)))
+    return int(lib().ovc_paged_attention_workspace_bytes(_byref(rq), cache._ref, _byref(b)))
 
 
 def paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, *,

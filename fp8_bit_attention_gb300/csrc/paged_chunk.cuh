@@ -492,26 +492,30 @@ __global__ void __launch_bounds__(kChThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sm.part_empty[d]));
         ++parts;
-        // Lane i takes keys 4 i .. 4 i + 3 (one page holds them).
-        auto load = [&](int i, uint32_t& kw, uint32_t& vw) {
+        // Lane i takes keys 4 i .. 4 i + 3 (one page holds them), from `row` of the
+        // cache on.
+        auto load = [&](int i, uint32_t& kw, uint32_t& vw, int& row) {
           const int key = (x.k0 + i) * kChKeys + 4 * lane;
           kw = vw = 0;
+          row = 0;
           if (i < x.nblk && key < x.kv) {
             const int j = key / P.by_page;
             const int p = __ldg(P.table + x.b * P.table_stride + j);
             if (p >= 0 && p < P.c.pages) {
-              const int64_t row = static_cast<int64_t>((p * P.c.heads + x.h) * P.c.page + key - j * P.c.page);
+              row = (p * P.c.heads + x.h) * P.c.page + key - j * P.c.page;
               kw = *reinterpret_cast<const uint32_t*>(P.c.ks + row);
               vw = *reinterpret_cast<const uint32_t*>(P.c.vs + row);
             }
           }
         };
         uint32_t kw, vw;
-        load(0, kw, vw);
+        int row;
+        load(0, kw, vw, row);
         int E = 0;
         for (int i = 0; i < x.nblk; ++i, ++n) {
           uint32_t kn, vn;
-          load(i + 1, kn, vn);
+          int rown;
+          load(i + 1, kn, vn, rown);
           const uint32_t s = n % Sh::kScales;
           const int left = x.kv - ((x.k0 + i) * kChKeys + 4 * lane);
           int e = 0;
@@ -525,7 +529,27 @@ __global__ void __launch_bounds__(kChThreads, 1)
               if (((kw >> (8 * j)) & 255u) == 255u) nan |= 1u << (8 * j);
             }
           }
-          E = max(E, __reduce_max_sync(0xFFFFFFFFu, e));
+          int Eb = __reduce_max_sync(0xFFFFFFFFu, e);
+          if (Eb == 127 && E < 127) {
+            // A vector of zeros has this byte by the format and counts for nothing.
+            e = 0;
+#pragma unroll 1
+            for (int j = 0; j < 4 && j < left; ++j) {
+              const int ev = (vw >> (8 * j)) & 255u;
+              uint32_t any = ev == 127 ? 0u : 0x7Fu;
+              if (ev == 127) {
+                const uint4* codes = reinterpret_cast<const uint4*>(P.c.v + static_cast<int64_t>(row + j) * 128);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  const uint4 y = codes[c];
+                  any |= y.x | y.y | y.z | y.w;
+                }
+              }
+              if (ev != 255 && (any & 0x7F7F7F7Fu)) e = max(e, ev);
+            }
+            Eb = __reduce_max_sync(0xFFFFFFFFu, e);
+          }
+          E = max(E, Eb);
           if (n >= Sh::kScales) ok = __all_sync(0xFFFFFFFFu, wait(sm.sc_empty[s], (n / Sh::kScales - 1) & 1));
           if (!ok) break;
           ChunkScales& sc = sm.sc[s];
@@ -553,6 +577,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[s]));
           kw = kn;
           vw = vn;
+          row = rown;
         }
         if (!ok) break;
       }

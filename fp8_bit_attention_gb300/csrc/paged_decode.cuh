@@ -129,6 +129,19 @@ __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_
 // 2^x for an integer x, 0 below FP32's normal range.
 __device__ __forceinline__ float exp2i(int x) { return x < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(x + 127) << 23); }
 
+// Bit 2 i: row i of the 16 of a tile of codes is a vector of zeros, of either sign.
+__device__ __forceinline__ uint32_t zero_rows(const uint8_t* codes) {
+  const uint8_t* half = codes + (threadIdx.x & 31) * 64;
+  uint32_t any = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint4 x = lds128(half + 16 * c);
+    any |= x.x | x.y | x.z | x.w;
+  }
+  const uint32_t b = __ballot_sync(0xFFFFFFFFu, (any & 0x7F7F7F7Fu) != 0);
+  return ~(b | b >> 1);
+}
+
 // The computing warps' own barrier: the loading warp is past them.
 __device__ __forceinline__ void decode_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kDecWarps) : "memory"); }
 
@@ -410,9 +423,16 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
             }
           }
       }
-      // The block's largest V scale among the sequence's keys.
-      const uint32_t ev = vs[lane & 15];
-      const int Eb = __reduce_max_sync(0xFFFFFFFFu, key0 + (lane & 15) < s.kv && ev != 255u ? static_cast<int>(ev) : 0);
+      // The block's largest V scale among the sequence's keys.  A vector of zeros
+      // has 127 by the format and counts for nothing: it is looked for where that
+      // byte would raise E.
+      int ev = vs[lane & 15];
+      if (key0 + (lane & 15) >= s.kv || ev == 255) ev = 0;
+      int Eb = __reduce_max_sync(0xFFFFFFFFu, ev);
+      if (Eb == 127 && E < 127) {
+        const bool zero = zero_rows(V) >> (2 * (lane & 15)) & 1u;
+        Eb = __reduce_max_sync(0xFFFFFFFFu, zero && ev == 127 ? 0 : ev);
+      }
       bool grown = Eb > E;
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)
@@ -452,7 +472,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
       for (int i = 0; i < 2; ++i) {
         const int kk = 8 * i + g;
         const uint32_t e = vs[kk];
-        const float sv = e == 255u ? __uint_as_float(0x7FFFFFFFu) : exp2i(static_cast<int>(e) - E + kDecPBias);
+        const float sv = e == 255u ? __uint_as_float(0x7FFFFFFFu) : exp2i(min(static_cast<int>(e) - E, 0) + kDecPBias);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
           float w[2];

@@ -50,9 +50,13 @@
 // Numbers: scores, references, sums and outputs are FP32.  Weights are 2^7 p
 // relative to a reference, the row's maximum when it was last looked for: that is
 // when the weights of a step add up to 2^15.5, so that none passes FP16's
-// largest value (O is then rescaled in tensor memory).  Weights are flushed below
-// 2^-32 of the one at the reference.  V's values are flushed below 2^-31 of the
-// largest token's.
+// largest value (O is then rescaled in tensor memory).  What is lost of a weight
+// is below 2^-32 of the one at the reference.  V's values are exact as long as its
+// scales spread over at most 2^kChSpread.  Beyond that ("wide") V goes in without
+// its scales and they go into the weights, which are then 2^7 p 2^(e - E) with an E
+// of each row's own, of the largest p 2^e that it sees: a token counts by its term
+// and one that is masked not at all.  Either way no more than 2^-20 of a row's
+// largest term is lost.
 #pragma once
 
 #include "paged_decode.cuh"
@@ -72,6 +76,9 @@ constexpr uint32_t kChTile16 = 2 * kChTile;        // bytes of V in FP16
 constexpr float kChPBias = 7.0f;                   // log2 of the weight at the reference
 constexpr float kChSumLimit = 46341.0f;            // 2^15.5: a row's weights in a step stay below FP16's largest value
 constexpr int kChVBias = 7;
+// Scales of V that spread further go into the weights.  A block is looked at
+// closely where a scale is above E or more than kChNear below it.
+constexpr int kChSpread = 12, kChNear = 6;
 constexpr int kChParts = 4;
 
 template <bool kHalf>
@@ -82,13 +89,15 @@ struct ChunkShape {
   static constexpr int kScales = 4;
 };
 
-// A block's scales: those of K as values, those of V as FP16 pairs 2^(e-E+7).
+// A block's scales: those of K as values, those of V as FP16 pairs 2^(e-E+7), or
+// 2^7 where they go into the weights.
 struct alignas(16) ChunkScales {
   float k[kChKeys];
   uint32_t v[kChKeys];
   uint8_t nan[kChKeys];                            // 1: K's scale is NaN, 2: V's (their values above are 1 and 0)
-  int e;                                           // E
-  int poison;                                      // any such token
+  uint8_t ve[kChKeys];                             // wide: V's e, 0 for vectors of zeros
+  int e;                                           // E, from the first wide block on unchanged
+  int rare;                                        // 1: any such NaN, 2: wide
 };
 
 // A tile's part.
@@ -113,7 +122,7 @@ struct ChunkSmem {
     PlanSmem plan;
   };
   float2 ml[128];                                  // solo: the second half's reference and sum
-  int e1;                                          // and its E
+  int e1[128];                                     // and its E
   ChunkPart part[kChParts];
   uint64_t k_full[Sh::kK], k_empty[Sh::kK];
   uint64_t v8_full[Sh::kV], v8_empty[Sh::kV];
@@ -511,45 +520,62 @@ __global__ void __launch_bounds__(kChThreads, 1)
         uint32_t kw, vw;
         int row;
         load(0, kw, vw, row);
-        int E = 0;
+        int E = -1, low = 255;                     // the scales of V so far: the largest, none below
+        int wide = 0;
         for (int i = 0; i < x.nblk; ++i, ++n) {
           uint32_t kn, vn;
           int rown;
           load(i + 1, kn, vn, rown);
           const uint32_t s = n % Sh::kScales;
           const int left = x.kv - ((x.k0 + i) * kChKeys + 4 * lane);
-          int e = 0;
-          uint32_t nan = 0;
+          int most = -1, least = 255;
+          uint32_t nan = 0, zeros = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t ev = (vw >> (8 * j)) & 255u;
+            const int ev = (vw >> (8 * j)) & 255u;
             if (j < left) {
-              if (ev == 255u) nan |= 2u << (8 * j);
-              else e = max(e, static_cast<int>(ev));
+              if (ev == 255) {
+                nan |= 2u << (8 * j);
+              } else {
+                most = max(most, ev);
+                least = min(least, ev);
+              }
               if (((kw >> (8 * j)) & 255u) == 255u) nan |= 1u << (8 * j);
             }
           }
-          int Eb = __reduce_max_sync(0xFFFFFFFFu, e);
-          if (Eb == 127 && E < 127) {
-            // A vector of zeros has this byte by the format and counts for nothing.
-            e = 0;
+          if (__any_sync(0xFFFFFFFFu, most > E || least < E - kChNear || wide)) {
+            // A vector of zeros has 127 by the format and counts for nothing.
+            most = -1;
+            least = 255;
 #pragma unroll 1
             for (int j = 0; j < 4 && j < left; ++j) {
               const int ev = (vw >> (8 * j)) & 255u;
-              uint32_t any = ev == 127 ? 0u : 0x7Fu;
+              uint32_t any = 1;
               if (ev == 127) {
                 const uint4* codes = reinterpret_cast<const uint4*>(P.c.v + static_cast<int64_t>(row + j) * 128);
+                any = 0;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                   const uint4 y = codes[c];
                   any |= y.x | y.y | y.z | y.w;
                 }
+                any &= 0x7F7F7F7Fu;
               }
-              if (ev != 255 && (any & 0x7F7F7F7Fu)) e = max(e, ev);
+              if (ev == 255 || any == 0) {
+                zeros |= 255u << (8 * j);
+              } else {
+                most = max(most, ev);
+                least = min(least, ev);
+              }
             }
-            Eb = __reduce_max_sync(0xFFFFFFFFu, e);
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            least = __reduce_min_sync(0xFFFFFFFFu, least);
+            if (most >= 0) {
+              low = min(low, E < 0 ? min(least, most - kChNear) : least);
+              if (max(E, most) - low > kChSpread) wide = 2;      // and stays so
+              if (!wide) E = max(E, most);
+            }
           }
-          E = max(E, Eb);
           if (n >= Sh::kScales) ok = __all_sync(0xFFFFFFFFu, wait(sm.sc_empty[s], (n / Sh::kScales - 1) & 1));
           if (!ok) break;
           ChunkScales& sc = sm.sc[s];
@@ -560,7 +586,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
           f.y = kscale((kw >> 8) & 255u);
           f.z = kscale((kw >> 16) & 255u);
           f.w = kscale(kw >> 24);
-          auto vscale = [&](uint32_t ev) { return ev == 255u ? 0u : exp2h2(min(static_cast<int>(ev) - E, 0) + kChVBias); };
+          const int to = wide ? 0 : E;
+          auto vscale = [&](uint32_t ev) { return ev == 255u ? 0u : exp2h2(min(static_cast<int>(ev) - to, 0) + kChVBias); };
           h.x = vscale(vw & 255u);
           h.y = vscale((vw >> 8) & 255u);
           h.z = vscale((vw >> 16) & 255u);
@@ -568,10 +595,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
           reinterpret_cast<float4*>(sc.k)[lane] = f;
           reinterpret_cast<uint4*>(sc.v)[lane] = h;
           reinterpret_cast<uint32_t*>(sc.nan)[lane] = nan;
+          if (wide) reinterpret_cast<uint32_t*>(sc.ve)[lane] = vw & ~zeros;
           const bool any = __any_sync(0xFFFFFFFFu, nan != 0);
           if (lane == 0) {
-            sc.e = E;
-            sc.poison = any;
+            sc.e = max(E, 0);
+            sc.rare = any | wide;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[s]));
@@ -731,7 +759,69 @@ __global__ void __launch_bounds__(kChThreads, 1)
       float m = kNegInf, l = 0.0f;
       int E = 0;
       bool begun = false;
-      for (int i = 0; i < x.nblk; ++i) {
+      // Keys that the row does not see: -inf in tensor memory, before the scores are
+      // read, by a loop that stays out of the common path.
+      auto hide = [&](uint32_t tS, int a, int b) {
+#pragma unroll 1
+        for (int c = 0; c < kChStep; c += 32) {
+          uint32_t y[32];
+          tmem_ld32(tS + c, y);
+          tmem_wait_ld32(y);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (c + k < a || c + k > b) y[k] = 0xFF800000u;
+          tmem_st32(tS + c, y);
+        }
+        tmem_wait_st();
+      };
+      // The row's largest score of a step, in log2 units.
+      auto largest = [&](uint32_t tS, const float* sk) {
+        float top = kNegInf;
+#pragma unroll 1
+        for (int c = 0; c < kChStep; c += 32) {
+          uint32_t y[32];
+          tmem_ld32(tS + c, y);
+          tmem_wait_ld32(y);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(sk + c + k);
+            top = fmax3(top, __uint_as_float(y[k]) * k4.x, __uint_as_float(y[k + 1]) * k4.y);
+            top = fmax3(top, __uint_as_float(y[k + 2]) * k4.z, __uint_as_float(y[k + 3]) * k4.w);
+          }
+        }
+        return top * rowf;
+      };
+      auto rescale = [&](float f) {
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_wait_ld32(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+          tmem_st32(tO + c, o);
+        }
+      };
+      // Tokens whose K or V is NaN: a NaN weight in the rows that see them, and for K
+      // a NaN sum.  (In tensor memory: picked out of registers by a loop, the weights
+      // would live in local memory.)
+      auto poison = [&](const ChunkScales& sc, int half, uint32_t tP, int a, int b) {
+        tmem_wait_st();
+#pragma unroll 1
+        for (int c = 0; c < kChStep; c += 2) {
+          const uint32_t bad0 = sc.nan[half * kChStep + c], bad1 = sc.nan[half * kChStep + c + 1];
+          if (bad0 | bad1) {
+            uint32_t y = tmem_ld1(tP + c / 2);
+            const uint32_t see0 = c >= a && c <= b ? bad0 : 0u, see1 = c + 1 >= a && c + 1 <= b ? bad1 : 0u;
+            if (see0) y |= 0x7FFFu;
+            if (see1) y |= 0x7FFF0000u;
+            if ((see0 | see1) & 1u) l = __uint_as_float(0x7FFFFFFFu);
+            tmem_st1(tP + c / 2, y);
+          }
+        }
+      };
+      int i = 0;
+      for (; i < x.nblk; ++i) {
         const uint32_t blk = n + i, ss = blk % Sh::kScales;
         ok = __all_sync(0xFFFFFFFFu, wait(sm.sc_full[ss], (blk / Sh::kScales) & 1));
         if (!ok) break;
@@ -741,6 +831,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           continue;
         }
         const ChunkScales& sc = sm.sc[ss];
+        if (sc.rare & 2) break;                    // wide: the loop below
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
         // Two steps a block: scores in columns 64 half .., weights in 32 half ..
@@ -753,21 +844,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const float* sk = sc.k + half * kChStep;
         const int key0 = (x.k0 + i) * kChKeys + half * kChStep, a = lo - key0, b = hi - key0;
         const bool masked = key0 < x.all_lo || key0 + kChStep - 1 > x.all_hi;
-        if (masked) {
-          // Keys that the row does not see: -inf in tensor memory, before the
-          // scores are read, by a loop that stays out of the common path.
-#pragma unroll 1
-          for (int c = 0; c < kChStep; c += 32) {
-            uint32_t y[32];
-            tmem_ld32(tS + c, y);
-            tmem_wait_ld32(y);
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c + k < a || c + k > b) y[k] = 0xFF800000u;
-            tmem_st32(tS + c, y);
-          }
-          tmem_wait_st();
-        }
+        if (masked) hide(tS, a, b);
         // Weights against the reference at hand.  Their sum tells whether it is
         // still good: only when that reaches kChSumLimit (and in the first
         // blocks, without a reference) is the maximum looked for and are the
@@ -777,24 +854,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int Eb = sc.e;
         uint32_t w[32];
         float sum;
-        // The row's largest score of the step, in log2 units.
-        auto largest = [&]() {
-          float top = kNegInf;
-#pragma unroll 1
-          for (int c = 0; c < kChStep; c += 32) {
-            uint32_t y[32];
-            tmem_ld32(tS + c, y);
-            tmem_wait_ld32(y);
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(sk + c + k);
-              top = fmax3(top, __uint_as_float(y[k]) * k4.x, __uint_as_float(y[k + 1]) * k4.y);
-              top = fmax3(top, __uint_as_float(y[k + 2]) * k4.z, __uint_as_float(y[k + 3]) * k4.w);
-            }
-          }
-          return top * rowf;
-        };
-        if (!begun && half == 0) m = largest();      // a part's first step has no reference to try
+        if (!begun && half == 0) m = largest(tS, sk);      // a part's first step has no reference to try
 #pragma unroll 1
         for (int attempt = 0; attempt < 2; ++attempt) {
           const float shift = kChPBias - (m == kNegInf ? 0.0f : m);
@@ -823,7 +883,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (!again && Eb == E) break;
           float f = 1.0f;
           if (again) {
-            const float mn = fmaxf(m, largest());
+            const float mn = fmaxf(m, largest(tS, sk));
             f = m == kNegInf ? 0.0f : ex2(m - mn);
             m = mn;
             l *= f;
@@ -836,42 +896,83 @@ __global__ void __launch_bounds__(kChThreads, 1)
             if (half == 1) ok = __all_sync(0xFFFFFFFFu, wait(sm.o_done[t], steps & 1));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + c, o);
-              tmem_wait_ld32(o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32(tO + c, o);
-            }
+            rescale(f);
           }
           if (!again) break;
         }
         if (!ok) break;
         l += sum;
         tmem_st32(tP, w);
-        if (sc.poison) {
-          // Tokens whose K or V is NaN: a NaN weight in the rows that see them,
-          // and for K a NaN sum.  (In tensor memory: picked out of registers by
-          // a loop, the weights would live in local memory.)
-          tmem_wait_st();
-#pragma unroll 1
-          for (int c = 0; c < kChStep; c += 2) {
-            const uint32_t bad0 = sc.nan[half * kChStep + c], bad1 = sc.nan[half * kChStep + c + 1];
-            if (bad0 | bad1) {
-              uint32_t y = tmem_ld1(tP + c / 2);
-              const uint32_t see0 = c >= a && c <= b ? bad0 : 0u, see1 = c + 1 >= a && c + 1 <= b ? bad1 : 0u;
-              if (see0) y |= 0x7FFFu;
-              if (see1) y |= 0x7FFF0000u;
-              if ((see0 | see1) & 1u) l = __uint_as_float(0x7FFFFFFFu);
-              tmem_st1(tP + c / 2, y);
-            }
-          }
-        }
+        if (sc.rare) poison(sc, half, tP, a, b);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_addr(&sm.p_full[t][half]));
+        }
+        if (!ok) break;
+        ++steps;
+        begun = true;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[ss]));
+      }
+      // Wide blocks (in a loop of their own: as a branch of the one above they slowed
+      // it down by 3%).  O's unit is 2^(m + E) with m the row's maximum; E follows
+      // that down, and the largest p 2^e of a step up.
+      for (; ok && i < x.nblk; ++i) {
+        const uint32_t blk = n + i, ss = blk % Sh::kScales;
+        ok = __all_sync(0xFFFFFFFFu, wait(sm.sc_full[ss], (blk / Sh::kScales) & 1));
+        if (!ok) break;
+        if (solo && (i & 1) != t) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sm.sc_empty[ss]));
+          continue;
+        }
+        const ChunkScales& sc = sm.sc[ss];
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t tS = tmem + lanes + t * 128 + half * kChStep, tP = tmem + lanes + t * 128 + half * (kChStep / 2);
+          // O is at rest as above.
+          ok = __all_sync(0xFFFFFFFFu, half ? wait(sm.o_done[t], steps & 1) : wait(sm.s_full[t], steps & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const float* sk = sc.k + half * kChStep;
+          const uint8_t* ve = sc.ve + half * kChStep;
+          const int key0 = (x.k0 + i) * kChKeys + half * kChStep, a = lo - key0, b = hi - key0;
+          if (key0 < x.all_lo || key0 + kChStep - 1 > x.all_hi) hide(tS, a, b);
+          const float mn = fmaxf(m, largest(tS, sk)), ref = mn == kNegInf ? 0.0f : mn, down = m - ref;
+          float most = kNegInf;
+#pragma unroll 1
+          for (int c = 0; c < kChStep; c += 32) {
+            uint32_t y[32];
+            tmem_ld32(tS + c, y);
+            tmem_wait_ld32(y);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              most = fmaxf(most, fmaf(__uint_as_float(y[k]) * sk[c + k], rowf, -ref) + static_cast<float>(ve[c + k]));
+          }
+          const int En = max(0, max(__float2int_rd(static_cast<float>(E) + down), __float2int_rd(most)));
+          if (begun || half == 1) rescale(m == kNegInf ? 0.0f : ex2(down + static_cast<float>(E - En)));
+          l *= ex2(down);
+          m = mn;
+          E = En;
+#pragma unroll 1
+          for (int c = 0; c < kChStep; c += 32) {      // P lies before the scores that are still to be read
+            uint32_t y[32], w[16];
+            tmem_ld32(tS + c, y);
+            tmem_wait_ld32(y);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float z = fmaf(__uint_as_float(y[k]) * sk[c + k], rowf, kChPBias - ref);
+              l += ex2(z);
+              y[k] = __float_as_uint(ex2(z + static_cast<float>(ve[c + k] - E)));
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = pack2<true>(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+            tmem_st16(tP + c / 2, w);
+          }
+          if (sc.rare & 1) poison(sc, half, tP, a, b);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_addr(&sm.p_full[t][half]));
         }
         if (!ok) break;
         ++steps;
@@ -891,7 +992,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       }
       if (solo && t == 1) {
         sm.ml[r] = make_float2(m, l);
-        if (r == 0) sm.e1 = E;
+        sm.e1[r] = E;
         mbar_arrive(smem_addr(&sm.x_full));
         // The first half reads this half's O.
         ok = __all_sync(0xFFFFFFFFu, wait(sm.x_empty, solos & 1));
@@ -905,15 +1006,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
         ++solos;
         if (!ok) break;
         tc_fence_after();
+        // A half's unit is 2^(m + E).
         const float2 y = sm.ml[r];
-        const int e1 = sm.e1;
-        const float mj = fmaxf(m, y.x), ref = mj == kNegInf ? 0.0f : mj;
-        const int Ej = max(E, e1);
-        f0 = ex2(m - ref);
-        f1 = ex2(y.x - ref);
-        l = l * f0 + y.y * f1;
-        f0 *= exp2i(E - Ej);
-        f1 = x.nblk > 1 ? f1 * exp2i(e1 - Ej) : 0.0f;
+        const int e1 = sm.e1[r];
+        const float mj = fmaxf(m, y.x), ref = mj == kNegInf ? 0.0f : mj, d0 = m - ref, d1 = y.x - ref;
+        const int Ej = max(0, max(E + __float2int_rd(d0), e1 + __float2int_rd(d1)));
+        l = l * ex2(d0) + y.y * ex2(d1);
+        f0 = ex2(d0 + static_cast<float>(E - Ej));
+        f1 = x.nblk > 1 ? ex2(d1 + static_cast<float>(e1 - Ej)) : 0.0f;
         m = mj;
         E = Ej;
       }

@@ -38,11 +38,16 @@
 // Numbers: Q enters as FP16 (BF16 rows scaled by a power of two: exact but for
 // elements below 2^-29 of the row's largest); scores, maxima, sums and outputs
 // are FP32; a weight is rounded to FP16 once, as 2^14 p 2^(e - E) with e the
-// token's V scale and E the largest so far, so that what is flushed is below
-// 2^-39 of the largest possible term.
+// token's V scale and E the largest so far: what is lost of it is below 2^-39 of
+// 2^E.  E is the same for all rows as long as the scales spread over at most
+// 2^kDecSpread.  Beyond that ("wide") every row has its own, of the largest
+// p 2^e that it sees, so that a token counts by its term and one that is masked
+// not at all.  Either way no more than 2^-20 of a row's largest term is lost.
 #pragma once
 
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "paged_plan.cuh"
 
@@ -54,6 +59,9 @@ constexpr int kDecKeys = 16;                       // keys of a block: a page is
 constexpr int kDecStages = 3;
 constexpr uint32_t kDecCodes = kDecKeys * 128;     // bytes of a block's K (or V) codes
 constexpr int kDecPBias = 14;
+// Scales of V that spread further have units by row.  A block is looked at closely
+// where a scale is above E or more than kDecNear below it.
+constexpr int kDecSpread = 19, kDecNear = 9;
 constexpr int kDecParts = 4;                       // descriptions of parts in flight
 
 // A tile's part, as the computing warps need it.
@@ -74,7 +82,7 @@ struct DecodeSmem {
   };
   uint8_t scale[kDecWarps][kDecStages][2][kDecKeys];
   float m[kDecWarps][8], l[kDecWarps][8];
-  int e[kDecWarps];
+  int e[kDecWarps][16];                            // the rows' E
   DecodePart part[kDecParts];
   uint64_t full[kDecWarps][kDecStages], empty[kDecWarps][kDecStages];
   uint64_t part_full[kDecParts], part_empty[kDecParts];
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
     }
 
     float m[kTiles][2], l[kTiles][2], o[kTiles][8][4];
-    int E = 0;
+    int E = -1, low = 255;                         // the scales of V so far: the largest, none below
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
@@ -357,11 +365,14 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
         for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
     }
 
-#pragma unroll 1
-    for (int kb = d.k0 + ((warp - (d.k0 - d.t0)) & (kDecWarps - 1)); kb < k1; kb += kDecWarps) {
+    // A block; with a true tag the rows have an E each (in shared memory).  False, with
+    // nothing done, if they have to have from this block on.  (Two loops: with both
+    // ways in one, 9 to 16 rows took 5% more.)
+    bool first = true;
+    auto block = [&](int kb, auto tag) __attribute__((always_inline)) -> bool {
+      constexpr bool rows_apart = decltype(tag)::value;
       const uint32_t stage = used % kDecStages;
       wait(sm.full[warp][stage], (used / kDecStages) & 1);
-      ++used;
       const uint8_t* K = sm.kv[warp][stage][0];
       const uint8_t* V = sm.kv[warp][stage][1];
       const uint8_t* ks = sm.scale[warp][stage][0];
@@ -423,68 +434,125 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
             }
           }
       }
-      // The block's largest V scale among the sequence's keys.  A vector of zeros
-      // has 127 by the format and counts for nothing: it is looked for where that
-      // byte would raise E.
+      // V's scales among the sequence's keys.
       int ev = vs[lane & 15];
-      if (key0 + (lane & 15) >= s.kv || ev == 255) ev = 0;
-      int Eb = __reduce_max_sync(0xFFFFFFFFu, ev);
-      if (Eb == 127 && E < 127) {
-        const bool zero = zero_rows(V) >> (2 * (lane & 15)) & 1u;
-        Eb = __reduce_max_sync(0xFFFFFFFFu, zero && ev == 127 ? 0 : ev);
-      }
-      bool grown = Eb > E;
+      if (key0 + (lane & 15) >= s.kv || ev == 255) ev = -1;
+      bool close = ev > E || (ev >= 0 && ev < E - kDecNear) || rows_apart;
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
           for (int d = 4; d <= 16; d <<= 1) top[n][j] = fmaxf(top[n][j], __shfl_xor_sync(0xFFFFFFFFu, top[n][j], d));
-          grown |= top[n][j] > m[n][j];
+          close |= top[n][j] > m[n][j];
         }
-      if (__any_sync(0xFFFFFFFFu, grown)) {
-        const int En = max(E, Eb);
-        const float fe = exp2i(E - En);
-        E = En;
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) {
-          float f[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float mn = fmaxf(m[n][j], top[n][j]);
-            f[j] = m[n][j] == kNegInf ? 0.0f : ex2(m[n][j] - mn);
-            m[n][j] = mn;
-            l[n][j] *= f[j];
-            f[j] *= fe;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            o[n][i][0] *= f[0];
-            o[n][i][1] *= f[1];
-            o[n][i][2] *= f[0];
-            o[n][i][3] *= f[1];
-          }
+      int En = E;
+      close = __any_sync(0xFFFFFFFFu, close);
+      if (close) {
+        // A vector of zeros has 127 by the format and counts for nothing.
+        if (__any_sync(0xFFFFFFFFu, ev == 127)) {
+          const bool zero = zero_rows(V) >> (2 * (lane & 15)) & 1u;
+          if (zero && ev == 127) ev = -1;
+        }
+        const int hi = __reduce_max_sync(0xFFFFFFFFu, ev), lo = __reduce_min_sync(0xFFFFFFFFu, ev < 0 ? 255 : ev);
+        if (hi >= 0 && !rows_apart) {
+          low = min(low, E < 0 ? min(lo, hi - kDecNear) : lo);
+          En = max(E, hi);
+          if (En - low > kDecSpread) return false;
         }
       }
-      // Weights: their sum in FP32, then rounded with the token's V scale.
       uint32_t pf[kTiles][2];
+      if constexpr (!rows_apart) {
+        if (close) {
+          const float fe = exp2i(E - En);
+          E = En;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int kk = 8 * i + g;
-        const uint32_t e = vs[kk];
-        const float sv = e == 255u ? __uint_as_float(0x7FFFFFFFu) : exp2i(min(static_cast<int>(e) - E, 0) + kDecPBias);
+          for (int n = 0; n < kTiles; ++n) {
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float mn = fmaxf(m[n][j], top[n][j]);
+              f[j] = m[n][j] == kNegInf ? 0.0f : ex2(m[n][j] - mn);
+              m[n][j] = mn;
+              l[n][j] *= f[j];
+              f[j] *= fe;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[n][i][0] *= f[0];
+              o[n][i][1] *= f[1];
+              o[n][i][2] *= f[0];
+              o[n][i][3] *= f[1];
+            }
+          }
+        }
+        // Weights: their sum in FP32, then rounded with the token's V scale.
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int kk = 8 * i + g;
+          const uint32_t e = vs[kk];
+          const float sv = e == 255u ? __uint_as_float(0x7FFFFFFFu) : exp2i(min(static_cast<int>(e) - E, 0) + kDecPBias);
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) {
+            float w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float y = z[n][2 * i + j];
+              const float p = ex2(y - (m[n][j] == kNegInf ? 0.0f : m[n][j]));
+              l[n][j] += p;
+              w[j] = masked && y == kNegInf ? 0.0f : p * sv;
+            }
+            pf[n][i] = transpose8x8(pack2<true>(w[0], w[1]));
+          }
+        }
+      } else {
+        // The same with units by row.  E of a row follows its maximum down, and the
+        // largest p 2^e of the block up.
+        const uint32_t counts = __ballot_sync(0xFFFFFFFFu, ev >= 0);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
-          float w[2];
+          float w[2][2];
+          int Er[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float y = z[n][2 * i + j];
-            const float p = ex2(y - (m[n][j] == kNegInf ? 0.0f : m[n][j]));
-            l[n][j] += p;
-            w[j] = masked && y == kNegInf ? 0.0f : p * sv;
+            const float mn = fmaxf(m[n][j], top[n][j]), ref = mn == kNegInf ? 0.0f : mn, down = m[n][j] - ref;
+            float x[2], most = kNegInf;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int kk = 8 * i + g;
+              x[i] = z[n][2 * i + j] - ref + (counts >> kk & 1u ? static_cast<float>(vs[kk]) : 0.0f);
+              most = fmaxf(most, x[i]);
+            }
+#pragma unroll
+            for (int d = 4; d <= 16; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+            const int Eo = first ? E : sm.e[warp][8 * n + 2 * t + j];
+            Er[j] = max(0, max(__float2int_rd(static_cast<float>(Eo) + down), __float2int_rd(most)));
+            const float f = m[n][j] == kNegInf ? 0.0f : ex2(down + static_cast<float>(Eo - Er[j]));
+            l[n][j] *= ex2(down);
+            m[n][j] = mn;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[n][i][j] *= f;
+              o[n][i][2 + j] *= f;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float y = z[n][2 * i + j];
+              l[n][j] += ex2(y - ref);
+              w[i][j] = masked && y == kNegInf ? 0.0f
+                        : vs[8 * i + g] == 255u ? __uint_as_float(0x7FFFFFFFu)
+                                                : ex2(x[i] + static_cast<float>(kDecPBias - Er[j]));
+            }
           }
-          pf[n][i] = transpose8x8(pack2<true>(w[0], w[1]));
+          __syncwarp();                              // every lane has read its rows' E
+          if (g == 0) {
+            sm.e[warp][8 * n + 2 * t] = Er[0];
+            sm.e[warp][8 * n + 2 * t + 1] = Er[1];
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) pf[n][i] = transpose8x8(pack2<true>(w[i][0], w[i][1]));
         }
+        first = false;
       }
       // O^T += V^T P^T.
       const int left = s.kv - key0;                  // keys of the sequence from here on
@@ -513,7 +581,15 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
         }
       __syncwarp();                                  // every lane is done with the stage
       if (lane == 0) mbar_arrive(smem_addr(&sm.empty[warp][stage]));
-    }
+      ++used;
+      return true;
+    };
+    int kb = d.k0 + ((warp - (d.k0 - d.t0)) & (kDecWarps - 1));
+#pragma unroll 1
+    for (; kb < k1; kb += kDecWarps)
+      if (!block(kb, std::false_type())) break;
+#pragma unroll 1
+    for (; kb < k1; kb += kDecWarps) block(kb, std::true_type());
     // The next part's rows, while this one ends.
     const int rows = d.rows, h = d.h, slot = d.slot;
     ++parts;
@@ -541,11 +617,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
           reinterpret_cast<float4*>(sm.o[warp][r])[(4 * g + q) ^ r] =
               make_float4(o[n][2 * q][j], o[n][2 * q][2 + j], o[n][2 * q + 1][j], o[n][2 * q + 1][2 + j]);
       }
-      if (n == 0 && lane == 0) sm.e[warp] = E;
+      if (n == 0 && first && lane < 16) sm.e[warp][lane] = max(E, 0);
       decode_sync();
-      int Et = 0;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) Et = max(Et, sm.e[w]);
 #pragma unroll
       for (int r = warp; r < 8; r += kDecWarps) {
         if (8 * n + r >= rows) break;
@@ -553,10 +626,14 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, sm.m[w][r]);
         const float ref = top == kNegInf ? 0.0f : top;
+        // The row's unit: a warp's is 2^(m + E).
+        int Et = 0;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) Et = max(Et, sm.e[w][8 * n + r] + __float2int_rd(sm.m[w][r] - ref));
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
-          const float f = ex2(sm.m[w][r] - ref), fe = f * exp2i(sm.e[w] - Et);
+          const float d = sm.m[w][r] - ref, f = ex2(d), fe = ex2(d + static_cast<float>(sm.e[w][8 * n + r] - Et));
           total += sm.l[w][r] * f;
           const float4 y = reinterpret_cast<const float4*>(sm.o[w][r])[lane ^ r];
           acc.x += fe * y.x;

@@ -508,6 +508,10 @@ size_t ovc_paged_attention_workspace_bytes(const ovc_rows* q, const ovc_kv_cache
  * scaled scores, FP32 [T, H] contiguous.  softmax_scale <= 0 selects
  * 1/sqrt(128).  A query row that holds a NaN or an infinity gives NaN, unless
  * it sees no key.
+ * Scores, sums and outputs are FP32, weights FP16 with a unit of their row's own:
+ * a key's weight times the size of its value is off by 2^-11 of itself and 2^-20
+ * of the largest such term of the row, whatever the tokens that it does not see
+ * hold.
  * Long sequences are split over the GPU and joined from the workspace
  * (256-byte aligned); calls that share it must not overlap.  The way of
  * splitting depends on all lengths of the batch: the last bits of a sequence's

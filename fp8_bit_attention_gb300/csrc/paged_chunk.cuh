@@ -89,7 +89,9 @@ struct ChunkShape {
   static constexpr int kScales = 4;
 };
 
-// A block's scales: those of K as values, those of V as FP16 pairs 2^(e-E+7), or
+// A block's scales: those of K times the scores' factor to log2 units (the row's
+// factor is then a power of two, and a score less the row's maximum one exact
+// subtraction, however large both are), those of V as FP16 pairs 2^(e-E+7), or
 // 2^7 where they go into the weights.
 struct alignas(16) ChunkScales {
   float k[kChKeys];
@@ -581,7 +583,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
           ChunkScales& sc = sm.sc[s];
           float4 f;
           uint4 h;
-          auto kscale = [&](uint32_t ek) { return ek == 255u ? 1.0f : scale_value(ek); };
+          // Never 0, which would make a hidden key's score NaN.
+          auto kscale = [&](uint32_t ek) { return ek == 255u ? 1.0f : fmaxf(P.c2 * scale_value(ek), __uint_as_float(1u)); };
           f.x = kscale(kw & 255u);
           f.y = kscale((kw >> 8) & 255u);
           f.z = kscale((kw >> 16) & 255u);
@@ -693,7 +696,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       if (here) row_range(P, s, tok, lo, hi);
 
       // Q's row in E4M3 parts, scaled by a power of two to at most 448.
-      float rowf = P.c2;
+      float rowf = 1.0f;
       if (!solo || t == 0) {
         uint32_t w[64];
 #pragma unroll

@@ -121,3 +121,54 @@ def test_values_of_every_size(q_len, group, spread):
     _check(c, o, lse, terms=True)
     o2, lse2 = c.run(return_lse=True)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# ------------------------------------------------------------- sizes of scores
+@pytest.mark.parametrize("scale", [1e-30, 1e-44])
+@pytest.mark.parametrize("q_len, group", ROWS)
+def test_scales_next_to_nothing(q_len, group, scale):
+    """All weights alike: each row's mean of the values that it sees."""
+    c = Case([q_len], [700], 2, group, 32, seed=38)
+    c.q = c.q * 2.0 ** -20
+    o, lse = c.run(return_lse=True, softmax_scale=scale)
+    _check(c, o, lse, scale=scale)
+    o, lse = c.run(return_lse=True, softmax_scale=scale, window=100)
+    _check(c, o, lse, scale=scale, window=100)
+
+
+@pytest.mark.parametrize("power", [6, 24, 36, 100])
+@pytest.mark.parametrize("most, mul", [(4, 1.0), (7, 1.5)])
+@pytest.mark.parametrize("q_len, group", ROWS[2:])
+def test_scores_far_apart(q_len, group, most, mul, power):
+    """Scores of whole multiples of mul * 2^power / sqrt(128): beyond power 6 a row gives
+    the mean of the values at its largest one.  Equal scores have to stay equal, and
+    the largest has to have the weight 1, however large it is."""
+    n = 700
+    c = Case([q_len], [n], 2, group, 32, seed=40)
+    k = torch.randint(-most, most + 1, (n, 2), device="cuda", generator=torch.Generator("cuda").manual_seed(41))
+    c.k[:] = 0.0
+    c.k[..., 3] = k.to(c.k.dtype)
+    sign = torch.where(c.q[..., 3] < 0, -1.0, 1.0)
+    c.q[:] = 0.0
+    c.q[..., 3] = sign * mul * 2.0 ** power
+    _rewrite(c)
+    o, lse = c.run(return_lse=True)
+    # distances to the largest score from whole numbers: in the definition's own
+    # 64 bits they would be lost beside scores of 2^100
+    s = sign.double().unsqueeze(-1) * k.double().T.repeat_interleave(group, 0)           # [rows, heads, keys]
+    seen = torch.arange(n, device="cuda") <= torch.arange(n - q_len, n, device="cuda").view(-1, 1, 1)
+    s = torch.where(seen, s, -math.inf)
+    top = s.amax(-1, keepdim=True)
+    unit = mul * 2.0 ** power / math.sqrt(128.0)
+    w = torch.exp((s - top) * unit)
+    total = w.sum(-1)
+    v = c.dense()[0][1].repeat_interleave(group, 1)
+    ref, av = (torch.einsum("thj,jhd->thd", w / total.unsqueeze(-1), x) for x in (v, v.abs()))
+    ref_lse = top.squeeze(-1) * unit + total.log()
+    # Scores share the factor's and their own last rounding, 2^-23: distances of up
+    # to 14 units are off by 2^-19 of a unit, which matters while weights are left.
+    ds = torch.full_like(ref_lse, 2.0 ** -19 * unit if power == 6 else 0.0)
+    eo, _ = error_bounds(ref, ref_lse, av, 2.0 ** 15 * ds)
+    assert ((o.double() - ref).abs() <= eo).all()
+    assert ((lse.double() - ref_lse).abs() <= ds + 2.0 ** -20 + 2.0 ** -21 * ref_lse.abs()).all()
+    assert ovc.device_status() == 0

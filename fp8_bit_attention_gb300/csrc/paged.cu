@@ -147,10 +147,10 @@ int ctas_per_sm(int R) { return R == 8 ? kDecodeCtas<1> : R == 16 ? kDecodeCtas<
 size_t work_bytes(int R, PagedWork* w, void* base) {
   uint8_t* p = static_cast<uint8_t*>(base);
   const size_t ctas = static_cast<size_t>(kMaxSms) * ctas_per_sm(R);
-  const size_t o = up256(ctas * 2 * R * 512), l = up256(ctas * 2 * R * 4);
+  const size_t o = up256(ctas * 2 * R * 512), l = up256(ctas * 2 * R * 8);
   if (w) {
     w->o = reinterpret_cast<float*>(p);
-    w->lse = reinterpret_cast<float*>(p + o);
+    w->ml = reinterpret_cast<float2*>(p + o);
     w->cut = reinterpret_cast<CutTile*>(p + o + l);
   }
   return o + l + up256(ctas * sizeof(CutTile));

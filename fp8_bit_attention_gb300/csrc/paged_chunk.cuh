@@ -1024,7 +1024,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
       const float inv = l == 0.0f ? 0.0f : exp2i(-kChVBias) / l, se = scale_value(E);
       f0 *= inv;
       f1 *= inv;
-      const float L = l == 0.0f ? kNegInf : m + log2f(l) - kChPBias;
       uint16_t* orow = static_cast<uint16_t*>(P.o.ptr) + (s.q0 + tok) * P.o.st + hq * P.o.sh;
       const int64_t place = (static_cast<int64_t>(blockIdx.x) * 2 + x.slot) * kChRows + row;
       const bool two = solo && x.nblk > 1;
@@ -1066,8 +1065,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
       }
       tc_fence_before();
       if (here) {
-        if (x.slot >= 0) work.lse[place] = L;
-        else if (P.lse) P.lse[static_cast<int64_t>(s.q0 + tok) * P.Hq + hq] = L * 0.69314718055994531f;
+        if (x.slot >= 0) work.ml[place] = make_float2(m, l * exp2i(-static_cast<int>(kChPBias)));
+        else if (P.lse) P.lse[static_cast<int64_t>(s.q0 + tok) * P.Hq + hq] = l == 0.0f ? kNegInf : (m + log2f(l) - kChPBias) * 0.69314718055994531f;
       }
       if (solo) mbar_arrive(smem_addr(&sm.x_empty));
     }

@@ -413,7 +413,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float& y = z[n][2 * i + j];
-            y = (kTiles == 1 ? y + z2[n][2 * i + j] : y) * sk * rowf[n][j];
+            // (A rounded product: fused with the subtraction of the maximum it would
+            // differ from that by the maximum's rounding, which can be large.)
+            y = __fmul_rn((kTiles == 1 ? y + z2[n][2 * i + j] : y) * sk, rowf[n][j]);
             top[n][j] = fmaxf(top[n][j], y);
           }
       }
@@ -647,16 +649,15 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
         acc.y = acc.y * inv * se;
         acc.z = acc.z * inv * se;
         acc.w = acc.w * inv * se;
-        const float L = total == 0.0f ? kNegInf : top + log2f(total);
         if (slot < 0) {
           const int p = p0 + 8 * n + r, tok = p / P.by_group, hq = h * P.group + p - tok * P.group;
           reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o.ptr) + (s.q0 + tok) * P.o.st + hq * P.o.sh)[lane] =
               make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w));
-          if (P.lse && lane == 0) P.lse[static_cast<int64_t>(s.q0 + tok) * P.Hq + hq] = L * 0.69314718055994531f;
+          if (P.lse && lane == 0) P.lse[static_cast<int64_t>(s.q0 + tok) * P.Hq + hq] = total == 0.0f ? kNegInf : (top + log2f(total)) * 0.69314718055994531f;
         } else {
           const int64_t place = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * R + 8 * n + r;
           reinterpret_cast<float4*>(work.o + place * 128)[lane] = acc;
-          if (lane == 0) work.lse[place] = L;
+          if (lane == 0) work.ml[place] = make_float2(top, total);
         }
       }
       if (n + 1 < kTiles) decode_sync();

@@ -7,7 +7,7 @@
 // block), form one line, which the CTAs of a persistent grid cut into equal
 // shares: lengths that differ, or a single long sequence, load every SM alike.
 // A tile that lies in one share is finished by its CTA.  A tile cut by a share's
-// end leaves partial results (each normalised, with its log-sum) in the
+// end leaves partial results (each normalised, with its maximum and sum) in the
 // workspace, at most two a CTA, which paged_join_kernel joins.  Every CTA
 // derives its share from the lengths on the device, so that lengths may change
 // under a captured graph and no other launch has to plan.
@@ -32,7 +32,7 @@ struct CutTile {
 // Workspace of one call.
 struct PagedWork {
   float* o;         // [ctas][2][R][128] normalised partial outputs
-  float* lse;       // [ctas][2][R] their log2-sums
+  float2* ml;       // [ctas][2][R] their largest scores (log2 units) and their sums against those
   CutTile* cut;     // [ctas]
 };
 
@@ -338,8 +338,9 @@ __device__ __forceinline__ void write_cut(const PagedParams& P, const Share& sh,
 }
 
 // ---------------------------------------------------------------------------
-// Join of a cut tile's partial results: with L_c the log2-sum of part c,
-// O = sum_c 2^(L_c - L) O_c, L = log2 sum_c 2^L_c.  Part c0 is in its CTA's
+// Join of a cut tile's partial results: with m_c and l_c the maximum and sum of
+// part c, M = max m_c and l = sum_c 2^(m_c - M) l_c, O = sum_c 2^(m_c - M) l_c O_c / l.
+// (A log-sum in one number would lose log2 l_c beside a large m_c.)  Part c0 is in its CTA's
 // second slot, the others in their CTA's first.  kWarps warps per row share the
 // parts (4 where few rows are cut into many parts), four channels a lane.
 // ---------------------------------------------------------------------------
@@ -362,16 +363,20 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (here) {
       auto at = [&](int k) { return (static_cast<int64_t>(c.c0 + k) * 2 + (k == 0)) * R + r; };
-      for (int k = lane; k < n; k += 32) top = fmaxf(top, w.lse[at(k)]);
+      for (int k = lane; k < n; k += 32) top = fmaxf(top, w.ml[at(k)].x);
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
       const float ref = top == kNegInf ? 0.0f : top;
-      for (int k = lane; k < n; k += 32) total += exp2f(w.lse[at(k)] - ref);
+      auto weight = [&](int k) {
+        const float2 x = w.ml[at(k)];
+        return exp2f(x.x - ref) * x.y;
+      };
+      for (int k = lane; k < n; k += 32) total += weight(k);
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
 #pragma unroll 8
       for (int k = sub; k < n; k += kWarps) {
-        const float f = exp2f(w.lse[at(k)] - ref);
+        const float f = weight(k);
         const float4 x = reinterpret_cast<const float4*>(w.o + at(k) * 128)[lane];
         acc.x += f * x.x;
         acc.y += f * x.y;

@@ -138,7 +138,7 @@ def test_scales_next_to_nothing(q_len, group, scale):
 
 @pytest.mark.parametrize("power", [6, 24, 36, 100])
 @pytest.mark.parametrize("most, mul", [(4, 1.0), (7, 1.5)])
-@pytest.mark.parametrize("q_len, group", ROWS[2:])
+@pytest.mark.parametrize("q_len, group", ROWS)
 def test_scores_far_apart(q_len, group, most, mul, power):
     """Scores of whole multiples of mul * 2^power / sqrt(128): beyond power 6 a row gives
     the mean of the values at its largest one.  Equal scores have to stay equal, and

@@ -287,6 +287,10 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
   P.window = b->window < P.most ? b->window : 0;
   const double sm = softmax_scale > 0.0f ? static_cast<double>(softmax_scale) : 1.0 / std::sqrt(128.0);
   P.c2 = static_cast<float>(1.4426950408889634074 * sm);
+  // A product of codes is below 448 * 448 * 128 * (1 + 2^-4) < 2^25, and c2 below 2^x.
+  int x = 0;
+  std::frexp(P.c2, &x);
+  P.k_most = 127 + 103 - std::max(x, 0);
   P.status = dev->status;
   PagedMaps M{};
   M.rows = static_cast<int32_t>(c->pages * c->heads * c->page);

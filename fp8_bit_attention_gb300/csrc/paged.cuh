@@ -259,6 +259,7 @@ struct PagedParams {
   int32_t most;             // tokens that a page table row holds
   int32_t unit;             // log2 of the key blocks between the places where work may be cut
   float c2;                 // softmax_scale * log2(e)
+  int32_t k_most;           // the largest scale of K that a product takes within FP32's range (many rows)
   int32_t q32, o32;         // rows of q, of o lie at multiples of 32 bytes
   unsigned int* status;
 };

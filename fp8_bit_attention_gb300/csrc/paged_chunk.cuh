@@ -91,7 +91,7 @@ struct ChunkShape {
 
 // A block's scales: those of K times the scores' factor to log2 units (the row's
 // factor is then a power of two, and a score less the row's maximum one exact
-// subtraction, however large both are), those of V as FP16 pairs 2^(e-E+7), or
+// subtraction, however large both are) over kmul, those of V as FP16 pairs 2^(e-E+7), or
 // 2^7 where they go into the weights.
 struct alignas(16) ChunkScales {
   float k[kChKeys];
@@ -100,6 +100,7 @@ struct alignas(16) ChunkScales {
   uint8_t ve[kChKeys];                             // wide: V's e, 0 for vectors of zeros
   int e;                                           // E, from the first wide block on unchanged
   int rare;                                        // 1: any such NaN, 2: wide
+  float kmul;                                      // 1, or what brings the largest scale of K down to k_most
 };
 
 // A tile's part.
@@ -530,28 +531,28 @@ __global__ void __launch_bounds__(kChThreads, 1)
           load(i + 1, kn, vn, rown);
           const uint32_t s = n % Sh::kScales;
           const int left = x.kv - ((x.k0 + i) * kChKeys + 4 * lane);
-          int most = -1, least = 255;
+          int most = -1, least = 255, kmost = 0;     // V's scales, the largest of K
           uint32_t nan = 0, zeros = 0;
+          bool poison = false;
+          float kmul = 1.0f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int ev = (vw >> (8 * j)) & 255u;
+          for (int j = 0; j < 4; ++j)
             if (j < left) {
-              if (ev == 255) {
-                nan |= 2u << (8 * j);
-              } else {
-                most = max(most, ev);
-                least = min(least, ev);
-              }
-              if (((kw >> (8 * j)) & 255u) == 255u) nan |= 1u << (8 * j);
+              const int ev = (vw >> (8 * j)) & 255u;
+              most = max(most, ev);
+              least = min(least, ev);
+              kmost = max(kmost, static_cast<int>((kw >> (8 * j)) & 255u));
             }
-          }
-          if (__any_sync(0xFFFFFFFFu, most > E || least < E - kChNear || wide)) {
-            // A vector of zeros has 127 by the format and counts for nothing.
+          if (__any_sync(0xFFFFFFFFu, most > E || least < E - kChNear || kmost > P.k_most || wide)) {
             most = -1;
             least = 255;
+            kmost = 0;
 #pragma unroll 1
             for (int j = 0; j < 4 && j < left; ++j) {
-              const int ev = (vw >> (8 * j)) & 255u;
+              const int ev = (vw >> (8 * j)) & 255u, ek = (kw >> (8 * j)) & 255u;
+              if (ek == 255) nan |= 1u << (8 * j);
+              else kmost = max(kmost, ek);
+              // A vector of zeros has 127 by the format and counts for nothing.
               uint32_t any = 1;
               if (ev == 127) {
                 const uint4* codes = reinterpret_cast<const uint4*>(P.c.v + static_cast<int64_t>(row + j) * 128);
@@ -563,6 +564,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 }
                 any &= 0x7F7F7F7Fu;
               }
+              if (ev == 255) nan |= 2u << (8 * j);
               if (ev == 255 || any == 0) {
                 zeros |= 255u << (8 * j);
               } else {
@@ -577,6 +579,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
               if (max(E, most) - low > kChSpread) wide = 2;      // and stays so
               if (!wide) E = max(E, most);
             }
+            poison = __any_sync(0xFFFFFFFFu, nan != 0);
+            kmul = exp2i(min(max(__reduce_max_sync(0xFFFFFFFFu, kmost) - P.k_most, 0), 127));
           }
           if (n >= Sh::kScales) ok = __all_sync(0xFFFFFFFFu, wait(sm.sc_empty[s], (n / Sh::kScales - 1) & 1));
           if (!ok) break;
@@ -584,7 +588,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
           float4 f;
           uint4 h;
           // Never 0, which would make a hidden key's score NaN.
-          auto kscale = [&](uint32_t ek) { return ek == 255u ? 1.0f : fmaxf(P.c2 * scale_value(ek), __uint_as_float(1u)); };
+          const float c2 = kmul == 1.0f ? P.c2 : P.c2 / kmul;
+          auto kscale = [&](uint32_t ek) { return ek == 255u ? 1.0f : fmaxf(c2 * scale_value(ek), __uint_as_float(1u)); };
           f.x = kscale(kw & 255u);
           f.y = kscale((kw >> 8) & 255u);
           f.z = kscale((kw >> 16) & 255u);
@@ -599,10 +604,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
           reinterpret_cast<uint4*>(sc.v)[lane] = h;
           reinterpret_cast<uint32_t*>(sc.nan)[lane] = nan;
           if (wide) reinterpret_cast<uint32_t*>(sc.ve)[lane] = vw & ~zeros;
-          const bool any = __any_sync(0xFFFFFFFFu, nan != 0);
           if (lane == 0) {
             sc.e = max(E, 0);
-            sc.rare = any | wide;
+            sc.rare = poison | wide;
+            sc.kmul = kmul;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&sm.sc_full[s]));
@@ -777,8 +782,15 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         tmem_wait_st();
       };
+      // The factor that is left of a score: a power of two, finite, so that a score of
+      // 0 stays 0; a NaN stays NaN.
+      auto row_factor = [&](const ChunkScales& sc) {
+        float y;
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(rowf * sc.kmul), "f"(1.7014118e38f));
+        return y;
+      };
       // The row's largest score of a step, in log2 units.
-      auto largest = [&](uint32_t tS, const float* sk) {
+      auto largest = [&](uint32_t tS, const float* sk, float rk) {
         float top = kNegInf;
 #pragma unroll 1
         for (int c = 0; c < kChStep; c += 32) {
@@ -792,7 +804,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             top = fmax3(top, __uint_as_float(y[k + 2]) * k4.z, __uint_as_float(y[k + 3]) * k4.w);
           }
         }
-        return top * rowf;
+        return top * rk;
       };
       auto rescale = [&](float f) {
 #pragma unroll 1
@@ -835,6 +847,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         const ChunkScales& sc = sm.sc[ss];
         if (sc.rare & 2) break;                    // wide: the loop below
+        const float rk = row_factor(sc);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
         // Two steps a block: scores in columns 64 half .., weights in 32 half ..
@@ -853,11 +866,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
         // blocks, without a reference) is the maximum looked for and are the
         // weights computed again.  P stays in registers until then, since it
         // overwrites S.
-        const uint64_t f2 = pack_f2(rowf, rowf);
+        const uint64_t f2 = pack_f2(rk, rk);
         const int Eb = sc.e;
         uint32_t w[32];
         float sum;
-        if (!begun && half == 0) m = largest(tS, sk);      // a part's first step has no reference to try
+        if (!begun && half == 0) m = largest(tS, sk, rk);      // a part's first step has no reference to try
 #pragma unroll 1
         for (int attempt = 0; attempt < 2; ++attempt) {
           const float shift = kChPBias - (m == kNegInf ? 0.0f : m);
@@ -886,7 +899,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (!again && Eb == E) break;
           float f = 1.0f;
           if (again) {
-            const float mn = fmaxf(m, largest(tS, sk));
+            const float mn = fmaxf(m, largest(tS, sk, rk));
             f = m == kNegInf ? 0.0f : ex2(m - mn);
             m = mn;
             l *= f;
@@ -941,7 +954,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           const uint8_t* ve = sc.ve + half * kChStep;
           const int key0 = (x.k0 + i) * kChKeys + half * kChStep, a = lo - key0, b = hi - key0;
           if (key0 < x.all_lo || key0 + kChStep - 1 > x.all_hi) hide(tS, a, b);
-          const float mn = fmaxf(m, largest(tS, sk)), ref = mn == kNegInf ? 0.0f : mn, down = m - ref;
+          const float rk = row_factor(sc), mn = fmaxf(m, largest(tS, sk, rk)), ref = mn == kNegInf ? 0.0f : mn, down = m - ref;
           float most = kNegInf;
 #pragma unroll 1
           for (int c = 0; c < kChStep; c += 32) {
@@ -950,7 +963,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             tmem_wait_ld32(y);
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              most = fmaxf(most, fmaf(__uint_as_float(y[k]) * sk[c + k], rowf, -ref) + static_cast<float>(ve[c + k]));
+              most = fmaxf(most, fmaf(__uint_as_float(y[k]) * sk[c + k], rk, -ref) + static_cast<float>(ve[c + k]));
           }
           const int En = max(0, max(__float2int_rd(static_cast<float>(E) + down), __float2int_rd(most)));
           if (begun || half == 1) rescale(m == kNegInf ? 0.0f : ex2(down + static_cast<float>(E - En)));
@@ -964,7 +977,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             tmem_wait_ld32(y);
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const float z = fmaf(__uint_as_float(y[k]) * sk[c + k], rowf, kChPBias - ref);
+              const float z = fmaf(__uint_as_float(y[k]) * sk[c + k], rk, kChPBias - ref);
               l += ex2(z);
               y[k] = __float_as_uint(ex2(z + static_cast<float>(ve[c + k] - E)));
             }

@@ -413,9 +413,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float& y = z[n][2 * i + j];
-            // (A rounded product: fused with the subtraction of the maximum it would
-            // differ from that by the maximum's rounding, which can be large.)
-            y = __fmul_rn((kTiles == 1 ? y + z2[n][2 * i + j] : y) * sk, rowf[n][j]);
+            // (The factors first: y * sk may pass FP32's range.  A rounded product:
+            // fused with the subtraction of the maximum it would differ from that by
+            // the maximum's rounding, which can be large.)
+            y = __fmul_rn(kTiles == 1 ? y + z2[n][2 * i + j] : y, sk * rowf[n][j]);
             top[n][j] = fmaxf(top[n][j], y);
           }
       }

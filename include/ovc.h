@@ -511,7 +511,9 @@ size_t ovc_paged_attention_workspace_bytes(const ovc_rows* q, const ovc_kv_cache
  * Scores, sums and outputs are FP32, weights FP16 with a unit of their row's own:
  * a key's weight times the size of its value is off by 2^-11 of itself and 2^-20
  * of the largest such term of the row, whatever the tokens that it does not see
- * hold.
+ * hold.  Queries and keys may have any finite size; a row may become NaN where
+ * its largest element times that of a key that it sees, times softmax_scale,
+ * passes FP32's range.
  * Long sequences are split over the GPU and joined from the workspace
  * (256-byte aligned); calls that share it must not overlap.  The way of
  * splitting depends on all lengths of the batch: the last bits of a sequence's

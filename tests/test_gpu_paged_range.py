@@ -172,3 +172,43 @@ def test_scores_far_apart(q_len, group, most, mul, power):
     assert ((o.double() - ref).abs() <= eo).all()
     assert ((lse.double() - ref_lse).abs() <= ds + 2.0 ** -20 + 2.0 ** -21 * ref_lse.abs()).all()
     assert ovc.device_status() == 0
+
+
+# --------------------------------------------------------------- sizes of keys
+@pytest.mark.parametrize("power", [118, -118])
+@pytest.mark.parametrize("q_len, group", ROWS)
+def test_large_keys_and_small_queries(q_len, group, power):
+    """Scores of ordinary size, whatever the sizes they come from."""
+    c = Case([q_len], [700], 2, group, 32, seed=36)
+    c.k = c.k * 2.0 ** power
+    c.q = c.q * 2.0 ** -power
+    _rewrite(c)
+    o, lse = c.run(return_lse=True)
+    c.check(o, lse)
+
+
+@pytest.mark.parametrize("q_len, group", ROWS)
+def test_a_huge_key_reaches_only_the_rows_that_see_it(q_len, group):
+    """Later rows have a single weight, or that token's is 0."""
+    n = 700
+    at = n - q_len + q_len // 2 + 1
+    row = at - (n - q_len)
+    c = Case([q_len], [n], 2, group, 32, seed=37)
+    c.k[at] = 0.0
+    c.k[at, :, 9] = 1e37
+    c.q[..., 9] = torch.where(c.q[..., 9] < 0, -1.0, 1.0)
+    _rewrite(c)
+    o, lse = c.run(return_lse=True)
+    _check(c, o, lse, slice(0, row))
+    k, v = c.dense()[0]
+    only = v[at].repeat_interleave(group, 0).unsqueeze(0).expand(q_len - row, -1, -1)
+    up = c.q[row:, :, 9] > 0
+    assert torch.equal(o[row:][up].double(), only[up].float().to(torch.bfloat16).double())
+    # where it has no weight: the definition without it
+    c.k[at, :, 9] = -1e37
+    c.q[..., 9] = c.q[..., 9].abs()
+    _rewrite(c)
+    o, lse = c.run(return_lse=True)
+    c.k[at, :, 9] = -2000.0
+    _rewrite(c)
+    _check(c, o, lse)

@@ -401,14 +401,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
         if (!ok) break;
       }
       if (lane == 0) write_cut<kChRows, kChKeys>(P, share, work);
-      if (!ok) {
-        give_up();
-        // The copies in flight end by themselves; shared memory must outlive them.
-        for (uint32_t i = n > Sh::kK ? n - Sh::kK : 0; i < n; ++i)
-          paged_wait(smem_addr(&sm.k_full[i % Sh::kK]), (i / Sh::kK) & 1, 4000000000ull, &sm.zero);
-        for (uint32_t i = nv > Sh::kV ? nv - Sh::kV : 0; i < nv; ++i)
-          paged_wait(smem_addr(&sm.v8_full[i % Sh::kV]), (i / Sh::kV) & 1, 4000000000ull, &sm.zero);
-      }
+      if (!ok) give_up();
+      // The CTA's shared memory must outlive the copies in flight, also where others
+      // give up on them after this warp's last wait.
+      for (uint32_t i = n > Sh::kK ? n - Sh::kK : 0; i < n; ++i)
+        paged_wait(smem_addr(&sm.k_full[i % Sh::kK]), (i / Sh::kK) & 1, 4000000000ull, &sm.zero);
+      for (uint32_t i = nv > Sh::kV ? nv - Sh::kV : 0; i < nv; ++i)
+        paged_wait(smem_addr(&sm.v8_full[i % Sh::kV]), (i / Sh::kV) & 1, 4000000000ull, &sm.zero);
     } else if (warp == 13) {
       // --------------------------------------------------------- the products
       // By one warp, the halves in turn: with a warp for each the two fall into

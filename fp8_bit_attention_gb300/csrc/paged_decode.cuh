@@ -278,9 +278,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecodeCtas<kTiles>)
       }
     }
     if (lane == 0) write_cut<R, kDecKeys>(P, share, work);
-    // After a timeout copies may still be in flight: they end by themselves, and
-    // the CTA's shared memory must outlive them.
-    if (*abort_flag && lane < kDecWarps)
+    // The CTA's shared memory must outlive the copies in flight, also where the
+    // computing warps give up on them after this warp's last look at the flag.
+    if (lane < kDecWarps)
       for (uint32_t n = issued > kDecStages ? issued - kDecStages : 0; n < issued; ++n)
         paged_wait(smem_addr(&sm.full[lane][n % kDecStages]), (n / kDecStages) & 1, 4000000000ull, &sm.zero);
     return;

@@ -381,7 +381,9 @@ def attention_probe(prep: Prepared, rep: Repair | None = None, *, softmax_scale=
 
 
 def device_status(stream=None) -> int:
-    """Synchronise and return (and clear) the device-side status (0 = ok)."""
+    """Synchronise and return (and clear) a device-side status: 0 for none, 5 for
+    a wait that ran out, 7 for an index out of range in a paged call (after 5, if
+    both are there)."""
     return int(lib().ovc_get_device_status(ctypes.c_void_p(_stream_handle(stream))))
 
 

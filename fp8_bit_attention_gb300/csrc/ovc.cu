@@ -29,6 +29,9 @@ __device__ unsigned int g_status;
 
 namespace {
 
+__global__ void clear_status_kernel(unsigned int bit) { atomicAnd(&g_status, ~bit); }
+
+
 // The instantiations of the attention kernel, by variant bits: 0-7, 8
 // (V-Smooth), 16-23 (Q smoothing), 32-35 and 48-51 (repair), and the
 // P-byte dump of the probe call with the method, the baseline variants, Q
@@ -700,12 +703,13 @@ ovc_status ovc_get_device_status(void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return OVC_ERR_CUDA;
   unsigned int word = 0;
   if (cudaMemcpyFromSymbol(&word, g_status, sizeof(word)) != cudaSuccess) return OVC_ERR_CUDA;
-  if (word != 0) {
-    const unsigned int zero = 0;
-    if (cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return OVC_ERR_CUDA;
-    return (word & kStatusTimeout) ? OVC_ERR_TIMEOUT : OVC_ERR_BAD_INDEX;
-  }
-  return OVC_OK;
+  if (word == 0) return OVC_OK;
+  // Only what is reported is cleared, by an atomic: another bit, or one that a
+  // kernel on another stream sets meanwhile, is for the next call.
+  const unsigned int bit = word & kStatusTimeout ? kStatusTimeout : kStatusBadIndex;
+  clear_status_kernel<<<1, 1, 0, s>>>(bit);
+  if (launch_status() != OVC_OK || cudaStreamSynchronize(s) != cudaSuccess) return OVC_ERR_CUDA;
+  return bit == kStatusTimeout ? OVC_ERR_TIMEOUT : OVC_ERR_BAD_INDEX;
 }
 
 const char* ovc_status_string(ovc_status s) {

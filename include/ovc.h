@@ -211,8 +211,10 @@ ovc_status ovc_prepare_v_repair(const ovc_tensor* v, const ovc_prepared* p, floa
 ovc_status ovc_attention_v_repair(const ovc_prepared* p, const ovc_repair* r, float softmax_scale,
                                   const ovc_output* o, void* stream);
 
-/* Synchronise `stream`, then report and clear the device-side status word:
- * OVC_ERR_TIMEOUT if any kernel gave up on a wait since the last call. */
+/* Synchronise `stream`, then report and clear a device-side status:
+ * OVC_ERR_TIMEOUT if any kernel gave up on a wait, OVC_ERR_BAD_INDEX if a paged
+ * call met an index out of range, since it was last reported.  Where both hold,
+ * the first call reports the former and the next one the latter. */
 ovc_status ovc_get_device_status(void* stream);
 
 /* A static English description of a status code. */

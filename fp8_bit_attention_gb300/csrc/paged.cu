@@ -261,6 +261,9 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
   if (st != OVC_OK) return st;
   if (o->T != q->T || o->H != q->H || o->dtype != OVC_BF16 || (lse && !at4(lse))) return OVC_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return OVC_ERR_INVALID_ARG;
+  const double sm = softmax_scale <= 0.0f ? 1.0 / std::sqrt(128.0) : static_cast<double>(softmax_scale);
+  const float c2 = static_cast<float>(1.4426950408889634074 * sm);
+  if (!std::isfinite(c2)) return OVC_ERR_INVALID_ARG;
   if (workspace_bytes < ovc_paged_attention_workspace_bytes(q, c, b)) return OVC_ERR_WORKSPACE_TOO_SMALL;
   DeviceState* dev = nullptr;
   st = device_state(&dev);
@@ -285,8 +288,7 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
   P.by_page = fast_div(P.c.page);
   P.causal = b->causal;
   P.window = b->window < P.most ? b->window : 0;
-  const double sm = softmax_scale > 0.0f ? static_cast<double>(softmax_scale) : 1.0 / std::sqrt(128.0);
-  P.c2 = static_cast<float>(1.4426950408889634074 * sm);
+  P.c2 = c2;
   // A product of codes is below 448 * 448 * 128 * (1 + 2^-4) < 2^25, and c2 below 2^x.
   int x = 0;
   std::frexp(P.c2, &x);

@@ -232,7 +232,8 @@ def paged_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, k
     ``q[cu_q[b]:cu_q[b+1]]``, its last tokens.  ``max_q``, the most rows of any
     sequence if known, only chooses between kernels.  ``causal``: a row sees the
     keys up to its own position, with ``window`` only the last `window` of them;
-    otherwise all keys of its sequence.
+    otherwise all keys of its sequence.  ``softmax_scale``: finite; 1/sqrt(128) if
+    not given or not positive.
 
     Returns O, BF16 shaped like q (with ``return_lse`` also the FP32 [T, query
     heads] natural log-sum-exp of the scaled scores).  A row that sees no key

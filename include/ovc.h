@@ -506,10 +506,11 @@ size_t ovc_paged_attention_workspace_bytes(const ovc_rows* q, const ovc_kv_cache
 
 /* o[t,h] = softmax(q[t,h] . K * softmax_scale) V over the keys that row t sees,
  * KV head h / (q->H / c->heads); q->H is a multiple of c->heads.  o is BF16,
- * shaped like q; its rows overlap neither each other nor q's.  lse, if not NULL, receives the natural log-sum-exp of the
- * scaled scores, FP32 [T, H] contiguous.  softmax_scale <= 0 selects
- * 1/sqrt(128).  A query row that holds a NaN or an infinity gives NaN, unless
- * it sees no key.
+ * shaped like q; its rows overlap neither each other nor q's.  lse, if not NULL,
+ * receives the natural log-sum-exp of the scaled scores, FP32 [T, H] contiguous.
+ * softmax_scale <= 0 selects 1/sqrt(128); NaN, and what passes FP32's range times
+ * log2(e), is refused.  A query row that holds a NaN or an infinity gives NaN,
+ * unless it sees no key.
  * Scores, sums and outputs are FP32, weights FP16 with a unit of their row's own:
  * a key's weight times the size of its value is off by 2^-11 of itself and 2^-20
  * of the largest such term of the row, whatever the tokens that it does not see

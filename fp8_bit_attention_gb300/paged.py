@@ -156,7 +156,8 @@ def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torc
 
 def kv_cache_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
     """The keys and values of the tokens in ``slots`` (int32 [T]) as a pair of
-    `dtype` (bfloat16 or float16) tensors [T, heads, 128], or in the pair `out`.
+    `dtype` (bfloat16 or float16) tensors [T, heads, 128], or in the pair `out`,
+    whose rows must not overlap.
     Negative slots give zeros; so do slots beyond the cache, which
     :func:`device_status` reports (7)."""
     dev = _device(cache.k, slots, *(out or ()), stream=stream)
@@ -170,6 +171,8 @@ def kv_cache_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype = t
         for x in out:
             if tuple(x.shape) != (n, cache.heads, 128) or x.dtype != out[0].dtype:
                 raise ValueError(f"out must be a pair of [{n}, {cache.heads}, 128] tensors of one dtype")
+        if n and out[0].data_ptr() == out[1].data_ptr():
+            raise ValueError("out must be two tensors that do not overlap")
 
     def run(s):
         pair = out if out is not None else tuple(

@@ -34,3 +34,18 @@ def test_each_status_is_reported_in_its_turn():
     assert [ovc.device_status() for _ in range(3)] == [TIMEOUT, BAD_INDEX, 0]
     ovc.kv_cache_write(c, x, x, _i32([32]))
     assert [ovc.device_status() for _ in range(2)] == [BAD_INDEX, 0]
+
+
+def test_one_tensor_for_keys_and_values_is_refused():
+    """Each of its rows would hold parts of both."""
+    c = ovc.kv_cache(2, 3, 16)
+    x = torch.ones((5, 3, 128), dtype=torch.bfloat16, device="cuda")
+    slots = _i32([1, 2, 3, 4, 20])
+    ovc.kv_cache_write(c, x, 2 * x, slots)
+    pair = torch.zeros((5, 6, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        ovc.kv_cache_read(c, slots, out=(pair[:, :3], pair[:, :3]))
+    k, v = ovc.kv_cache_read(c, slots, out=(pair[:, :3], pair[:, 3:]))
+    assert (k == 1).all() and (v == 2).all() and ovc.device_status() == 0
+    none = pair[:0, :3]
+    ovc.kv_cache_read(c, _i32([]), out=(none, none))

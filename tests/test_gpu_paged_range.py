@@ -212,3 +212,25 @@ def test_a_huge_key_reaches_only_the_rows_that_see_it(q_len, group):
     c.k[at, :, 9] = -2000.0
     _rewrite(c)
     _check(c, o, lse)
+
+
+# --------------------------------------------------------------- sizes of queries
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("q_len, group", ROWS)
+def test_a_query_channel_far_above_the_others(q_len, group, dtype):
+    """The large channel's keys are small.  A query element is off by what lies
+    below 2^-18 of its row's largest: half a subnormal step of E4M3, 2^-10, where
+    the largest is scaled to between 224 and 448, is 2^-17.8 of it.  Each score is
+    off by that much times scale * sum |k| more."""
+    c = Case([q_len], [700], 2, group, 32, dtype, seed=39)
+    c.q[..., 7] *= 2.0 ** 8
+    c.k[..., 7] *= 2.0 ** -8
+    _rewrite(c)
+    o, lse = c.run(return_lse=True)
+    dense = c.dense()
+    ref, ref_lse, av, sq = attention(c.q, dense, c.q_lens, c.kv_lens, c.group)
+    amax = c.q.double().abs().amax(-1)
+    k1 = dense[0][0].abs().sum(-1).amax(0).repeat_interleave(group)
+    more = 2.0 ** -17.8 * amax * k1 / math.sqrt(128.0)
+    eo, el = error_bounds(ref, ref_lse, av, sq + 2.0 ** 15 * more)
+    assert ((o.double() - ref).abs() <= eo).all() and ((lse.double() - ref_lse).abs() <= el).all()

@@ -96,7 +96,7 @@ __device__ __forceinline__ int tile_places(const PagedParams& P, int t0, int t1)
 struct Share {
   Seq s;
   int b, h, i, off, t0, t1;
-  int len, at, share;
+  int len, share;
 };
 
 struct PlanSmem {
@@ -199,7 +199,7 @@ __device__ Share plan_share(const PagedParams& P, PlanSmem& sm, int min_share) {
   // hand, a longer one adds them up again.
   auto found = [&](const Seq& s, int b, int i, int rem, int t0, int t1) {
     const int n = tile_places<BK>(P, t0, t1), h = static_cast<unsigned>(rem) / static_cast<unsigned>(n);
-    sm.found = Share{s, b, h, i, rem - h * n, t0, t1, min(share, total - static_cast<int>(at)), static_cast<int>(at), share};
+    sm.found = Share{s, b, h, i, rem - h * n, t0, t1, min(share, total - static_cast<int>(at)), share};
   };
   int base = 0;
 #pragma unroll 1

@@ -115,8 +115,8 @@ int common_divisor(int a, int b) { return b ? common_divisor(b, a % b) : a; }
 constexpr uint64_t kTimeoutNs = 4000000000ull;    // 4 s per wait
 constexpr int kMaxSms = 160;                      // that a persistent grid uses
 // The least share worth a CTA.  16, 8 and 4 blocks of 16 keys: 1 sequence of 1024
-// keys, 2 KV heads 13.7, 12.3, 12.5 us; with 8 KV heads and 16 rows 16.4, 14.4,
-// 14.7 us; longer calls alike.  2 to 8 blocks of 128: alike.
+// keys, 8 KV heads and 16 rows 16.5, 14.5, 15.1 us; other calls alike.  2 to 8
+// blocks of 128: alike.
 constexpr int kDecodeMinShare = 8;                // blocks of 16 keys
 constexpr int kChunkMinShare = 4;                 // blocks of 128 keys
 
@@ -124,17 +124,22 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Query rows of a tile: the smallest of the kernels' that holds a sequence's
 // rows of one KV head.  Tiles of 8, 16 and 256 (a call of at most 128 rows works
-// on 128), times in us:
-//                                        rows     8      16     256
-//   1 sequence of 1024 keys, 8 heads         8    12.4   14.4   16.6
-//   16 sequences of 8192, 8 heads            8    55     76     75
-//   256 sequences of 256, 8 heads           16    66     72     107
-//   16 sequences of 8192, 8 heads           16    94     80     75
-//   8 sequences of 65536, 8 heads           16    323    253    232
-//   1 sequence of 1024, 8 heads             32    14.4   16.4   18.2
-//   16 sequences of 8192, 8 heads           32    166    142    76
-// For 9 to 16 rows the middle one is never far off; which of the others is best
-// depends on lengths that the host does not know.
+// on 128), 8 KV heads, times in us with queries in BF16 and FP16:
+//                              rows       8            16           256
+//   1 sequence of 1024 keys      8    12.6  12.4   13.4  12.4   16.6  16.5
+//                               16    12.6  12.6   14.5  13.9   16.6  18.5
+//                               32    14.6  14.5   16.6  14.5   18.6  18.6
+//   256 sequences of 256         8      43    41     64    53    107   113
+//                               16      66    64     71    60    111   115
+//                               32     121   117    127   103    111   115
+//   16 sequences of 8192         8      55    54     76    62     77   110
+//                               16      92    92     80    68     76   111
+//                               32     163   162    142   117     78   111
+//   8 sequences of 65536         8     170   169    241   197    236   359
+//                               16     322   321    249   202    237   359
+//                               32     623   622    471   379    237   360
+// For 9 to 16 rows the middle one is the best with FP16, and never far off with
+// BF16, where the best depends on lengths that the host does not know.
 int tile_rows(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b) {
   const int64_t group = q->H / c->heads;
   const int64_t most = (b->cu_q ? (b->max_q > 0 ? b->max_q : q->T) : 1) * group;

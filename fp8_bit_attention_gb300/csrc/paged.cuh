@@ -103,7 +103,8 @@ struct RowsView {
   int64_t st, sh;   // element strides
 };
 
-// Division of 0 <= n < 2^31 by a number known at the launch: with 2^(s-1) < d <=
+// Division of 0 <= n < 2^31 by a number known at the launch (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994): with 2^(s-1) < d <=
 // 2^s and m = floor(2^32 (2^s - d) / d) + 1, n / d = (m n / 2^32 + n) >> s.  (A
 // division by a register is about 20 dependent instructions, and a CTA does a
 // dozen of them before its first load.)

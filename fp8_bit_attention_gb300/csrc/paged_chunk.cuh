@@ -29,11 +29,15 @@
 // softmax 1500 to 1870 of its four warps while the others run (900 alone), and
 // two turns in step 2900.  Calls of many tiles with few keys, what a tile costs
 // beside its blocks: 8 us (Q's rows in, their conversion, the first scores, O's
-// rows out; one CTA fills the SM, so nothing covers them).  Few rows over many
-// keys ("solo"), V's conversion and the softmax: 8 x 65536 keys x 8 heads for 32
-// rows 232 us, 69% of a copy's rate.  Instructions are a resource: every warp role
-// runs its own code at once, and waiting for instructions was the second largest
-// stall, so what is not in the inner loop is kept in loops of little code.
+// rows out; one CTA fills the SM, so nothing covers them): 8 prompts of 512 tokens
+// 55 us, a prompt of 1024 tokens 53 us, a batch of chunks and short sequences 82 us.
+// Few rows over many keys ("solo"): 8 x 65536 keys x 8 heads for 32 rows 237 us, 67%
+// of a copy's rate.  Without V's conversion and softmax such a call took 200 of 232
+// us, so more than half of the gap lies elsewhere, and FP16, with one stage of V's
+// codes and two of K's, takes 360: too few bytes are on their way.  Instructions
+// are a resource: every warp role runs its own code at once, and waiting for
+// instructions was the second largest stall, so what is not in the inner loop is
+// kept in loops of little code, or of its own.
 //
 // Measured and left out (ms for 4096 over 65536; the kernel of the time in
 // brackets): scores of 64 keys in two buffers a half 3.5 (3.1); 16 softmax warps,
@@ -56,7 +60,7 @@
 // its scales and they go into the weights, which are then 2^7 p 2^(e - E) with an E
 // of each row's own, of the largest p 2^e that it sees: a token counts by its term
 // and one that is masked not at all.  Either way no more than 2^-20 of a row's
-// largest term is lost.
+// largest term is lost.  (All blocks wide: 4096 over 65536 9.1 ms, 32 rows 648 us.)
 #pragma once
 
 #include "paged_decode.cuh"

@@ -7,16 +7,16 @@
 // heads, group 7: 35 us, 56%, the rest being the start, the tiles' ends and the
 // join.  Short calls (1024 keys: 12 us) are bound by their two launches and the
 // latency of a chain of loads.  With 9 to 16 rows (kTiles = 2) the products and
-// conversions of two tiles bound it: 8 x 65536 keys, 8 heads: 253 us, 63%.
+// conversions of two tiles bound it: 8 x 65536 keys, 8 heads: 249 us with BF16
+// queries (64%), whose kernel spills some registers, 202 us with FP16 (79%).
 //
 // A CTA is a loading warp and four computing ones.  The
 // loading warp walks the CTA's share, looks up pages, and streams 16-key blocks
 // (2 KB of K, 2 KB of V) by TMA into a ring for each computing warp, which keeps
 // its own running maximum, sum and output in registers; no barrier joins the
 // warps until a tile's part ends.  Several such CTAs share an SM, so that one's
-// ends and starts lie under the others' streams: 3 CTAs of 3 stages (the two
-// calls above: 324 and 35 us when chosen) against 4 of 2 stages (326, 39) and one
-// CTA of 8 warps and 32-key blocks (334, 60).
+// ends and starts lie under the others' streams: 3 CTAs of 3 stages, against 4
+// of 2 stages 319 and 323 us, 34.7 and 36.4 us for the two calls above.
 //
 // The products run transposed, S^T = K Q^T and O^T = V^T P^T, with
 // mma.m16n8k16: keys and channels fill the 16 rows of the instruction, and the
@@ -43,6 +43,7 @@
 // 2^kDecSpread.  Beyond that ("wide") every row has its own, of the largest
 // p 2^e that it sees, so that a token counts by its term and one that is masked
 // not at all.  Either way no more than 2^-20 of a row's largest term is lost.
+// (All blocks wide: the first call above 368 us, 16 rows 380.)
 #pragma once
 
 #include <cuda.h>

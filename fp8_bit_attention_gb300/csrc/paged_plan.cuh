@@ -59,19 +59,19 @@ __device__ __forceinline__ int tiles_of(const PagedParams& P, const Seq& s) {
 
 // What a tile costs beside its key blocks (query rows in, the warps' join, rows
 // out), in blocks: each tile stands for so many more blocks on the line, behind
-// its own, where there is nothing to do.  (Blocks of 128 keys, measured: a block
-// takes 1.7 us, a tile's start and end 8 us.  A cost of 2, 3, 4: 8 sequences of
-// 500 ragged tokens 116, 104, 104 us, 8 x 512 tokens of prefill 82, 79, 77 us;
-// later, 4, 5, 6: the first 85, 89, 90 us, 16 x 4 tokens over 8192 keys 25, 28,
-// 27 us.)
+// its own, where there is nothing to do.  (3, 4 and 5 for blocks of 128 keys: 8
+// ragged sequences of up to 500 tokens with a window of 4096 89, 82, 88 us; 16 x 4
+// tokens over 8192 keys 27, 25, 27 us; a prompt of 1024 tokens 53, 53, 57 us.  4, 8
+// and 16 for blocks of 16: 32 single tokens over ragged contexts 43, 35, 35 us; 256
+// sequences of 256 keys, 16 rows, 75, 71, 72 us.)
 template <int BK>
 constexpr int kTileCost = BK < 128 ? 8 : 4;
 
 // A cut so near a tile's start or end is moved there: so few blocks are not worth
-// a part of their own, with its partial results and their join (with against
-// without: 8 x 512 tokens of prefill 68 and 76 us, 16 x 4 tokens over 8192 keys, 8
-// heads, 92 and 101 us; for 128-key blocks 2, 3, 4: the latter with one head 25,
-// 25, 29 us).
+// a part of their own, with its partial results and their join.  (0, 2, 3 and 4 for
+// blocks of 128 keys: 8 prompts of 512 tokens 64, 55, 55, 55 us; 8 ragged sequences
+// with a window 84, 83, 82, 82 us; 16 x 4 tokens over 8192 keys 25, 25, 25, 29 us.
+// 0 and 4 for blocks of 16: 256 sequences of 256 keys, 16 rows, 74 and 71 us.)
 template <int BK>
 constexpr int kSnap = BK < 128 ? 4 : 3;
 

@@ -514,7 +514,7 @@ size_t ovc_paged_attention_workspace_bytes(const ovc_rows* q, const ovc_kv_cache
  * Scores, sums and outputs are FP32, weights FP16 with a unit of their row's own:
  * a key's weight times the size of its value is off by 2^-11 of itself and 2^-20
  * of the largest such term of the row, whatever the tokens that it does not see
- * hold.  Of a query row what lies below 2^-18 of its largest element may be lost.
+ * hold.  An element of a query may be off by 2^-17 of its row's largest.
  * Queries and keys may have any finite size; a row may become NaN where
  * its largest element times that of a key that it sees, times softmax_scale,
  * passes FP32's range.

@@ -29,8 +29,9 @@
 // softmax 1500 to 1870 of its four warps while the others run (900 alone), and
 // two turns in step 2900.  Calls of many tiles with few keys, what a tile costs
 // beside its blocks: 8 us (Q's rows in, their conversion, the first scores, O's
-// rows out; one CTA fills the SM, so nothing covers them): 8 prompts of 512 tokens
-// 55 us, a prompt of 1024 tokens 53 us, a batch of chunks and short sequences 82 us.
+// rows out; one CTA fills the SM, so nothing covers them): 8 prompts of 512 tokens,
+// 32 heads, 55 us, one of 1024 tokens 39 us, a batch of chunks and short sequences
+// 81 us.
 // Few rows over many keys ("solo"): 8 x 65536 keys x 8 heads for 32 rows 237 us, 67%
 // of a copy's rate.  Without V's conversion and softmax such a call took 200 of 232
 // us, so more than half of the gap lies elsewhere, and FP16, with one stage of V's

@@ -61,7 +61,7 @@ __device__ __forceinline__ int tiles_of(const PagedParams& P, const Seq& s) {
 // out), in blocks: each tile stands for so many more blocks on the line, behind
 // its own, where there is nothing to do.  (3, 4 and 5 for blocks of 128 keys: 8
 // ragged sequences of up to 500 tokens with a window of 4096 89, 82, 88 us; 16 x 4
-// tokens over 8192 keys 27, 25, 27 us; a prompt of 1024 tokens 53, 53, 57 us.  4, 8
+// tokens over 8192 keys 27, 25, 27 us; a prompt of 1024 tokens, 56 heads, 53, 53, 57 us.  4, 8
 // and 16 for blocks of 16: 32 single tokens over ragged contexts 43, 35, 35 us; 256
 // sequences of 256 keys, 16 rows, 75, 71, 72 us.)
 template <int BK>

@@ -234,3 +234,66 @@ def test_a_query_channel_far_above_the_others(q_len, group, dtype):
     more = 2.0 ** -17.8 * amax * k1 / math.sqrt(128.0)
     eo, el = error_bounds(ref, ref_lse, av, sq + 2.0 ** 15 * more)
     assert ((o.double() - ref).abs() <= eo).all() and ((lse.double() - ref_lse).abs() <= el).all()
+
+
+# ------------------------------------------------------------ all of it at once
+def _largest_terms(c, dense, causal=True, window=None):
+    """max_j p_j * 448 * 2^(e_j - 127) of every row (at most: twice the largest
+    magnitude of the vector), NaN tokens left out."""
+    out, at = [], 0
+    for (k, v), ql, kl in zip(dense, c.q_lens, c.kv_lens):
+        x = c.q[at:at + ql].double()
+        at += ql
+        k, big = (t.repeat_interleave(c.group, 1) for t in (torch.nan_to_num(k), 2.0 * torch.nan_to_num(v).abs().amax(-1)))
+        s = torch.einsum("thd,jhd->thj", x, k) / math.sqrt(128.0)
+        j, pos = torch.arange(kl, device="cuda"), torch.arange(kl - ql, kl, device="cuda").unsqueeze(1)
+        seen = (j <= pos) if causal else torch.ones((ql, kl), dtype=torch.bool, device="cuda")
+        if window:
+            seen = seen & (j > pos - window)
+        p = torch.softmax(torch.where(seen.unsqueeze(1), s, -math.inf), -1)
+        out.append((p * big.T).amax(-1))
+    return torch.cat(out)
+
+
+@pytest.mark.parametrize("mode", ["causal", "window", "all"])
+@pytest.mark.parametrize("dtype, spread", [(torch.bfloat16, 40), (torch.float16, 12)])
+@pytest.mark.parametrize("q_lens, group", [((1, 3), 2), ((4, 4), 4), ((9, 2), 8), ((70, 150), 4)])
+def test_wide_values_and_nan_tokens_in_long_sequences(q_lens, group, dtype, spread, mode):
+    """Parts cut between CTAs, zero vectors and tokens that are not finite among
+    values of every size."""
+    kw = {"causal": dict(), "window": dict(window=301), "all": dict(causal=False)}[mode]
+    lens = [6000, 2111]
+    c = Case(q_lens, lens, 2, group, 48, dtype, seed=42, k_mul=2.0, v_spread=spread)
+    c.v[::7] = 0.0
+    rows = sum(q_lens)
+    if mode != "all":
+        c.v[lens[0] - q_lens[0] // 2 - 1, 0, 3] = math.inf      # the last rows of the first sequence see it
+        c.k[sum(lens) - 1, 1, 77] = math.nan                    # the last row of the second
+    _rewrite(c)
+    o, lse = c.run(return_lse=True, **kw)
+    dense = c.dense()
+    ref, ref_lse, av, sq = attention(c.q, dense, c.q_lens, c.kv_lens, group, **kw)
+    want = torch.isnan(ref).any(-1) | torch.isnan(ref_lse)
+    assert torch.equal(torch.isnan(o).any(-1), want) and torch.equal(torch.isnan(o).all(-1), want)
+    assert int(want.sum()) == (0 if mode == "all" else group * (q_lens[0] // 2 + 1 + 1))
+    eo, el = error_bounds(ref, ref_lse, av, sq)
+    seen = 301 if mode == "window" else max(lens)
+    eo = eo + 2.0 ** -20 * seen * _largest_terms(c, dense, **kw).unsqueeze(-1)
+    ok = ~want
+    assert ((o.double() - ref).abs() <= eo)[ok].all() and ((lse.double() - ref_lse).abs() <= el)[ok].all()
+    o2, lse2 = c.run(return_lse=True, **kw)
+    assert torch.equal(o.nan_to_num(), o2.nan_to_num()) and torch.equal(lse.nan_to_num(), lse2.nan_to_num())
+    assert o.shape[0] == rows and ovc.device_status() == 0
+
+
+@pytest.mark.parametrize("q_len, group", ROWS)
+def test_fp16_queries_over_a_huge_bf16_key(q_len, group):
+    n = 700
+    at = n - q_len + q_len // 2 + 1
+    c = Case([q_len], [n], 2, group, 32, seed=43)
+    c.k[at] = 3e38
+    c.v[at] = -3e38
+    _rewrite(c)
+    c.q = c.q.half()
+    o, lse = c.run(return_lse=True)
+    _check(c, o, lse, slice(0, at - (n - q_len)))

@@ -28,6 +28,7 @@ OVC_ATTN_NATURAL_ORDER = 2
 OVC_ATTN_BASELINE = 3
 OVC_BF16 = 0
 OVC_FP16 = 1
+OVC_FP32 = 2
 
 
 class OvcTensor(ctypes.Structure):
@@ -78,6 +79,17 @@ class OvcPagedBatch(ctypes.Structure):
                 ("cu_q", c_ptr), ("max_q", c_i32), ("causal", c_i32), ("window", c_i32)]
 
 
+class OvcKVPages(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("pages", c_i64), ("width", c_i32), ("page", c_i32), ("page_table", c_ptr),
+                ("kv_lens", c_ptr), ("refs", c_ptr)]
+
+
+class OvcDrafts(ctypes.Structure):
+    _fields_ = [("B", c_i64), ("N", c_i64), ("V", c_i64), ("cu_drafts", c_ptr), ("drafts", c_ptr), ("target", c_ptr),
+                ("draft", c_ptr), ("dtype", c_i32), ("target_stride", c_i64), ("draft_stride", c_i64),
+                ("accept_u", c_ptr), ("sample_u", c_ptr)]
+
+
 P = ctypes.POINTER
 SIGNATURES = {
     "ovc_prepare_workspace_bytes": (ctypes.c_size_t, [c_i64, c_i64, c_i64, c_i64]),
@@ -114,6 +126,12 @@ SIGNATURES = {
     "ovc_paged_attention_workspace_bytes": (ctypes.c_size_t, [P(OvcRows), P(OvcKVCache), P(OvcPagedBatch)]),
     "ovc_paged_attention": (c_i32, [P(OvcRows), P(OvcKVCache), P(OvcPagedBatch), ctypes.c_float, P(OvcRows), c_ptr, c_ptr,
                                     ctypes.c_size_t, c_ptr]),
+    "ovc_kv_pages_reserve": (c_i32, [P(OvcKVPages), c_ptr, c_ptr, c_ptr]),
+    "ovc_kv_pages_release": (c_i32, [P(OvcKVPages), c_ptr, c_ptr]),
+    "ovc_kv_pages_fork": (c_i32, [P(OvcKVPages), c_ptr, c_ptr, c_i64, c_ptr]),
+    "ovc_kv_copy": (c_i32, [P(OvcKVCache), P(OvcKVCache), c_ptr, c_ptr, c_ptr, c_i64, c_ptr]),
+    "ovc_kv_compact": (c_i32, [P(OvcKVCache), P(OvcKVPages), c_ptr, c_i64, c_ptr, c_i64, c_ptr]),
+    "ovc_verify_drafts": (c_i32, [P(OvcDrafts), c_ptr, c_ptr, c_ptr]),
 }
 
 _lock = threading.Lock()

@@ -8,10 +8,11 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SRCS = [os.path.join(CSRC, f) for f in ("ovc.cu", "paged.cu")]
+SRCS = [os.path.join(CSRC, f) for f in ("ovc.cu", "paged.cu", "serve.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("ptx.cuh", "prepare.cuh", "attention.cuh", "repair.cuh", "group.cuh",
                                            "host_stream.cuh", "host.cuh", "paged.cuh", "paged_plan.cuh",
-                                           "paged_decode.cuh", "paged_chunk.cuh")]
+                                           "paged_decode.cuh", "paged_chunk.cuh", "paged_args.cuh", "pages.cuh", "move.cuh",
+                                           "drafts.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libovc.so")

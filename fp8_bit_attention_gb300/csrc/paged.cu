@@ -12,6 +12,7 @@
 #include "ovc.h"
 #include "host.cuh"
 #include "paged.cuh"
+#include "paged_args.cuh"
 #include "paged_chunk.cuh"
 #include "paged_decode.cuh"
 
@@ -19,17 +20,6 @@ namespace ovc {
 namespace {
 
 static_assert(kPagedBadIndex == kStatusBadIndex, "status bits");
-
-bool at16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool at4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-bool cache_ok(const ovc_kv_cache* c) {
-  if (!c || c->pages < 1 || c->heads < 1 || c->page < 16 || c->page > 1024 || c->page % 16) return false;
-  if (!at16(c->k) || !at16(c->v) || !at16(c->k_scale) || !at16(c->v_scale)) return false;
-  constexpr int64_t kMost = (int64_t{1} << 31) - 1024;
-  return c->heads <= 65535 && c->pages <= kMost && c->pages * c->page <= kMost &&
-         c->pages * c->page * c->heads <= kMost;
-}
 
 ovc_status rows_ok(const ovc_rows* r) {
   if (!r || r->T < 1 || r->H < 1 || r->T > 0x7FFFFC00 || r->H > 65535 * 256) return OVC_ERR_INVALID_ARG;
@@ -52,14 +42,7 @@ bool at32(const ovc_rows* r) {
   return (reinterpret_cast<uintptr_t>(r->ptr) & 31u) == 0 && r->stride_t % 16 == 0 && r->stride_h % 16 == 0;
 }
 
-CacheView view(const ovc_kv_cache* c) {
-  return {c->k, c->v, c->k_scale, c->v_scale, static_cast<int32_t>(c->pages), static_cast<int32_t>(c->heads),
-          static_cast<int32_t>(c->page)};
-}
-
 RowsView view(const ovc_rows* r) { return {r->ptr, r->stride_t, r->stride_h}; }
-
-ovc_status launched() { return cudaGetLastError() == cudaSuccess ? OVC_OK : OVC_ERR_CUDA; }
 
 // Arguments that ovc_kv_write and ovc_kv_read (with its check of the rows) share.
 ovc_status cache_call_ok(const ovc_kv_cache* c, const ovc_rows* k, const ovc_rows* v, const int32_t* slots,

@@ -21,7 +21,7 @@
  *
  * Conventions for every call:
  *   - All pointers inside ovc_tensor / ovc_output / ovc_prepared / ovc_repair /
- *     ovc_kv_cache / ovc_rows / ovc_paged_batch are DEVICE pointers of the current CUDA device.  The caller owns every
+ *     ovc_kv_cache / ovc_rows / ovc_paged_batch / ovc_kv_pages / ovc_drafts are DEVICE pointers of the current CUDA device.  The caller owns every
  *     buffer; the library never allocates or frees device memory.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Every
  *     call is asynchronous on it; argument errors are returned synchronously
@@ -55,7 +55,7 @@ typedef enum {
                                        length outside its cache, page table or rows */
 } ovc_status;
 
-enum { OVC_BF16 = 0, OVC_FP16 = 1 };
+enum { OVC_BF16 = 0, OVC_FP16 = 1, OVC_FP32 = 2 };  /* OVC_FP32: probabilities (ovc_drafts) only */
 
 /* A BF16/FP16 tensor [B,S,H,D] (use B = 1 for [S,H,D]); strides in elements,
  * the channel stride is 1. */
@@ -525,6 +525,121 @@ size_t ovc_paged_attention_workspace_bytes(const ovc_rows* q, const ovc_kv_cache
 ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const ovc_paged_batch* b,
                                float softmax_scale, const ovc_rows* o, float* lse, void* workspace,
                                size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The pages of growing sequences: who holds which page of the caches (one page
+ * table serves the caches of all layers).  All arrays are int32 on the device:
+ *   page_table  [rows, width] contiguous: the pages of each sequence in order;
+ *               row b holds ceil(kv_lens[b] / page) of them, entries behind are
+ *               written as -1 by the calls below and never read
+ *   kv_lens     [rows] tokens of each sequence
+ *   refs        [pages] how many entries of the table name the page, and what the
+ *               program adds itself to keep one from being given out; 0 is free
+ * An empty state is page_table -1, kv_lens 0, refs 0.  pages*page and width*page
+ * are below 2^31 - 1024.  The calls change the state in place and run one after
+ * the other; arrays of lengths and lists may be any others on the device.  Rows
+ * whose kv_len the table cannot hold, and entries that name no page, are reported
+ * as OVC_ERR_BAD_INDEX by ovc_get_device_status() and left alone. */
+typedef struct {
+  int64_t rows, pages;
+  int32_t width, page;              /* page: a multiple of 16, at most 1024, as in the caches */
+  int32_t* page_table;
+  int32_t* kv_lens;
+  int32_t* refs;
+} ovc_kv_pages;
+
+/* Let rows grow: row b from kv_lens[b] to lens[b] tokens (not larger, negative:
+ * it stays as it is; more than the table holds: reported, it stays).  It gets the
+ * pages that it lacks; where its last page is partly filled and others hold it
+ * too (refs > 1), it gets a page in its place as well, so that what it writes next
+ * is its own.  If all holders of such a page (refs of them) grow in this call,
+ * the highest row keeps it.  The lowest free pages are taken, in the order of
+ * rows and then of columns.  A row grows only if the rows up to and including it
+ * need no more pages than are free: kv_lens says which did.
+ * copies [3, rows] receives, for each row whose last page was replaced, that page,
+ * its successor, and the tokens to copy (ovc_kv_copy, in the cache of each layer,
+ * before the next of these calls); -1, -1, 0 for the others.
+ * At most 8192 rows. */
+ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int32_t* copies, void* stream);
+
+/* Let rows shrink to lens[b] tokens (not smaller, negative: it stays): pages
+ * that hold none of them are given back (refs - 1, entry -1).  Giving back a page
+ * that nobody holds is reported. */
+ovc_status ovc_kv_pages_release(const ovc_kv_pages* p, const int32_t* lens, void* stream);
+
+/* Row children[i] becomes a second holder of what row parents[i] holds, for
+ * i < n <= rows: pages, refs + 1, length; nothing is copied.  A child's row is
+ * empty (kv_len 0) and named once, in either list; entries for which that does
+ * not hold, or with a row outside the table, are reported and skipped.  Both
+ * negative: padding. */
+ovc_status ovc_kv_pages_fork(const ovc_kv_pages* p, const int32_t* parents, const int32_t* children, int64_t n, void* stream);
+
+/* Copy pages, codes and scales of all heads: the first tokens[i] tokens (NULL: all)
+ * of page src[i] of `from` (NULL: the same cache) become those of page dst[i] of
+ * `to`, i < n <= 2^30; the rest of dst[i] stays.  The caches have one number of
+ * heads and one page size.  Negative src or dst: nothing.  Pages or numbers of
+ * tokens out of range are skipped and reported.  No page that is written is
+ * named by another entry of the call (it would hold parts of both). */
+ovc_status ovc_kv_copy(const ovc_kv_cache* to, const ovc_kv_cache* from, const int32_t* src, const int32_t* dst,
+                       const int32_t* tokens, int64_t n, void* stream);
+
+/* Move the kept tokens of each sequence together, in place: for row b of `p` and
+ * i < cu_keep[b+1] - cu_keep[b], the token at position keep[cu_keep[b] + i]
+ * goes to position i, in every head, or with keep_stride > 0 in head h by its own
+ * list keep + h * keep_stride (keep_stride >= n; all lists have the same lengths).
+ * The positions of a sequence ascend strictly and lie below its kv_len.  What lies
+ * behind the kept tokens is left as it is or holds parts of moved tokens; pages and
+ * kv_lens do not change (ovc_kv_pages_release with the new lengths, after every
+ * layer's cache).  Every page that is written is this row's alone (refs 1): a
+ * sequence with another is reported and left as it was.  Positions that do not
+ * ascend or lie outside are reported and not moved, the sequence's other tokens
+ * then unspecified.  c->pages and c->page are those of `p`; n: the size of a list;
+ * rows <= 65535, heads <= 32767. */
+ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const int32_t* keep, int64_t keep_stride,
+                          const int32_t* cu_keep, int64_t n, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Verification of drafted tokens.  N tokens were drafted for B sequences:
+ *   cu_drafts  [B+1] int32: sequence b's drafts are drafts[cu_drafts[b] ..
+ *              cu_drafts[b+1] - 1] (ascending, from 0 to N), or NULL: N / B each
+ *   drafts     [N] int32; a negative one ends its sequence's drafts (padding); one
+ *              from V on does too and is reported
+ *   target     [N + B, V] probabilities of the verifying model: row cu_drafts[b] +
+ *              b + i is that of the token after i of sequence b's drafts
+ *   draft      [N, V] probabilities that the drafts were drawn with, or NULL: each
+ *              was certain (found by lookup, or the drafter's first choice)
+ *   accept_u   [N], sample_u [B] FP32 random numbers in [0, 1)
+ * Probabilities are FP32, BF16 or FP16 (both arrays the same), not negative,
+ * finite, aligned to their size, rows at the given strides in elements; a row
+ * need not sum to 1 exactly. */
+typedef struct {
+  int64_t B, N, V;
+  const int32_t* cu_drafts;
+  const int32_t* drafts;
+  const void* target;
+  const void* draft;
+  int32_t dtype;                    /* OVC_FP32, OVC_BF16 or OVC_FP16 */
+  int64_t target_stride, draft_stride;
+  const float* accept_u;
+  const float* sample_u;
+} ovc_drafts;
+
+/* Draft x = drafts[cu_drafts[b] + i] stays if all before it did and
+ * accept_u * q(x) < p(x), with p the target's row and q the draft's (q = 1 without
+ * `draft`).  At the first that does not, the next token is drawn from
+ * max(p - q, 0) (q = 1 at x and 0 elsewhere without `draft`), from p where that is
+ * zero everywhere; after the last, from its row of p: the least token t whose
+ * running sum w_0 + ... + w_t exceeds sample_u times the sum of all.  The tokens
+ * are then distributed as the target's own.  NaN probabilities count as 0; a row
+ * that leaves nothing to draw from gives -1.
+ * tokens [N + B] int32, in target's order: the drafts that stayed, the next
+ * token, -1 for the rest.  accepted [B] int32: how many stayed.  Where cu_drafts
+ * descends or leaves [0, N], that sequence's accepted is 0, its tokens are left as
+ * they were, and it is reported.
+ * u * q < p is exact and sums hold 48 bits (FP32 pairs, then FP64): a result
+ * differs from exact arithmetic's only where sample_u lies within about V * 2^-46
+ * of a border. The same inputs give the same tokens. */
+ovc_status ovc_verify_drafts(const ovc_drafts* d, int32_t* tokens, int32_t* accepted, void* stream);
 
 #ifdef __cplusplus
 }

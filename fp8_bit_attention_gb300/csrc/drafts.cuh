@@ -11,9 +11,10 @@ namespace ovc {
 
 constexpr int kDraftThreads = 256;
 constexpr int kDraftWarps = kDraftThreads / 32;
-constexpr int kDraftTile = 1024;                 // probabilities whose weights a warp sums at a time, or a power of two times that
+constexpr int kDraftTile = 1024;                 // probabilities whose weights a warp sums into one, or a power of two times that
 constexpr int kDraftTiles = 1024;                // most tiles of a CTA
-constexpr int kDraftClusters = 8;
+constexpr int kDraftClusters = 8;                // most CTAs of a sequence
+constexpr int kDraftCtas = 2;                    // of an SM
 
 struct DraftParams {
   const int32_t* cu;        // or nullptr: each drafts
@@ -38,61 +39,155 @@ __device__ __forceinline__ float prob(const void* p, int64_t i) {
   return __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
 }
 
-// A sum of 24-bit numbers in 48 bits: hi + lo.  (Sums of a vocabulary in FP32
-// would move the borders between tokens by more than the least of them are wide;
-// the FP64 units are too few for one addition a probability.)
-struct Sum2 {
-  float hi = 0.0f, lo = 0.0f;
-
-  // + max(p - q, 0), for p, q >= 0.  d + e = p - q without error where p >= q
-  // (Dekker, "A floating-point technique for extending the available precision",
-  // 1971), and s + e = hi + d always (Knuth's sum).
-  __device__ __forceinline__ void add(float p, float q) {
-    const float d = p - q;
-    if (!(d > 0.0f)) return;                     // a NaN counts as nothing
-    const float e = (p - d) - q;
-    const float s = hi + d, t = s - hi;
-    lo += ((hi - (s - t)) + (d - t)) + e;
-    hi = s;
-  }
-  __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+// Sums are pairs hi + lo of FP32 numbers, 48 bits: sums of a vocabulary in FP32
+// would move the borders between tokens by more than the least of them are wide,
+// and the FP64 units (2 additions a cycle and SM) would take several times as long
+// as the memory.
+struct FF {
+  float hi, lo;
 };
 
-__device__ __forceinline__ double weight(float p, float q) { return p > q ? static_cast<double>(p) - static_cast<double>(q) : 0.0; }
+// hi + lo = a + b without error (Knuth, "The Art of Computer Programming" 2, 4.2.2).
+__device__ __forceinline__ FF two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ FF operator+(const FF& a, const FF& b) {
+  FF s = two_sum(a.hi, b.hi);
+  s.lo += a.lo + b.lo;
+  const float hi = s.hi + s.lo;                  // |lo| <= half a step of hi again
+  return {hi, s.lo - (hi - s.hi)};
+}
+__device__ __forceinline__ bool above(const FF& a, const FF& b) { return (a.hi - b.hi) + (a.lo - b.lo) > 0.0f; }
 
-__device__ __forceinline__ double warp_sum(double x) {
+// max(p - q, 0), NaN: 0.  Where p >= q >= 0 the lower part makes it exact (Dekker,
+// "A floating-point technique for extending the available precision", 1971).
+__device__ __forceinline__ FF weight(float p, float q) {
+  const float d = p - q;
+  return d > 0.0f ? FF{d, (p - d) - q} : FF{0.0f, 0.0f};
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pairs(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub_pairs(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Two sums, of every other weight, by instructions that add two FP32 numbers at once.
+struct Sums {
+  uint64_t hi = 0, lo = 0;
+
+  // A NaN or negative p counts as nothing (fmaxf drops a NaN).
+  __device__ __forceinline__ void add(uint64_t p) {
+    const float2 x = unpair(p);
+    const uint64_t d = pair(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f));
+    const uint64_t s = add_pairs(hi, d), t = sub_pairs(s, hi);
+    lo = add_pairs(lo, add_pairs(sub_pairs(hi, sub_pairs(s, t)), sub_pairs(d, t)));
+    hi = s;
+  }
+  __device__ __forceinline__ void add(uint64_t p, uint64_t q) {
+    const uint64_t c = sub_pairs(p, q);
+    const float2 x = unpair(c), y = unpair(sub_pairs(sub_pairs(p, c), q));
+    const uint64_t d = pair(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f));
+    const uint64_t e = pair(x.x > 0.0f ? y.x : 0.0f, x.y > 0.0f ? y.y : 0.0f);
+    const uint64_t s = add_pairs(hi, d), t = sub_pairs(s, hi);
+    lo = add_pairs(lo, add_pairs(add_pairs(sub_pairs(hi, sub_pairs(s, t)), sub_pairs(d, t)), e));
+    hi = s;
+  }
+  __device__ __forceinline__ FF sum() const {
+    const float2 h = unpair(hi), l = unpair(lo);
+    return FF{h.x, l.x} + FF{h.y, l.y};
+  }
+};
+
+// 32 probabilities a lane of the 1024 from v0 on: 16 bytes a load where rows are
+// aligned (kVec), else one probability; zeros from v1 on.
+template <int kType, bool kVec>
+struct Line {
+  static constexpr int kEach = !kVec ? 1 : kType == 2 ? 4 : 8;     // of a load
+  static constexpr int kLoads = 32 / kEach;
+  uint32_t w[kType == 2 || !kVec ? 32 : 16];
+
+  __device__ __forceinline__ static int64_t place(int64_t v0, int load) {
+    return v0 + load * (32 * kEach) + static_cast<int>(threadIdx.x & 31) * kEach;
+  }
+  __device__ __forceinline__ void one(const void* p, int64_t v, int i) {          // value i of the line
+    uint32_t x = 0;
+    if (kType == 2) x = __float_as_uint(prob<2>(p, v));
+    else x = __ldg(static_cast<const uint16_t*>(p) + v);
+    if (kType == 2 || !kVec) w[i] = x;
+    else w[i / 2] |= x << 16 * (i & 1);
+  }
+  __device__ __forceinline__ void load(const void* p, int64_t v0, int64_t v1) {
+    if (v0 + kDraftTile <= v1) {
+      const uint8_t* at = static_cast<const uint8_t*>(p) + place(v0, 0) * (kType == 2 ? 4 : 2);
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+      for (int j = 0; j < kLoads; ++j) {
+        if (kVec) {
+          const uint4 x = __ldcs(reinterpret_cast<const uint4*>(at) + 32 * j);
+          w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+        } else {
+          w[j] = kType == 2 ? __ldcs(reinterpret_cast<const uint32_t*>(at) + 32 * j) : __ldcs(reinterpret_cast<const uint16_t*>(at) + 32 * j);
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < (kType == 2 || !kVec ? 32 : 16); ++i) w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int64_t v = place(v0, i / kEach) + i % kEach;
+      if (v < v1) one(p, v, i);
+    }
+  }
+  // Value i as nothing.
+  __device__ __forceinline__ void clear(int i) {
+    if (kType == 2 || !kVec) w[i] = 0u;
+    else w[i / 2] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+  }
+  // Values 2 i and 2 i + 1.
+  __device__ __forceinline__ uint64_t two(int i) const {
+    if (kType == 2) return pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    const uint32_t x = kVec ? w[i] : w[2 * i] | w[2 * i + 1] << 16;
+    const float2 f = unpack2<kType == 1>(x);
+    return pair(f.x, f.y);
+  }
+};
+
+// Inclusive sum over the warp's lanes, of the first kLanes of them.
+template <int kLanes>
+__device__ __forceinline__ FF warp_scan(FF x) {
+#pragma unroll
+  for (int d = 1; d < kLanes; d *= 2) {
+    const FF y = {__shfl_up_sync(0xFFFFFFFFu, x.hi, d), __shfl_up_sync(0xFFFFFFFFu, x.lo, d)};
+    if (static_cast<int>(threadIdx.x & 31) >= d) x = y + x;
+  }
   return x;
 }
-
-// Inclusive sum over the block's threads, in their order; `part` has a place for
-// each warp, and the block's sum is returned in `all`.
-__device__ __forceinline__ double block_scan(double x, double* part, double* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const double y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  double before = 0.0, sum = 0.0;
-#pragma unroll
-  for (int w = 0; w < kDraftWarps; ++w) {
-    if (w == warp) before = sum;
-    sum += part[w];
-  }
-  __syncthreads();
-  *all = sum;
-  return before + x;
+__device__ __forceinline__ FF from_lane(const FF& x, int lane) {
+  return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
 }
 
-template <int kType>
-__global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(DraftParams P) {
-  __shared__ double tile_own[kDraftTiles], tile_sum[kDraftTiles], part[kDraftWarps], cta_sum[kDraftClusters];
+template <int kType, bool kVec>
+__global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kernel(DraftParams P) {
+  __shared__ FF tile_own[kDraftTiles], tile_sum[kDraftTiles], part[kDraftWarps], cta_sum[kDraftClusters];
   __shared__ uint32_t stop;
-  __shared__ int first_over, last_some;
+  __shared__ int first_over, last_some, owner_tile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
   const int b = blockIdx.x / ctas;
@@ -104,6 +199,7 @@ __global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(DraftParam
       P.accepted[b] = 0;
       atomicOr(P.status, kPagedBadIndex);
     }
+    __syncwarp();
     cluster_wait();
     return;
   }
@@ -117,6 +213,7 @@ __global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(DraftParam
     const int i = i0 + tid;
     if (i < n) {
       const int x = P.drafts[a0 + i];
+      const float u = P.accept_u[a0 + i];
       if (x < 0 || x >= P.V) {
         atomicMin(&stop, 2u * i + 1u);
         if (x >= P.V) atomicOr(P.status, kPagedBadIndex);
@@ -124,7 +221,7 @@ __global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(DraftParam
         const float p = prob<kType>(P.target, (row0 + i) * P.target_stride + x);
         const float q = P.draft ? prob<kType>(P.draft, static_cast<int64_t>(a0 + i) * P.draft_stride + x) : 1.0f;
         // 24 by 24 bits: exact in 64
-        if (!(static_cast<double>(P.accept_u[a0 + i]) * q < p)) atomicMin(&stop, 2u * i);
+        if (!(static_cast<double>(u) * q < p)) atomicMin(&stop, 2u * i);
       }
     }
     __syncthreads();
@@ -140,122 +237,159 @@ __global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(DraftParam
   }
 
   // Sums of the weights of this CTA's part of the vocabulary, tile by tile.
-  const uint8_t* pr = static_cast<const uint8_t*>(P.target) + (row0 + kept) * P.target_stride * (kType == 2 ? 4 : 2);
+  constexpr int kBytes = kType == 2 ? 4 : 2;
+  const uint8_t* pr = static_cast<const uint8_t*>(P.target) + (row0 + kept) * P.target_stride * kBytes;
   const uint8_t* qr = nullptr;
-  int out = -1;                                       // a token that counts for nothing
+  int64_t out = -1;                                   // a token that counts for nothing
   if (rejected) {
-    if (P.draft) qr = static_cast<const uint8_t*>(P.draft) + static_cast<int64_t>(a0 + kept) * P.draft_stride * (kType == 2 ? 4 : 2);
+    if (P.draft) qr = static_cast<const uint8_t*>(P.draft) + static_cast<int64_t>(a0 + kept) * P.draft_stride * kBytes;
     else out = P.drafts[a0 + kept];
   }
   const int tile = kDraftTile << P.tile_shift;
   const int all_tiles = (P.V + tile - 1) / tile, per = (all_tiles + ctas - 1) / ctas;
   const int t0 = min(static_cast<int>(rank) * per, all_tiles), tiles = min(per, all_tiles - t0);
-  double mine = 0.0, total = 0.0;
+  FF mine, total, upto;                               // upto: of the CTAs up to the one with this lane's rank
   for (int pass = 0;; ++pass) {
     for (int t = warp; t < tiles; t += kDraftWarps) {
-      Sum2 s;
-      const int64_t v0 = static_cast<int64_t>(t0 + t) * tile;
+      Sums a, c;
+      int64_t v0 = static_cast<int64_t>(t0 + t) * tile;
       const int64_t v1 = v0 + tile < P.V ? v0 + tile : P.V;
-#pragma unroll 8
-      for (int64_t v = v0 + lane; v < v1; v += 32) {
-        const float q = qr ? prob<kType>(qr, v) : v == out ? INFINITY : 0.0f;
-        s.add(prob<kType>(pr, v), q);
+      for (; v0 < v1; v0 += kDraftTile) {
+        Line<kType, kVec> p;
+        p.load(pr, v0, v1);
+        if (qr) {
+          Line<kType, kVec> q;
+          q.load(qr, v0, v1);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            a.add(p.two(i), q.two(i));
+            c.add(p.two(i + 1), q.two(i + 1));
+          }
+        } else {
+          if (out >= v0 && out < v0 + kDraftTile) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (p.place(v0, i / p.kEach) + i % p.kEach == out) p.clear(i);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            a.add(p.two(i));
+            c.add(p.two(i + 1));
+          }
+        }
       }
-      const double w = warp_sum(s.value());
+      FF w = a.sum() + c.sum();
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1)
+        w = w + FF{__shfl_xor_sync(0xFFFFFFFFu, w.hi, d), __shfl_xor_sync(0xFFFFFFFFu, w.lo, d)};
       if (lane == 0) tile_own[t] = w;
     }
     __syncthreads();
-    mine = 0.0;
-    for (int k = 0; k < kDraftTiles; k += kDraftThreads) {       // running sums over the tiles
-      if (k >= tiles) break;
-      const int t = k + tid;
-      double all;
-      const double x = block_scan(t < tiles ? tile_own[t] : 0.0, part, &all);
-      if (t < tiles) tile_sum[t] = mine + x;
-      mine += all;
+    // Running sums over the tiles, and those of the CTAs exchanged.
+    mine = {0.0f, 0.0f};
+    if (warp == 0) {
+      for (int k = 0; k < tiles; k += 32) {
+        const int t = k + lane;
+        const FF x = mine + warp_scan<32>(t < tiles ? tile_own[t] : FF{0.0f, 0.0f});
+        if (t < tiles) tile_sum[t] = x;
+        mine = from_lane(x, 31);
+      }
+      __syncwarp();
     }
     cluster_wait();
-    if (tid < ctas)
-      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(cluster_addr(&cta_sum[rank], tid)), "d"(mine) : "memory");
-    __syncwarp();
+    if (warp == 0) {
+      if (lane < ctas)
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(&cta_sum[rank], lane)), "f"(mine.hi), "f"(mine.lo)
+                     : "memory");
+      __syncwarp();
+    }
     cluster_arrive();
     cluster_wait();
-    total = 0.0;
-    for (uint32_t c = 0; c < ctas; ++c) total += cta_sum[c];
-    if (total > 0.0 || (!qr && out < 0) || pass) break;
+    upto = warp_scan<kDraftClusters>(lane < ctas ? cta_sum[lane] : FF{0.0f, 0.0f});
+    total = from_lane(upto, kDraftClusters - 1);
+    if (total.hi > 0.0f || (!qr && out < 0) || pass) break;
     // Nothing is left of p - q: p itself.
+    __syncwarp();
     cluster_arrive();
     qr = nullptr;
     out = -1;
   }
-
-  // The CTA within whose part the running sum first exceeds u * total, or, where
-  // rounding (or u >= 1) leaves none, the last that holds any weight.
-  const double goal = static_cast<double>(P.sample_u[b]) * total;
-  int owner = -1, last = 0;
-  double before = 0.0, sum = 0.0;
-  for (uint32_t c = 0; c < ctas; ++c) {
-    if (cta_sum[c] > 0.0) last = c;
-    sum += cta_sum[c];
-    if (owner < 0 && cta_sum[c] > 0.0 && sum > goal) owner = c;
-    if (owner < 0 && c < rank) before = sum;
-  }
-  if (!(total > 0.0)) {
+  if (!(total.hi > 0.0f)) {
     if (rank == 0 && tid == 0) P.tokens[row0 + kept] = -1;
     return;
   }
-  if (static_cast<int>(rank) != (owner < 0 ? last : owner)) return;
-  if (owner < 0) {
-    before = 0.0;
-    for (uint32_t c = 0; c < rank; ++c) before += cta_sum[c];
-  }
-  if (tid == 0) {
-    first_over = kDraftTiles;
-    last_some = 0;
-  }
-  __syncthreads();
-  for (int t = tid; t < tiles; t += kDraftThreads) {
-    if (tile_own[t] > 0.0) {
-      atomicMax(&last_some, t);
-      if (before + tile_sum[t] > goal) atomicMin(&first_over, t);
+
+  // The part of the vocabulary, tile and thread within which the running sum first
+  // exceeds u * total, or, where rounding (or u >= 1) leaves none, the last that
+  // holds any weight.
+  const float u = P.sample_u[b];
+  FF goal = {u * total.hi, 0.0f};
+  goal.lo = fmaf(u, total.hi, -goal.hi) + u * total.lo;
+  const bool some = lane < ctas && cta_sum[lane].hi > 0.0f;
+  const uint32_t any = __ballot_sync(0xFFFFFFFFu, some), over = __ballot_sync(0xFFFFFFFFu, some && above(upto, goal));
+  if (static_cast<int>(rank) != (over ? __ffs(over) - 1 : 31 - __clz(any))) return;
+  FF before = rank ? from_lane(upto, rank - 1) : FF{0.0f, 0.0f};
+  if (warp == 0) {
+    int first = -1, last = 0;
+    for (int k = 0; k < tiles && first < 0; k += 32) {
+      const int t = k + lane;
+      const bool holds = t < tiles && tile_own[t].hi > 0.0f;
+      const uint32_t h = __ballot_sync(0xFFFFFFFFu, holds);
+      const uint32_t o = __ballot_sync(0xFFFFFFFFu, holds && above(before + tile_sum[t < tiles ? t : 0], goal));
+      if (h) last = k + 31 - __clz(h);
+      if (o) first = k + __ffs(o) - 1;
+    }
+    if (lane == 0) {
+      owner_tile = first >= 0 ? first : last;
+      first_over = 0x7FFFFFFF;
+      last_some = -1;
     }
   }
   __syncthreads();
-  const int t = first_over < kDraftTiles ? first_over : last_some;
-  if (t) before += tile_sum[t - 1];
-  __syncthreads();
-  if (tid == 0) {
-    first_over = 0x7FFFFFFF;
-    last_some = -1;
-  }
-  __syncthreads();
+  const int t = owner_tile;
+  if (t) before = before + tile_sum[t - 1];
   // Its probabilities in order, a few consecutive ones a thread.
   const int64_t v0 = static_cast<int64_t>(t0 + t) * tile;
   const int64_t v1 = v0 + tile < P.V ? v0 + tile : P.V;
   for (int64_t k = v0; k < v1; k += 4 * kDraftThreads) {
-    double w[4], own = 0.0, all;
+    FF w[4], own = {0.0f, 0.0f};
     const int64_t v = k + 4 * tid;
+    float p[4], q[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      w[j] = 0.0;
-      if (v + j < v1) w[j] = weight(prob<kType>(pr, v + j), qr ? prob<kType>(qr, v + j) : v + j == out ? INFINITY : 0.0f);
-      own += w[j];
+      const bool there = v + j < v1 && v + j != out;
+      p[j] = there ? prob<kType>(pr, v + j) : 0.0f;
+      q[j] = there && qr ? prob<kType>(qr, v + j) : 0.0f;
     }
-    double x = before + (block_scan(own, part, &all) - own);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      x += w[j];
-      if (w[j] > 0.0) {
-        atomicMax(&last_some, static_cast<int>(v + j));
-        if (x > goal) {
-          atomicMin(&first_over, static_cast<int>(v + j));
-          break;
+      w[j] = weight(p[j], q[j]);
+      own = own + w[j];
+    }
+    const FF in_warp = warp_scan<32>(own);
+    if (lane == 31) part[warp] = in_warp;
+    __syncthreads();
+    const FF parts = warp_scan<kDraftWarps>(lane < kDraftWarps ? part[lane] : FF{0.0f, 0.0f});
+    const FF ahead = from_lane(parts, warp ? warp - 1 : 0);
+    const FF up = warp ? before + ahead + in_warp : before + in_warp;
+    // A thread within whose numbers it may exceed goes through them once more.
+    if (own.hi > 0.0f) {
+      int has = -1, hit = -1;
+      FF x = up + FF{-own.hi, -own.lo};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x = x + w[j];
+        if (w[j].hi > 0.0f) {
+          has = static_cast<int>(v + j);
+          if (hit < 0 && above(x, goal)) hit = has;
         }
       }
+      atomicMax(&last_some, has);
+      if (hit >= 0) atomicMin(&first_over, hit);
     }
     __syncthreads();
     if (first_over != 0x7FFFFFFF) break;
-    before += all;
+    before = before + from_lane(parts, kDraftWarps - 1);
   }
   if (tid == 0) P.tokens[row0 + kept] = first_over != 0x7FFFFFFF ? first_over : last_some;
 }

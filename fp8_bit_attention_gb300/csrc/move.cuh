@@ -62,12 +62,18 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(CopyParams P) {
 // Compact, in place: position i of a sequence takes token keep[i] >= i.  A cluster
 // takes one head of K or V of one sequence and goes over the positions upwards,
 // a chunk of 256 for each of its CTAs at a time.  The tokens of later chunks lie
-// behind what a chunk writes (keep ascends, so keep[j] >= j), and those of the same
-// and earlier chunks have been read when the cluster passes its barrier: between
-// it and the next the chunk is written, while the next one is being read already.
+// behind what a chunk writes (keep ascends, so keep[j] >= j), so they may be read
+// at any time; those of the same and earlier chunks have been read when the
+// cluster passes its barrier, and then the chunk is written.
+//
+// A warp moves 32 positions of a chunk through its own part of shared memory:
+// list, page table, and tokens of the chunks ahead are on their way while one is
+// written.
 // ---------------------------------------------------------------------------
 constexpr int kCompactThreads = 256;
 constexpr int kCompactChunk = 256;                // positions of a CTA at a time: 32 a warp, 8 x 16 bytes a lane
+constexpr int kCompactStages = 3;                 // chunks in shared memory
+constexpr int kCompactSmem = kCompactStages * kCompactChunk * 128;
 
 struct CompactParams {
   CacheView c;
@@ -78,20 +84,13 @@ struct CompactParams {
   int32_t n;                // kept tokens in all
 };
 
-struct Kept {               // what a warp moves at once
-  uint4 x[8];
-  uint8_t e;
-  int64_t to;               // this lane's position's row, -1: none
-};
-
-// Row of the cache that holds position t of a sequence, or -1.
-__device__ __forceinline__ int64_t token_row(const CompactParams& C, const int32_t* table, int t, int h) {
-  const int col = t / C.P.by_page, p = table[col];
-  if (p < 0 || p >= C.c.pages) return -1;
-  return (static_cast<int64_t>(p) * C.c.heads + h) * C.c.page + (t - col * C.c.page);
+__device__ __forceinline__ void copy_async16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
-__global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactParams C) {
+__global__ void __launch_bounds__(kCompactThreads, 2) kv_compact_kernel(CompactParams C) {
+  extern __shared__ __align__(128) uint8_t tokens[];
+  __shared__ uint8_t scale_of[kCompactThreads];
   __shared__ int found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = cluster_size(), rank = cluster_rank();
@@ -137,48 +136,94 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactPara
   uint8_t* codes = kv ? C.c.v : C.c.k;
   uint8_t* scales = kv ? C.c.vs : C.c.ks;
 
-  auto read = [&](int i0, Kept& r) {              // the warp's 32 positions from i0 on
-    const int i = i0 + lane;
-    int64_t from = -1;
-    r.to = -1;
-    if (i < n) {
-      const int t = __ldg(keep + i), before = i ? __ldg(keep + i - 1) : -1;
-      if (t >= i && t > before && t < len) {
-        from = token_row(C, table, t, h);
-        r.to = token_row(C, table, i, h);
-      }
-      if (from < 0) {
-        r.to = -1;
+  // The same number of steps in every CTA; step s is this lane's position lo + s * stride + ...
+  const int stride = kCompactChunk * ctas, steps = (n - lo + stride - 1) / stride;
+  const int first = lo + rank * kCompactChunk + tid;
+  struct Ahead {            // of one position: its token and the one before it, the pages of both
+    int t, before, from, to;
+  };
+  // Each of the three uses what the one before it loaded a step earlier: a value
+  // looked at in the step that loads it would make the warp wait for it.
+  auto listed = [&](int s, Ahead& x) {            // its token
+    const int64_t i = first + static_cast<int64_t>(s) * stride;
+    x.t = i < n ? __ldg(keep + i) : -1;
+    x.before = lane == 0 && i > 0 && i < n ? __ldg(keep + i - 1) : -1;
+  };
+  auto paged = [&](int s, Ahead& x) {             // its pages
+    const int64_t i = first + static_cast<int64_t>(s) * stride;
+    const int up = __shfl_up_sync(0xFFFFFFFFu, x.t, 1);
+    const bool ok = i < n && x.t >= i && x.t > (lane ? up : x.before) && x.t < len;
+    if (!ok && i < n) atomicOr(C.P.status, kPagedBadIndex);
+    if (!ok) x.t = -1;
+    x.from = ok ? __ldg(table + x.t / C.P.by_page) : -1;
+    x.to = ok ? __ldg(table + static_cast<int>(i) / C.P.by_page) : -1;
+  };
+  auto row_of = [&](int t, int p) { return (p * C.c.heads + h) * C.c.page + (t - t / C.P.by_page * C.c.page); };
+  const uint32_t mine = smem_addr(tokens) + warp * (32 * 128) + lane * 16;
+  int to[kCompactStages], scale[kCompactStages];
+  auto fetch = [&](int s, int stage, const Ahead& x) {            // its token's codes and scale on their way
+    int from = -1;
+    to[stage] = -1;
+    if (x.t >= 0) {
+      if (x.from >= 0 && x.from < C.c.pages && x.to >= 0 && x.to < C.c.pages) {
+        from = row_of(x.t, x.from);
+        to[stage] = row_of(first + s * stride, x.to);
+      } else {
         atomicOr(C.P.status, kPagedBadIndex);
       }
     }
-    r.e = r.to >= 0 ? __ldcg(scales + from) : 0;
+    scale[stage] = from >= 0 ? __ldcg(scales + from) : 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t row = __shfl_sync(0xFFFFFFFFu, from, 4 * j + (lane >> 3));
-      if (row >= 0) r.x[j] = __ldcg(reinterpret_cast<const uint4*>(codes + row * 128) + (lane & 7));
+      const int row = __shfl_sync(0xFFFFFFFFu, from, 4 * j + (lane >> 3));
+      if (row >= 0) copy_async16(mine + stage * (kCompactChunk * 128) + j * 512, codes + static_cast<int64_t>(row) * 128 + (lane & 7) * 16);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto write = [&](const Kept& r) {
+  Ahead x0, x1, x2;
+  listed(0, x0);
+  listed(1, x1);
+  listed(2, x2);
+  paged(0, x0);
+  paged(1, x1);
+  fetch(0, 0, x0);
+  fetch(1, 1, x1);
+  x0 = x2;
+  paged(2, x0);
+  listed(3, x1);
+  int s = 0;
+  while (s < steps) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t row = __shfl_sync(0xFFFFFFFFu, r.to, 4 * j + (lane >> 3));
-      if (row >= 0) reinterpret_cast<uint4*>(codes + row * 128)[lane & 7] = r.x[j];
+    for (int stage = 0; stage < kCompactStages; ++stage, ++s) {   // step s is in `stage`
+      if (s >= steps) break;
+      fetch(s + 2, (stage + 2) % kCompactStages, x0);
+      x0 = x1;
+      paged(s + 3, x0);
+      listed(s + 4, x1);
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      scale_of[tid] = scale[stage];               // what this thread reads has arrived
+      __syncwarp();
+      if (ctas > 1) {
+        // Only reads have to be over, and those are: no fence for what was written.
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        cluster_wait();
+      } else {
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int row = __shfl_sync(0xFFFFFFFFu, to[stage], 4 * j + (lane >> 3));
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(mine + stage * (kCompactChunk * 128) + j * 512));
+        if (row >= 0) *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(row) * 128 + (lane & 7) * 16) = v;
+      }
+      if (to[stage] >= 0) scales[to[stage]] = scale_of[tid];
+      __syncwarp();
     }
-    if (r.to >= 0) scales[r.to] = r.e;
-  };
-  // The same number of steps in every CTA.
-  const int stride = kCompactChunk * ctas, steps = (n - lo + stride - 1) / stride;
-  int i0 = lo + rank * kCompactChunk + warp * 32;
-  Kept r;
-  for (int s = 0; s < steps; ++s, i0 += stride) {
-    read(i0, r);
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-    write(r);
-    __syncwarp();
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 }  // namespace ovc

@@ -59,15 +59,20 @@ __global__ void __launch_bounds__(1024) pages_release_kernel(PagesView P, const 
   if (to < 0 || to >= len) return;                   // uniform over the CTA
   const int end = pages_of(P, len);
   int32_t* row = P.table + static_cast<int64_t>(b) * P.width;
-  for (int c = pages_of(P, to) + threadIdx.x; c < end; c += blockDim.x) {
-    const int p = row[c];
-    row[c] = -1;
-    bool ok = p >= 0 && p < P.pages;
-    if (ok && atomicSub(P.refs + p, 1) <= 0) {       // nobody held it: as it was
-      atomicAdd(P.refs + p, 1);
-      ok = false;
+  for (int c0 = pages_of(P, to) + threadIdx.x; c0 < end; c0 += 4 * blockDim.x) {
+    int p[4];
+    bool ok[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = c0 + j * blockDim.x < end ? row[c0 + j * blockDim.x] : -2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ok[j] = p[j] >= 0 && p[j] < P.pages && P.refs[p[j]] > 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c0 + j * blockDim.x >= end) break;
+      row[c0 + j * blockDim.x] = -1;
+      if (ok[j]) atomicSub(P.refs + p[j], 1);        // (a use of what it returns would be waited for)
+      else atomicOr(P.status, kPagedBadIndex);
     }
-    if (!ok) atomicOr(P.status, kPagedBadIndex);
   }
   __syncthreads();
   if (threadIdx.x == 0) P.lens[b] = to;
@@ -85,7 +90,8 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView P, c
   if (a < 0 && b < 0) return;                        // padding
   bool bad = a < 0 || a >= P.rows || b < 0 || b >= P.rows;
   // A child that another entry names, as child or as parent, would change under it.
-  for (int j = threadIdx.x; j < n; j += kForkThreads) bad |= parents[j] == b || (j != i && children[j] == b);
+#pragma unroll 4
+  for (int j = threadIdx.x; j < n; j += kForkThreads) bad |= (parents[j] == b) | ((j != i) & (children[j] == b));
   bad = __syncthreads_or(bad);
   const int len = bad ? -1 : row_len(P, a);
   if (len < 0 || P.lens[b] != 0) {
@@ -95,11 +101,17 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView P, c
   const int32_t* from = P.table + static_cast<int64_t>(a) * P.width;
   int32_t* row = P.table + static_cast<int64_t>(b) * P.width;
   const int end = pages_of(P, len);
-  for (int c = threadIdx.x; c < end; c += kForkThreads) {
-    const int p = from[c];
-    row[c] = p;
-    if (p >= 0 && p < P.pages) atomicAdd(P.refs + p, 1);
-    else atomicOr(P.status, kPagedBadIndex);
+  for (int c0 = threadIdx.x; c0 < end; c0 += 4 * kForkThreads) {
+    int p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = c0 + j * kForkThreads < end ? from[c0 + j * kForkThreads] : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c0 + j * kForkThreads >= end) break;
+      row[c0 + j * kForkThreads] = p[j];
+      if (p[j] >= 0 && p[j] < P.pages) atomicAdd(P.refs + p[j], 1);
+      else atomicOr(P.status, kPagedBadIndex);
+    }
   }
   __syncthreads();
   if (threadIdx.x == 0) P.lens[b] = len;
@@ -107,14 +119,18 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView P, c
 
 // ---------------------------------------------------------------------------
 // Reserve: one cluster.  Every CTA works out for itself how many pages each row
-// needs, and counts the free pages of its own part of refs; the counts are
-// exchanged once, and then each free page knows its rank among all, and by it the
-// row and column that it goes to.
+// needs.  The pages are cut into chunks, dealt out to the CTAs in turn, so that
+// the lowest ones, where the free pages are taken, are spread over all of them;
+// the chunks' numbers of free pages are exchanged once, and then each free page
+// knows its rank among all, and by it the row and column that it goes to.
 // ---------------------------------------------------------------------------
 constexpr int kReserveThreads = 1024;
 constexpr int kReserveWarps = kReserveThreads / 32;
 constexpr int kReserveRows = 8192;             // most rows of a call: their sums are held in shared memory
 constexpr int kReserveClusters = 8;            // most CTAs
+constexpr int kReserveBatch = 4;               // loads of 16 bytes a lane at a time
+constexpr int kReserveChunk = kReserveThreads * 4 * kReserveBatch;   // pages, or a power of two times that
+constexpr int kReserveChunks = 1024;           // most of them
 constexpr uint32_t kMoves = 0x80000000u;       // in `first`: the row's last page is replaced
 
 struct ReserveSmem {
@@ -137,14 +153,45 @@ __host__ __device__ inline size_t reserve_smem(int rows) {
   return r * 10 + reserve_hash(rows) * 8;
 }
 
+// The last row b with start[b] <= r, from one on that fulfils it; rows give way
+// slowly as ranks rise.
+__device__ __forceinline__ int row_of_rank(const uint32_t* start, int b, int rows, uint32_t r) {
+  if (b + 1 >= rows || r < start[b + 1]) return b;
+  int e = rows;
+  while (e - b > 1) {
+    const int m = (b + e) >> 1;
+    if (start[m] <= r) b = m;
+    else e = m;
+  }
+  return b;
+}
+
+// Bits k of f[j]: page p0 + 128 j + 4 lane + k, of those below hi, is free.
+__device__ __forceinline__ void free_of(const PagesView& P, int p0, int hi, uint32_t (&f)[kReserveBatch]) {
+  int4 x[kReserveBatch];
+#pragma unroll
+  for (int j = 0; j < kReserveBatch; ++j) {
+    const int p = p0 + 128 * j + 4 * (threadIdx.x & 31);
+    x[j] = make_int4(1, 1, 1, 1);
+    if (p + 3 < hi) {
+      x[j] = *reinterpret_cast<const int4*>(P.refs + p);
+    } else {
+      if (p < hi) x[j].x = P.refs[p];
+      if (p + 1 < hi) x[j].y = P.refs[p + 1];
+      if (p + 2 < hi) x[j].z = P.refs[p + 2];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kReserveBatch; ++j)
+    f[j] = (x[j].x == 0) | (x[j].y == 0) << 1 | (x[j].z == 0) << 2 | (x[j].w == 0) << 3;
+}
+
 __global__ void __launch_bounds__(kReserveThreads) pages_reserve_kernel(PagesView P, const int32_t* __restrict__ lens,
-                                                                        int32_t* __restrict__ copies) {
+                                                                        int32_t* __restrict__ copies, int chunk_shift) {
   extern __shared__ __align__(16) uint8_t raw[];
-  __shared__ uint32_t warp_free[kReserveWarps], cta_free[kReserveClusters], scan[kReserveWarps], carry, granted;
+  __shared__ uint32_t warp_free[kReserveWarps], free_in[kReserveChunks], scan[kReserveWarps], carry, granted;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
-  cluster_arrive();                                  // every CTA has begun before another writes to it
-
   ReserveSmem S;
   S.hash = reserve_hash(P.rows);
   const size_t r8 = (static_cast<size_t>(P.rows) + 8) / 8 * 8;
@@ -159,17 +206,31 @@ __global__ void __launch_bounds__(kReserveThreads) pages_reserve_kernel(PagesVie
   }
   if (tid == 0) carry = granted = 0;
 
-  // Free pages of this warp's part.
-  const int per_cta = static_cast<int>((static_cast<int64_t>(P.pages) + ctas - 1) / ctas);
-  const int per_warp = ((per_cta + kReserveWarps - 1) / kReserveWarps + 31) / 32 * 32;
-  const int64_t lo64 = static_cast<int64_t>(rank) * per_warp * kReserveWarps + static_cast<int64_t>(warp) * per_warp;
-  const int lo = static_cast<int>(lo64 < P.pages ? lo64 : P.pages), hi = P.pages - lo < per_warp ? P.pages : lo + per_warp;
-  uint32_t mine = 0;
-#pragma unroll 8
-  for (int p = lo + lane; p < hi; p += 32) mine += P.refs[p] == 0;
-  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-  if (lane == 0) warp_free[warp] = mine;
+  const int chunk = kReserveChunk << chunk_shift, part = chunk / kReserveWarps;    // of a CTA, of a warp
+  const int chunks = static_cast<int>((static_cast<int64_t>(P.pages) + chunk - 1) / chunk);
+  for (int k = tid; k < chunks; k += kReserveThreads) free_in[k] = 0;
   __syncthreads();
+  cluster_arrive();                                  // others may write to free_in from here on
+  // The free pages of this CTA's chunks.
+  auto count = [&](int lo, int hi) {                 // of a warp's pages
+    uint32_t n = 0, f[kReserveBatch];
+    for (int p = lo; p < hi; p += 128 * kReserveBatch) {
+      free_of(P, p, hi, f);
+#pragma unroll
+      for (int j = 0; j < kReserveBatch; ++j) n += __popc(f[j]);
+    }
+    return __reduce_add_sync(0xFFFFFFFFu, n);
+  };
+  auto place = [&](int k, int& lo, int& hi) {        // a warp's pages of chunk k
+    lo = k * chunk + warp * part;                    // below 2^27 + 2^15 << 10
+    hi = min(P.pages, lo + part);
+  };
+  for (int k = rank; k < chunks; k += ctas) {
+    int lo, hi;
+    place(k, lo, hi);
+    const uint32_t n = count(lo, hi);
+    if (lane == 0 && n) atomicAdd(&free_in[k], n);
+  }
 
   // What each row needs, its last page apart.
   for (int b = tid; b < P.rows; b += kReserveThreads) {
@@ -247,22 +308,22 @@ __global__ void __launch_bounds__(kReserveThreads) pages_reserve_kernel(PagesVie
     __syncthreads();
   }
 
-  // The free pages before this CTA's, and all of them.
+  // The other CTAs' counts.
   cluster_wait();
-  if (tid < ctas) {
-    uint32_t sum = 0;
-    for (int w = 0; w < kReserveWarps; ++w) sum += warp_free[w];
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&cta_free[rank], tid)), "r"(sum) : "memory");
+  for (int i = tid; i < chunks * static_cast<int>(ctas); i += kReserveThreads) {
+    const uint32_t k = i / ctas, to = i - k * ctas;
+    if (k % ctas == rank && to != rank)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&free_in[k], to)), "r"(free_in[k]) : "memory");
   }
   __syncwarp();
   cluster_arrive();
   cluster_wait();                                    // and no CTA reads the rows' state any more
-  uint32_t base = 0, total = 0;
-  for (uint32_t c = 0; c < ctas; ++c) {
-    if (c < rank) base += cta_free[c];
-    total += cta_free[c];
-  }
-  for (int w = 0; w < warp; ++w) base += warp_free[w];
+  auto free_below = [&](int k) {                     // in the chunks before k
+    uint32_t sum = 0;
+    for (int i = lane; i < k; i += 32) sum += free_in[i];
+    return __reduce_add_sync(0xFFFFFFFFu, sum);
+  };
+  const uint32_t total = free_below(chunks);
 
   uint32_t most = 0;                                 // pages given out
   for (int b = tid; b < P.rows; b += kReserveThreads) {
@@ -277,23 +338,47 @@ __global__ void __launch_bounds__(kReserveThreads) pages_reserve_kernel(PagesVie
   int32_t* src = copies;
   int32_t* dst = copies + P.rows;
   int32_t* tokens = dst + P.rows;
-  for (int p0 = lo; p0 < hi && base < most; p0 += 32) {
-    const int p = p0 + lane;
-    const bool free = p < hi && P.refs[p] == 0;
-    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, free);
-    const uint32_t r = base + __popc(mask & ((1u << lane) - 1u));
-    base += __popc(mask);
-    if (!free || r >= most) continue;
-    int b = 0, e = P.rows;                           // start[b] <= r < start[e]
-    while (e - b > 1) {
-      const int m = (b + e) >> 1;
-      if (S.start[m] <= r) b = m;
-      else e = m;
+  for (int k = rank; k < chunks; k += ctas) {
+    uint32_t base = free_below(k);
+    if (base >= most) break;                         // the whole CTA
+    int lo, hi;
+    place(k, lo, hi);
+    const uint32_t n = count(lo, hi);
+    if (lane == 0) warp_free[warp] = n;
+    __syncthreads();
+    base += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_free[lane] : 0u);
+    __syncthreads();
+    int row = 0;                                     // start[row] <= base
+    for (int p0 = lo; p0 < hi && base < most; p0 += 128 * kReserveBatch) {
+      uint32_t f[kReserveBatch];
+      free_of(P, p0, hi, f);
+#pragma unroll
+      for (int j = 0; j < kReserveBatch; ++j) {
+        if (base >= most) break;
+        row = row_of_rank(S.start, row, P.rows, base);
+        uint32_t r = base;                           // rank of this lane's first free page
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t mask = __ballot_sync(0xFFFFFFFFu, f[j] >> i & 1u);
+          r += __popc(mask & ((1u << lane) - 1u));
+          base += __popc(mask);
+        }
+        int b = row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if ((f[j] >> i & 1u) && r < most) {
+            const int p = p0 + 128 * j + 4 * lane + i;
+            b = row_of_rank(S.start, b, P.rows, r);
+            const uint32_t first = S.first[b], at = r - S.start[b];
+            P.table[static_cast<int64_t>(b) * P.width + (first & ~kMoves) + at] = p;
+            P.refs[p] = 1;
+            if ((first & kMoves) && at == 0) dst[b] = p;
+          }
+          r += f[j] >> i & 1u;
+        }
+        __syncwarp();
+      }
     }
-    const uint32_t first = S.first[b], at = r - S.start[b];
-    P.table[static_cast<int64_t>(b) * P.width + (first & ~kMoves) + at] = p;
-    P.refs[p] = 1;
-    if ((first & kMoves) && at == 0) dst[b] = p;
   }
   for (int b = rank * kReserveThreads + tid; b < P.rows; b += ctas * kReserveThreads) {
     const int to = lens[b], len = P.lens[b];

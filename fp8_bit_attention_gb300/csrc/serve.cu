@@ -23,7 +23,7 @@ bool pages_ok(const ovc_kv_pages* p) {
   if (!p || p->rows < 1 || p->rows > kMost || p->pages < 1 || p->pages > kMost || p->width < 1) return false;
   if (p->page < 16 || p->page > 1024 || p->page % 16) return false;
   return p->pages * p->page <= kMost && static_cast<int64_t>(p->width) * p->page <= kMost && at4(p->page_table) &&
-         at4(p->kv_lens) && at4(p->refs);
+         at4(p->kv_lens) && at16(p->refs);
 }
 
 PagesView view(const ovc_kv_pages* p, const DeviceState* dev) {
@@ -66,7 +66,8 @@ ovc_status serve_init(int device) {
   std::lock_guard<std::mutex> lock(g_serve_mu);
   if (g_serve_init[device]) return OVC_OK;
   if (cudaFuncSetAttribute(pages_reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(reserve_smem(kReserveRows))) != cudaSuccess)
+                           static_cast<int>(reserve_smem(kReserveRows))) != cudaSuccess ||
+      cudaFuncSetAttribute(kv_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCompactSmem) != cudaSuccess)
     return OVC_ERR_CUDA;
   g_serve_init[device] = true;
   return OVC_OK;
@@ -86,9 +87,11 @@ ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int3
   if (st != OVC_OK) return st;
   st = serve_init(dev->index);
   if (st != OVC_OK) return st;
-  const int ctas = clusters_for(1, (p->pages + 16383) / 16384, kReserveClusters);
+  int shift = 0;
+  while (p->pages > (int64_t{kReserveChunk} << shift) * kReserveChunks) ++shift;
+  const int ctas = clusters_for(1, (p->pages + kReserveChunk - 1) / kReserveChunk, kReserveClusters);
   return launch_clusters(pages_reserve_kernel, dim3(ctas), kReserveThreads, reserve_smem(static_cast<int>(p->rows)), ctas,
-                         static_cast<cudaStream_t>(stream), view(p, dev), lens, copies);
+                         static_cast<cudaStream_t>(stream), view(p, dev), lens, copies, shift);
 }
 
 ovc_status ovc_kv_pages_release(const ovc_kv_pages* p, const int32_t* lens, void* stream) {
@@ -143,7 +146,7 @@ ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const in
     return OVC_ERR_INVALID_ARG;
   if (!at4(keep) || !at4(cu_keep) || n < 1 || n > kMost || (keep_stride != 0 && keep_stride < n)) return OVC_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
-  const ovc_status st = device_state(&dev);
+  ovc_status st = device_state(&dev);
   if (st != OVC_OK) return st;
   CompactParams C{};
   C.c = view(c);
@@ -152,9 +155,11 @@ ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const in
   C.keep_stride = keep_stride;
   C.cu = cu_keep;
   C.n = static_cast<int32_t>(n);
+  st = serve_init(dev->index);
+  if (st != OVC_OK) return st;
   const int ctas = clusters_for(p->rows * c->heads * 2, 2 * dev->sms, 8);
   return launch_clusters(kv_compact_kernel, dim3(ctas, static_cast<unsigned>(2 * c->heads), static_cast<unsigned>(p->rows)),
-                         kCompactThreads, 0, ctas, static_cast<cudaStream_t>(stream), C);
+                         kCompactThreads, kCompactSmem, ctas, static_cast<cudaStream_t>(stream), C);
 }
 
 ovc_status ovc_verify_drafts(const ovc_drafts* d, int32_t* tokens, int32_t* accepted, void* stream) {
@@ -185,12 +190,16 @@ ovc_status ovc_verify_drafts(const ovc_drafts* d, int32_t* tokens, int32_t* acce
   P.accepted = accepted;
   P.status = dev->status;
   const int most = clusters_for(1, (d->V + 4095) / 4096, kDraftClusters);
-  const int ctas = clusters_for(d->B, 2 * dev->sms, most);
+  int ctas = 1;                                  // as many as run at once
+  while (ctas < most && d->B * ctas * 2 <= kDraftCtas * dev->sms) ctas *= 2;
   while ((d->V + (int64_t{kDraftTile} << P.tile_shift) - 1) / (int64_t{kDraftTile} << P.tile_shift) > int64_t{kDraftTiles} * ctas)
     ++P.tile_shift;
-  auto* fn = d->dtype == OVC_FP32   ? verify_drafts_kernel<2>
-             : d->dtype == OVC_FP16 ? verify_drafts_kernel<1>
-                                    : verify_drafts_kernel<0>;
+  const int64_t bytes = d->dtype == OVC_FP32 ? 4 : 2;
+  const bool vec = at16(d->target) && d->target_stride * bytes % 16 == 0 &&
+                   (!d->draft || (at16(d->draft) && d->draft_stride * bytes % 16 == 0));
+  auto* fn = d->dtype == OVC_FP32   ? (vec ? verify_drafts_kernel<2, true> : verify_drafts_kernel<2, false>)
+             : d->dtype == OVC_FP16 ? (vec ? verify_drafts_kernel<1, true> : verify_drafts_kernel<1, false>)
+                                    : (vec ? verify_drafts_kernel<0, true> : verify_drafts_kernel<0, false>);
   return launch_clusters(fn, dim3(static_cast<unsigned>(d->B * ctas)), kDraftThreads, 0, ctas, static_cast<cudaStream_t>(stream), P);
 }
 

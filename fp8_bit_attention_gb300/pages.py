@@ -50,6 +50,8 @@ class KVPages:
             raise ValueError("page_table must be [sequences, pages per sequence] and refs [pages]")
         ptrs = [_ints(t, t.shape, "page_table"), _ints(self.kv_lens, (t.shape[0],), "kv_lens"),
                 _ints(self.refs, (self.refs.shape[0],), "refs")]
+        if ptrs[2] % 16:
+            raise ValueError("refs must be 16-byte aligned")
         if self.page % 16 or not 16 <= self.page <= 1024:
             raise ValueError(f"page size {self.page} is not a multiple of 16 up to 1024")
         if max(self.refs.shape[0], t.shape[1]) * self.page > 2 ** 31 - 1024:

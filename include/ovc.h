@@ -534,7 +534,8 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
  *               written as -1 by the calls below and never read
  *   kv_lens     [rows] tokens of each sequence
  *   refs        [pages] how many entries of the table name the page, and what the
- *               program adds itself to keep one from being given out; 0 is free
+ *               program adds itself to keep one from being given out; 0 is free;
+ *               16-byte aligned
  * An empty state is page_table -1, kv_lens 0, refs 0.  pages*page and width*page
  * are below 2^31 - 1024.  The calls change the state in place and run one after
  * the other; arrays of lengths and lists may be any others on the device.  Rows

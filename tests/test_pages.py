@@ -83,7 +83,7 @@ def test_checked_tokens_lie_at_their_place():
 
 # ------------------------------------------------------------------- refusals
 BAD_PAGES = [dict(rows=0), dict(pages=0), dict(width=0), dict(page=8), dict(page=24), dict(page=2048), dict(page_table=0),
-             dict(kv_lens=0x20002), dict(refs=None), dict(pages=1 << 27), dict(width=1 << 27), dict(rows=1 << 31)]
+             dict(kv_lens=0x20002), dict(refs=None), dict(refs=0x30004), dict(pages=1 << 27), dict(width=1 << 27), dict(rows=1 << 31)]
 
 
 @pytest.mark.parametrize("bad", BAD_PAGES, ids=str)

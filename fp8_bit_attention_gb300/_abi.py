@@ -126,7 +126,7 @@ SIGNATURES = {
     "ovc_paged_attention_workspace_bytes": (ctypes.c_size_t, [P(OvcRows), P(OvcKVCache), P(OvcPagedBatch)]),
     "ovc_paged_attention": (c_i32, [P(OvcRows), P(OvcKVCache), P(OvcPagedBatch), ctypes.c_float, P(OvcRows), c_ptr, c_ptr,
                                     ctypes.c_size_t, c_ptr]),
-    "ovc_kv_pages_reserve": (c_i32, [P(OvcKVPages), c_ptr, c_ptr, c_ptr]),
+    "ovc_kv_pages_reserve": (c_i32, [P(OvcKVPages), c_ptr, c_ptr, c_ptr, c_ptr, c_ptr]),
     "ovc_kv_pages_release": (c_i32, [P(OvcKVPages), c_ptr, c_ptr]),
     "ovc_kv_pages_fork": (c_i32, [P(OvcKVPages), c_ptr, c_ptr, c_i64, c_ptr]),
     "ovc_kv_copy": (c_i32, [P(OvcKVCache), P(OvcKVCache), c_ptr, c_ptr, c_ptr, c_i64, c_ptr]),

@@ -127,11 +127,18 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView P, c
 constexpr int kReserveThreads = 1024;
 constexpr int kReserveWarps = kReserveThreads / 32;
 constexpr int kReserveRows = 8192;             // most rows of a call: their sums are held in shared memory
-constexpr int kReserveClusters = 8;            // most CTAs
-constexpr int kReserveBatch = 4;               // loads of 16 bytes a lane at a time
-constexpr int kReserveChunk = kReserveThreads * 4 * kReserveBatch;   // pages, or a power of two times that
-constexpr int kReserveChunks = 1024;           // most of them
+constexpr int kReserveClusters = 16;           // most CTAs
+constexpr int kReserveWords = 4;               // words of 32 pages of a warp in a block
+constexpr int kReserveBlock = kReserveWarps * kReserveWords * 32;  // pages that a CTA deals out together
+constexpr int kReserveAhead = 4;               // blocks on their way at a time where they are counted
+constexpr int kReserveChunks = 1024;           // most chunks: blocks, or a power of two of them each
 constexpr uint32_t kMoves = 0x80000000u;       // in `first`: the row's last page is replaced
+
+struct ReserveOut {       // [rows] each: what has to be copied
+  int32_t* src;
+  int32_t* dst;
+  int32_t* tokens;
+};
 
 struct ReserveSmem {
   uint32_t* start;      // [rows + 1] pages that the rows before need
@@ -139,25 +146,60 @@ struct ReserveSmem {
   uint16_t* slot;       // [rows] where `key` holds its last page, or kNoSlot
   int32_t* key;         // [hash] pages that rows want to write to and others hold too
   uint32_t* val;        // [hash] how many such rows << 16 | the highest of them + 1, if those are all holders
-  uint32_t hash;
 };
 constexpr uint32_t kNoSlot = 0xFFFFu;
 
-__host__ __device__ inline uint32_t reserve_hash(int rows) {
+// Places for the pages of `rows` rows, at most half of them taken.
+__host__ inline uint32_t reserve_hash(int rows) {
   uint32_t h = 64;
   while (h < 2u * static_cast<uint32_t>(rows)) h *= 2;
   return h;
 }
-__host__ __device__ inline size_t reserve_smem(int rows) {
-  const size_t r = (static_cast<size_t>(rows) + 8) / 8 * 8;      // rows + 1 fit
-  return r * 10 + reserve_hash(rows) * 8;
-}
+__host__ __device__ inline int reserve_room(int rows) { return (rows + 8) / 8 * 8; }     // rows + 1 fit
+__host__ inline size_t reserve_smem(int rows) { return static_cast<size_t>(reserve_room(rows)) * 10 + reserve_hash(rows) * 8; }
 
-// The last row b with start[b] <= r, from one on that fulfils it; rows give way
-// slowly as ranks rise.
+// refs of a block of pages from p0 on.  Word m of 32 pages is word m / 32 of warp
+// m % 32, so that the lowest free pages are spread over the warps.
+struct Block {
+  int32_t x[kReserveWords];
+  __device__ __forceinline__ void load(const PagesView& P, int p0, int end) {
+    const int p = p0 + static_cast<int>(threadIdx.x);
+#pragma unroll
+    for (int j = 0; j < kReserveWords; ++j) x[j] = p + kReserveThreads * j < end ? P.refs[p + kReserveThreads * j] : 1;
+  }
+  // Free ones among this lane's.
+  __device__ __forceinline__ uint32_t count() const {
+    uint32_t n = 0;
+#pragma unroll
+    for (int j = 0; j < kReserveWords; ++j) n += x[j] == 0;
+    return n;
+  }
+  // In lane j < kReserveWords: which pages of the warp's word j are free.
+  __device__ __forceinline__ uint32_t free() const {
+    uint32_t f = 0;
+#pragma unroll
+    for (int j = 0; j < kReserveWords; ++j) {
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, x[j] == 0);
+      if (static_cast<int>(threadIdx.x & 31) == j) f = m;
+    }
+    return f;
+  }
+};
+
+// The last row with start <= r, from row b on that fulfils it, for ascending r
+// over the lanes: among the next 32 rows by exchanging their starts, which takes
+// a third of the time of a search in shared memory.
 __device__ __forceinline__ int row_of_rank(const uint32_t* start, int b, int rows, uint32_t r) {
-  if (b + 1 >= rows || r < start[b + 1]) return b;
+  const int next = b + 1 + static_cast<int>(threadIdx.x & 31);
+  const uint32_t s = next < rows ? start[next] : 0xFFFFFFFFu;
+  int n = 0;
+#pragma unroll
+  for (int step = 16; step; step >>= 1)
+    if (__shfl_sync(0xFFFFFFFFu, s, n + step - 1) <= r) n += step;
+  if (__shfl_sync(0xFFFFFFFFu, s, n) <= r) ++n;
+  if (n < 32) return b + n;
   int e = rows;
+  b += 32;
   while (e - b > 1) {
     const int m = (b + e) >> 1;
     if (start[m] <= r) b = m;
@@ -166,104 +208,90 @@ __device__ __forceinline__ int row_of_rank(const uint32_t* start, int b, int row
   return b;
 }
 
-// Bits k of f[j]: page p0 + 128 j + 4 lane + k, of those below hi, is free.
-__device__ __forceinline__ void free_of(const PagesView& P, int p0, int hi, uint32_t (&f)[kReserveBatch]) {
-  int4 x[kReserveBatch];
-#pragma unroll
-  for (int j = 0; j < kReserveBatch; ++j) {
-    const int p = p0 + 128 * j + 4 * (threadIdx.x & 31);
-    x[j] = make_int4(1, 1, 1, 1);
-    if (p + 3 < hi) {
-      x[j] = *reinterpret_cast<const int4*>(P.refs + p);
-    } else {
-      if (p < hi) x[j].x = P.refs[p];
-      if (p + 1 < hi) x[j].y = P.refs[p + 1];
-      if (p + 2 < hi) x[j].z = P.refs[p + 2];
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kReserveBatch; ++j)
-    f[j] = (x[j].x == 0) | (x[j].y == 0) << 1 | (x[j].z == 0) << 2 | (x[j].w == 0) << 3;
-}
+__device__ __forceinline__ uint32_t capped_sum(uint32_t a, uint32_t b) { return min(a + b, 0x80000000u); }
 
-__global__ void __launch_bounds__(kReserveThreads) pages_reserve_kernel(PagesView P, const int32_t* __restrict__ lens,
-                                                                        int32_t* __restrict__ copies, int chunk_shift) {
+__global__ void __launch_bounds__(kReserveThreads, 1) pages_reserve_kernel(PagesView P, const int32_t* __restrict__ lens,
+                                                                        ReserveOut out, int chunk_shift, uint32_t hash) {
   extern __shared__ __align__(16) uint8_t raw[];
-  __shared__ uint32_t warp_free[kReserveWarps], free_in[kReserveChunks], scan[kReserveWarps], carry, granted;
+  __shared__ uint32_t word_base[kReserveWarps * kReserveWords], free_in[kReserveChunks], scan[kReserveWarps], granted;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  const int rank = cluster_rank(), ctas = cluster_size();
+  // The first row of each thread, and the CTA's first pages, are on their way
+  // while shared memory is set up.
+  int to = -1, len = 0;
+  if (tid < P.rows) to = lens[tid], len = P.lens[tid];
+  const int chunk = kReserveBlock << chunk_shift, chunks = (P.pages - 1) / chunk + 1;
+  const int blocks = ((chunks - rank + ctas - 1) / ctas) << chunk_shift;           // the CTA's, of all its chunks
+  const auto chunk_of = [&](int i) { return rank + (i >> chunk_shift) * ctas; };   // of its block i
+  Block ahead[kReserveAhead];
+  const auto fetch = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < kReserveAhead; ++j)
+      ahead[j].load(P, chunk_of(i + j) * chunk + ((i + j) & ((1 << chunk_shift) - 1)) * kReserveBlock, i + j < blocks ? P.pages : 0);
+  };
+  fetch(0);
+
   ReserveSmem S;
-  S.hash = reserve_hash(P.rows);
-  const size_t r8 = (static_cast<size_t>(P.rows) + 8) / 8 * 8;
+  const int room = reserve_room(P.rows);
   S.start = reinterpret_cast<uint32_t*>(raw);
-  S.first = S.start + r8;
-  S.key = reinterpret_cast<int32_t*>(S.first + r8);
-  S.val = reinterpret_cast<uint32_t*>(S.key + S.hash);
-  S.slot = reinterpret_cast<uint16_t*>(S.val + S.hash);
-  for (uint32_t i = tid; i < S.hash; i += kReserveThreads) {
+  S.first = S.start + room;
+  S.key = reinterpret_cast<int32_t*>(S.first + room);
+  S.val = reinterpret_cast<uint32_t*>(S.key + hash);
+  S.slot = reinterpret_cast<uint16_t*>(S.val + hash);
+  for (uint32_t i = tid; i < hash; i += kReserveThreads) {
     S.key[i] = -1;
     S.val[i] = 0;
   }
-  if (tid == 0) carry = granted = 0;
-
-  const int chunk = kReserveChunk << chunk_shift, part = chunk / kReserveWarps;    // of a CTA, of a warp
-  const int chunks = static_cast<int>((static_cast<int64_t>(P.pages) + chunk - 1) / chunk);
+  if (tid == 0) granted = 0;
   for (int k = tid; k < chunks; k += kReserveThreads) free_in[k] = 0;
   __syncthreads();
-  cluster_arrive();                                  // others may write to free_in from here on
-  // The free pages of this CTA's chunks.
-  auto count = [&](int lo, int hi) {                 // of a warp's pages
-    uint32_t n = 0, f[kReserveBatch];
-    for (int p = lo; p < hi; p += 128 * kReserveBatch) {
-      free_of(P, p, hi, f);
-#pragma unroll
-      for (int j = 0; j < kReserveBatch; ++j) n += __popc(f[j]);
-    }
-    return __reduce_add_sync(0xFFFFFFFFu, n);
-  };
-  auto place = [&](int k, int& lo, int& hi) {        // a warp's pages of chunk k
-    lo = k * chunk + warp * part;                    // below 2^27 + 2^15 << 10
-    hi = min(P.pages, lo + part);
-  };
-  for (int k = rank; k < chunks; k += ctas) {
-    int lo, hi;
-    place(k, lo, hi);
-    const uint32_t n = count(lo, hi);
-    if (lane == 0 && n) atomicAdd(&free_in[k], n);
-  }
+  if (ctas > 1) cluster_arrive();                    // others may write to free_in from here on
 
   // What each row needs, its last page apart.
   for (int b = tid; b < P.rows; b += kReserveThreads) {
-    const int to = lens[b];
+    if (b != tid) to = lens[b], len = P.lens[b];
     uint32_t fresh = 0, first = 0, slot = kNoSlot;
-    int len = to < 0 ? 0 : row_len(P, b);
-    bool bad = to > P.width * P.page;
-    if (to >= 0 && len >= 0 && to > len && !bad) {
-      const int have = pages_of(P, len);
-      fresh = pages_of(P, to) - have;
-      first = have;
-      if (len % P.page) {
-        const int last = P.table[static_cast<int64_t>(b) * P.width + have - 1];
-        if (last < 0 || last >= P.pages) {
-          bad = true;
-        } else if (P.refs[last] > 1) {
-          uint32_t h = (static_cast<uint32_t>(last) * 2654435761u >> 16) & (S.hash - 1);
-          for (;; h = (h + 1) & (S.hash - 1)) {      // at most half of the places are taken
-            const int was = atomicCAS(S.key + h, -1, last);
-            if (was == -1 || was == last) break;
+    if (to >= 0) {
+      const int most = P.width * P.page;
+      bool bad = to > most || len < 0 || len > most;
+      if (!bad && to > len) {
+        const int have = pages_of(P, len);
+        fresh = pages_of(P, to) - have;
+        first = have;
+        if (len != have * P.page) {
+          const int last = P.table[static_cast<int64_t>(b) * P.width + have - 1];
+          if (last < 0 || last >= P.pages) {
+            bad = true;
+          } else if (P.refs[last] > 1) {
+            uint32_t h = (static_cast<uint32_t>(last) * 2654435761u >> 16) & (hash - 1);
+            for (;; h = (h + 1) & (hash - 1)) {
+              const int was = atomicCAS(S.key + h, -1, last);
+              if (was == -1 || was == last) break;
+            }
+            atomicAdd(S.val + h, 1u << 16);
+            slot = h;
           }
-          atomicAdd(S.val + h, 1u << 16);
-          slot = h;
         }
       }
-    }
-    if (bad) {
-      atomicOr(P.status, kPagedBadIndex);
-      fresh = 0, first = 0, slot = kNoSlot;
+      if (bad) {
+        atomicOr(P.status, kPagedBadIndex);
+        fresh = 0, first = 0;
+      }
     }
     S.start[b] = fresh;
     S.first[b] = first;
     S.slot[b] = static_cast<uint16_t>(slot);
+  }
+
+  // The free pages of this CTA's chunks; of the first block each warp keeps which.
+  const uint32_t mine = ahead[0].free();
+  for (int i = 0; i < blocks; i += kReserveAhead) {
+    if (i) fetch(i);
+#pragma unroll
+    for (int j = 0; j < kReserveAhead; ++j) {
+      const uint32_t n = __reduce_add_sync(0xFFFFFFFFu, ahead[j].count());
+      if (lane == 0 && n) atomicAdd(&free_in[chunk_of(i + j)], n);
+    }
   }
   __syncthreads();
   // The highest row keeps a page all of whose holders grow.
@@ -274,7 +302,9 @@ __global__ void __launch_bounds__(kReserveThreads) pages_reserve_kernel(PagesVie
     if (static_cast<int>(count) == P.refs[S.key[h]]) atomicMax(S.val + h, count << 16 | (b + 1));
   }
   __syncthreads();
-  // Sums over the rows, in order.
+  // Sums over the rows, in order.  They stop at 2^31, more than any cache's pages:
+  // a start is exact below that, and beyond it nothing is granted.
+  uint32_t carry = 0;
   for (int b0 = 0; b0 < P.rows; b0 += kReserveThreads) {
     const int b = b0 + tid;
     uint32_t fresh = 0;
@@ -287,37 +317,40 @@ __global__ void __launch_bounds__(kReserveThreads) pages_reserve_kernel(PagesVie
       }
       fresh = min(fresh, static_cast<uint32_t>(P.pages) + 1u);
     }
-    // Sums stop at 2^31, more than any cache's pages.
     uint32_t x = fresh;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-      if (lane >= d) x = min(x + y, 0x80000000u);
+      if (lane >= d) x = capped_sum(x, y);
     }
     if (lane == 31) scan[warp] = x;
     __syncthreads();
-    uint32_t before = carry;
-    for (int w = 0; w < warp; ++w) before = min(before + scan[w], 0x80000000u);
-    const uint32_t upto = min(before + x, 0x80000000u);
-    __syncthreads();
-    if (b < P.rows) S.start[b] = upto - fresh;       // exact up to 2^31, and beyond it nothing is granted
-    if (tid == kReserveThreads - 1) {
-      carry = upto;
-      if (b0 + kReserveThreads >= P.rows) S.start[P.rows] = upto;
+    uint32_t w = scan[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, w, d);
+      if (lane >= d) w = capped_sum(w, y);
     }
+    const uint32_t all = __shfl_sync(0xFFFFFFFFu, w, 31), before = __shfl_sync(0xFFFFFFFFu, w, (warp + 31) & 31);
+    x = capped_sum(capped_sum(carry, warp ? before : 0u), x);
+    carry = capped_sum(carry, all);
+    if (b < P.rows) S.start[b] = x - fresh;
+    if (b == P.rows - 1) S.start[P.rows] = x;
     __syncthreads();
   }
 
   // The other CTAs' counts.
-  cluster_wait();
-  for (int i = tid; i < chunks * static_cast<int>(ctas); i += kReserveThreads) {
-    const uint32_t k = i / ctas, to = i - k * ctas;
-    if (k % ctas == rank && to != rank)
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&free_in[k], to)), "r"(free_in[k]) : "memory");
+  if (ctas > 1) {
+    cluster_wait();
+    for (int i = tid; i < chunks * ctas; i += kReserveThreads) {
+      const int k = i / ctas, other = i - k * ctas;
+      if (k % ctas == rank && other != rank)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&free_in[k], other)), "r"(free_in[k]) : "memory");
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();                                  // and no CTA reads the rows' state any more
   }
-  __syncwarp();
-  cluster_arrive();
-  cluster_wait();                                    // and no CTA reads the rows' state any more
   auto free_below = [&](int k) {                     // in the chunks before k
     uint32_t sum = 0;
     for (int i = lane; i < k; i += 32) sum += free_in[i];
@@ -335,67 +368,72 @@ __global__ void __launch_bounds__(kReserveThreads) pages_reserve_kernel(PagesVie
   __syncthreads();
   most = granted;
 
-  int32_t* src = copies;
-  int32_t* dst = copies + P.rows;
-  int32_t* tokens = dst + P.rows;
+  // The rows: which page is copied, and the lengths.
+  for (int b = rank * kReserveThreads + tid; b < P.rows; b += ctas * kReserveThreads) {
+    const bool fits = S.start[b + 1] <= total;
+    const uint32_t first = S.first[b];
+    int from = -1, n = 0;
+    if (first || S.start[b + 1] > S.start[b]) {      // it wants to grow
+      if (fits && (first & kMoves)) {
+        from = S.key[S.slot[b]];
+        n = P.lens[b] - static_cast<int>(first & ~kMoves) * P.page;
+        atomicSub(P.refs + from, 1);
+      }
+      if (fits) P.lens[b] = lens[b];
+    }
+    out.src[b] = from;
+    out.tokens[b] = n;
+    if (from < 0) out.dst[b] = -1;
+  }
+  // The pages.
   for (int k = rank; k < chunks; k += ctas) {
     uint32_t base = free_below(k);
     if (base >= most) break;                         // the whole CTA
-    int lo, hi;
-    place(k, lo, hi);
-    const uint32_t n = count(lo, hi);
-    if (lane == 0) warp_free[warp] = n;
-    __syncthreads();
-    base += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_free[lane] : 0u);
-    __syncthreads();
-    int row = 0;                                     // start[row] <= base
-    for (int p0 = lo; p0 < hi && base < most; p0 += 128 * kReserveBatch) {
-      uint32_t f[kReserveBatch];
-      free_of(P, p0, hi, f);
+    const int end = min(P.pages, (k + 1) * chunk);
+    for (int p0 = k * chunk; p0 < end && base < most; p0 += kReserveBlock) {
+      uint32_t f = mine;
+      if (p0 != rank * chunk) {
+        Block x;
+        x.load(P, p0, P.pages);
+        f = x.free();
+      }
+      // Ranks of the words: sums over all of the block's, in their order.
+      __syncthreads();
+      if (lane < kReserveWords) word_base[lane * kReserveWarps + warp] = __popc(f);
+      __syncthreads();
+      uint32_t x = tid < kReserveWarps * kReserveWords ? word_base[tid] : 0u;
+      const uint32_t own = x;
 #pragma unroll
-      for (int j = 0; j < kReserveBatch; ++j) {
-        if (base >= most) break;
-        row = row_of_rank(S.start, row, P.rows, base);
-        uint32_t r = base;                           // rank of this lane's first free page
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t mask = __ballot_sync(0xFFFFFFFFu, f[j] >> i & 1u);
-          r += __popc(mask & ((1u << lane) - 1u));
-          base += __popc(mask);
+      for (int d = 1; d < 32; d *= 2) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+        if (lane >= d) x += y;
+      }
+      if (lane == 31) scan[warp] = x;
+      __syncthreads();
+      x += base + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scan[lane] : 0u);
+      base += __reduce_add_sync(0xFFFFFFFFu, scan[lane]);
+      if (tid < kReserveWarps * kReserveWords) word_base[tid] = x - own;
+      __syncthreads();
+      const uint32_t at = word_base[(lane & (kReserveWords - 1)) * kReserveWarps + warp];
+      int row = 0;                                   // start[row] <= ranks to come
+#pragma unroll 1
+      for (uint32_t words = __ballot_sync(0xFFFFFFFFu, f && at < most); words; words &= words - 1) {
+        const int j = __ffs(words) - 1;
+        const uint32_t w = __shfl_sync(0xFFFFFFFFu, f, j);
+        const uint32_t r = __shfl_sync(0xFFFFFFFFu, at, j) + __popc(w & ((1u << lane) - 1u));
+        // Most often the whole word goes to one row.
+        const bool one = row + 1 >= P.rows || __shfl_sync(0xFFFFFFFFu, r, 31) < S.start[row + 1];
+        const int b = one ? row : row_of_rank(S.start, row, P.rows, r);
+        if (w >> lane & 1u && r < most) {
+          const int p = p0 + 32 * (j * kReserveWarps + warp) + lane;
+          const uint32_t first = S.first[b], col = r - S.start[b];
+          P.table[static_cast<int64_t>(b) * P.width + (first & ~kMoves) + col] = p;
+          P.refs[p] = 1;
+          if ((first & kMoves) && col == 0) out.dst[b] = p;
         }
-        int b = row;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if ((f[j] >> i & 1u) && r < most) {
-            const int p = p0 + 128 * j + 4 * lane + i;
-            b = row_of_rank(S.start, b, P.rows, r);
-            const uint32_t first = S.first[b], at = r - S.start[b];
-            P.table[static_cast<int64_t>(b) * P.width + (first & ~kMoves) + at] = p;
-            P.refs[p] = 1;
-            if ((first & kMoves) && at == 0) dst[b] = p;
-          }
-          r += f[j] >> i & 1u;
-        }
-        __syncwarp();
+        row = __shfl_sync(0xFFFFFFFFu, b, 0);
       }
     }
-  }
-  for (int b = rank * kReserveThreads + tid; b < P.rows; b += ctas * kReserveThreads) {
-    const int to = lens[b], len = P.lens[b];
-    const bool fits = S.start[b + 1] <= total;
-    const bool moves = fits && (S.first[b] & kMoves);
-    const bool grows = fits && to > len && len >= 0 && to <= P.width * P.page;
-    int from = -1, n = 0;
-    if (moves) {
-      from = S.key[S.slot[b]];
-      n = len % P.page;
-      atomicSub(P.refs + from, 1);
-    } else {
-      dst[b] = -1;
-    }
-    src[b] = from;
-    tokens[b] = n;
-    if (grows && (S.first[b] || S.start[b + 1] > S.start[b])) P.lens[b] = to;
   }
 }
 

@@ -67,6 +67,7 @@ ovc_status serve_init(int device) {
   if (g_serve_init[device]) return OVC_OK;
   if (cudaFuncSetAttribute(pages_reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(reserve_smem(kReserveRows))) != cudaSuccess ||
+      cudaFuncSetAttribute(pages_reserve_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
       cudaFuncSetAttribute(kv_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCompactSmem) != cudaSuccess)
     return OVC_ERR_CUDA;
   g_serve_init[device] = true;
@@ -80,18 +81,19 @@ using namespace ovc;
 
 extern "C" {
 
-ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int32_t* copies, void* stream) {
-  if (!pages_ok(p) || p->rows > kReserveRows || !at4(lens) || !at4(copies)) return OVC_ERR_INVALID_ARG;
+ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int32_t* src, int32_t* dst, int32_t* tokens,
+                                void* stream) {
+  if (!pages_ok(p) || p->rows > kReserveRows || !at4(lens) || !at4(src) || !at4(dst) || !at4(tokens)) return OVC_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   ovc_status st = device_state(&dev);
   if (st != OVC_OK) return st;
   st = serve_init(dev->index);
   if (st != OVC_OK) return st;
   int shift = 0;
-  while (p->pages > (int64_t{kReserveChunk} << shift) * kReserveChunks) ++shift;
-  const int ctas = clusters_for(1, (p->pages + kReserveChunk - 1) / kReserveChunk, kReserveClusters);
+  while (p->pages > (int64_t{kReserveBlock} << shift) * kReserveChunks) ++shift;
+  const int ctas = clusters_for(1, (p->pages - 1) / (kReserveBlock * kReserveAhead) + 1, kReserveClusters);
   return launch_clusters(pages_reserve_kernel, dim3(ctas), kReserveThreads, reserve_smem(static_cast<int>(p->rows)), ctas,
-                         static_cast<cudaStream_t>(stream), view(p, dev), lens, copies, shift);
+                         static_cast<cudaStream_t>(stream), view(p, dev), lens, ReserveOut{src, dst, tokens}, shift, reserve_hash(static_cast<int>(p->rows)));
 }
 
 ovc_status ovc_kv_pages_release(const ovc_kv_pages* p, const int32_t* lens, void* stream) {

@@ -21,6 +21,17 @@ def _floats(x: torch.Tensor, shape: tuple, what: str) -> int:
     return x.data_ptr()
 
 
+def _probs(x: torch.Tensor, rows: int, what: str) -> tuple[int, int, int]:
+    """Vocabulary, address and row stride."""
+    shape = x.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < 1:
+        raise ValueError(f"{what} must be [{rows}, vocabulary], got {tuple(shape)}")
+    strides = x.stride()
+    if strides[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{what} needs unit column stride")
+    return shape[1], x.data_ptr(), strides[0]
+
+
 def verify_drafts(target_probs: torch.Tensor, drafts: torch.Tensor, accept_u: torch.Tensor, sample_u: torch.Tensor, *,
                   draft_probs: torch.Tensor | None = None, cu_drafts: torch.Tensor | None = None, stream=None):
     """Verify the N drafted tokens of B sequences and draw the next token of each.
@@ -47,33 +58,36 @@ def verify_drafts(target_probs: torch.Tensor, drafts: torch.Tensor, accept_u: to
     dtype = _TYPES.get(target_probs.dtype)
     if dtype is None:
         raise TypeError(f"target_probs must be float32, bfloat16 or float16, got {target_probs.dtype}")
+    shape = drafts.shape
     if cu_drafts is None:
-        if drafts.dim() != 2:
-            raise ValueError(f"drafts must be [sequences, drafts] (or [drafts] with cu_drafts), got {tuple(drafts.shape)}")
-        cu, batch = None, drafts.shape[0]
+        if len(shape) != 2:
+            raise ValueError(f"drafts must be [sequences, drafts] (or [drafts] with cu_drafts), got {tuple(shape)}")
+        cu, batch = None, shape[0]
+        n = batch * shape[1]
     else:
-        if drafts.dim() != 1 or cu_drafts.dim() != 1 or cu_drafts.shape[0] < 1:
+        if len(shape) != 1 or cu_drafts.dim() != 1 or cu_drafts.shape[0] < 1:
             raise ValueError("with cu_drafts [sequences + 1], drafts must be [drafts]")
-        batch = cu_drafts.shape[0] - 1
+        n, batch = shape[0], cu_drafts.shape[0] - 1
         cu = _ints(cu_drafts, (batch + 1,), "cu_drafts")
-    n = drafts.numel()
-    pd, pu = _ints(drafts, drafts.shape, "drafts"), _floats(accept_u, drafts.shape, "accept_u")
+    pd, pu = _ints(drafts, shape, "drafts"), _floats(accept_u, shape, "accept_u")
     ps = _floats(sample_u, (batch,), "sample_u")
-    for x, rows, what in ((target_probs, n + batch, "target_probs"), (draft_probs, n, "draft_probs")):
-        if x is not None and (x.dim() != 2 or x.shape[0] != rows or x.shape[1] < 1 or (x.shape[1] > 1 and x.stride(1) != 1)):
-            raise ValueError(f"{what} must be [{rows}, vocabulary] with unit column stride, got {tuple(x.shape)}")
-    if draft_probs is not None and (draft_probs.shape[1] != target_probs.shape[1] or draft_probs.dtype != target_probs.dtype):
-        raise ValueError("draft_probs must have the vocabulary and dtype of target_probs")
-    desc = _abi.OvcDrafts(batch, n, target_probs.shape[1], cu, pd, target_probs.data_ptr(),
-                          None if draft_probs is None or n == 0 else draft_probs.data_ptr(), dtype, target_probs.stride(0),
-                          0 if draft_probs is None else draft_probs.stride(0), pu, ps)
+    vocab, target, stride = _probs(target_probs, n + batch, "target_probs")
+    draft, draft_stride = None, 0
+    if draft_probs is not None:
+        same, draft, draft_stride = _probs(draft_probs, n, "draft_probs")
+        if same != vocab or draft_probs.dtype != target_probs.dtype:
+            raise ValueError("draft_probs must have the vocabulary and dtype of target_probs")
+        if n == 0:
+            draft = None
+    desc = _abi.OvcDrafts(batch, n, vocab, cu, pd, target, draft, dtype, stride, draft_stride, pu, ps)
 
     def run(s):
-        out = torch.empty(n + 2 * batch, dtype=torch.int32, device=dev)
+        # two tensors: views of a new one take the host longer than allocating them
+        tokens = torch.empty(n + batch, dtype=torch.int32, device=dev)
+        accepted = torch.empty(batch, dtype=torch.int32, device=dev)
         if batch:
-            at = out.data_ptr()
-            check(lib().ovc_verify_drafts(_byref(desc), at, at + 4 * (n + batch), s), "ovc_verify_drafts")
-        return out[:n + batch], out[n + batch:]
+            check(lib().ovc_verify_drafts(_byref(desc), tokens.data_ptr(), accepted.data_ptr(), s), "ovc_verify_drafts")
+        return tokens, accepted
 
     return _call(dev, stream, run)
 

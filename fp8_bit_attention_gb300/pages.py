@@ -91,9 +91,10 @@ def kv_pages_reserve(pages: KVPages, lens: torch.Tensor, *, stream=None):
     pl = _ints(lens, (n,), "lens")
 
     def run(s):
-        copies = torch.empty((3, n), dtype=torch.int32, device=dev)
-        check(lib().ovc_kv_pages_reserve(pages._ref, pl, copies.data_ptr(), s), "ovc_kv_pages_reserve")
-        return copies.unbind(0)
+        # three tensors: views of a new one take the host longer than allocating them
+        src, dst, tokens = torch.empty_like(lens), torch.empty_like(lens), torch.empty_like(lens)
+        check(lib().ovc_kv_pages_reserve(pages._ref, pl, src.data_ptr(), dst.data_ptr(), tokens.data_ptr(), s), "ovc_kv_pages_reserve")
+        return src, dst, tokens
 
     return _call(dev, stream, run)
 

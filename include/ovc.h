@@ -557,11 +557,12 @@ typedef struct {
  * the highest row keeps it.  The lowest free pages are taken, in the order of
  * rows and then of columns.  A row grows only if the rows up to and including it
  * need no more pages than are free: kv_lens says which did.
- * copies [3, rows] receives, for each row whose last page was replaced, that page,
- * its successor, and the tokens to copy (ovc_kv_copy, in the cache of each layer,
- * before the next of these calls); -1, -1, 0 for the others.
+ * src, dst and tokens [rows] receive, for each row whose last page was replaced,
+ * that page, its successor, and the tokens to copy (ovc_kv_copy, in the cache of
+ * each layer, before the next of these calls); -1, -1, 0 for the others.
  * At most 8192 rows. */
-ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int32_t* copies, void* stream);
+ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int32_t* src, int32_t* dst, int32_t* tokens,
+                                void* stream);
 
 /* Let rows shrink to lens[b] tokens (not smaller, negative: it stays): pages
  * that hold none of them are given back (refs - 1, entry -1).  Giving back a page

@@ -89,7 +89,7 @@ BAD_PAGES = [dict(rows=0), dict(pages=0), dict(width=0), dict(page=8), dict(page
 @pytest.mark.parametrize("bad", BAD_PAGES, ids=str)
 def test_bad_pages_are_refused(lib, bad):  # noqa: F811
     p = _pages(**bad)
-    assert lib.ovc_kv_pages_reserve(R(p), B(0x1000), B(0x2000), None) == BAD
+    assert lib.ovc_kv_pages_reserve(R(p), B(0x1000), B(0x2000), B(0x3000), B(0x4000), None) == BAD
     assert lib.ovc_kv_pages_release(R(p), B(0x1000), None) == BAD
     assert lib.ovc_kv_pages_fork(R(p), B(0x1000), B(0x2000), 1, None) == BAD
     c = _cache(pages=p.pages, page=p.page)
@@ -99,8 +99,9 @@ def test_bad_pages_are_refused(lib, bad):  # noqa: F811
 def test_bad_lists_are_refused(lib):  # noqa: F811
     p, c = _pages(), _cache()
     for x in (None, 0x1002):
-        assert lib.ovc_kv_pages_reserve(R(p), B(x), B(0x2000), None) == BAD
-        assert lib.ovc_kv_pages_reserve(R(p), B(0x1000), B(x), None) == BAD
+        for i in range(4):
+            args = [B(x if i == j else 0x1000 * (j + 1)) for j in range(4)]
+            assert lib.ovc_kv_pages_reserve(R(p), *args, None) == BAD
         assert lib.ovc_kv_pages_release(R(p), B(x), None) == BAD
         assert lib.ovc_kv_pages_fork(R(p), B(x), B(0x2000), 1, None) == BAD
         assert lib.ovc_kv_pages_fork(R(p), B(0x1000), B(x), 1, None) == BAD
@@ -109,7 +110,7 @@ def test_bad_lists_are_refused(lib):  # noqa: F811
         assert lib.ovc_kv_compact(R(c), R(p), B(x), 0, B(0x2000), 5, None) == BAD
         assert lib.ovc_kv_compact(R(c), R(p), B(0x1000), 0, B(x), 5, None) == BAD
     assert lib.ovc_kv_copy(R(c), None, B(0x1000), B(0x2000), B(0x3002), 1, None) == BAD
-    assert lib.ovc_kv_pages_reserve(R(_pages(rows=8193)), B(0x1000), B(0x2000), None) == BAD
+    assert lib.ovc_kv_pages_reserve(R(_pages(rows=8193)), B(0x1000), B(0x2000), B(0x3000), B(0x4000), None) == BAD
     for n in (0, -1, 4):
         assert lib.ovc_kv_pages_fork(R(p), B(0x1000), B(0x2000), n, None) == BAD
     for n in (0, -1, 1 << 31):

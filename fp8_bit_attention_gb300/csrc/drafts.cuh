@@ -11,7 +11,9 @@ namespace ovc {
 
 constexpr int kDraftThreads = 256;
 constexpr int kDraftWarps = kDraftThreads / 32;
-constexpr int kDraftTile = 1024;                 // probabilities whose weights a warp sums into one, or a power of two times that
+constexpr int kDraftLoads = 8;                   // of 16 bytes a lane and row
+template <int kType>
+constexpr int kDraftTile = 32 * kDraftLoads * (kType == 2 ? 4 : 8);   // probabilities whose weights a warp sums into one, or a power of two times that
 constexpr int kDraftTiles = 1024;                // most tiles of a CTA
 constexpr int kDraftClusters = 8;                // most CTAs of a sequence
 constexpr int kDraftCtas = 2;                    // of an SM
@@ -27,7 +29,7 @@ struct DraftParams {
   const float* sample_u;
   int32_t* tokens;
   int32_t* accepted;
-  int32_t tile_shift;       // a tile is kDraftTile << tile_shift
+  int32_t tile_shift;       // a tile is kDraftTile<type> << tile_shift
   unsigned int* status;
 };
 
@@ -115,57 +117,75 @@ struct Sums {
   }
 };
 
-// 32 probabilities a lane of the 1024 from v0 on: 16 bytes a load where rows are
-// aligned (kVec), else one probability; zeros from v1 on.
-template <int kType, bool kVec>
+// The probabilities of a tile that a lane holds, kEach consecutive ones a load.
+// Tiles begin at multiples of 16 bytes of the target's row, wherever that begins;
+// a row of the draft's that lies otherwise is shifted into place.
+template <int kType>
 struct Line {
-  static constexpr int kEach = !kVec ? 1 : kType == 2 ? 4 : 8;     // of a load
-  static constexpr int kLoads = 32 / kEach;
-  uint32_t w[kType == 2 || !kVec ? 32 : 16];
+  static constexpr int kEach = kType == 2 ? 4 : 8;
+  static constexpr int kTile = kDraftTile<kType>;
+  uint32_t w[4 * kDraftLoads];
 
-  __device__ __forceinline__ static int64_t place(int64_t v0, int load) {
-    return v0 + load * (32 * kEach) + static_cast<int>(threadIdx.x & 31) * kEach;
+  // Where value i of this lane lies in a tile from v0 on.
+  __device__ __forceinline__ static int64_t place(int64_t v0, int i) {
+    return v0 + i / kEach * (32 * kEach) + static_cast<int>(threadIdx.x & 31) * kEach + i % kEach;
   }
-  __device__ __forceinline__ void one(const void* p, int64_t v, int i) {          // value i of the line
-    uint32_t x = 0;
-    if (kType == 2) x = __float_as_uint(prob<2>(p, v));
-    else x = __ldg(static_cast<const uint16_t*>(p) + v);
-    if (kType == 2 || !kVec) w[i] = x;
-    else w[i / 2] |= x << 16 * (i & 1);
+  __device__ __forceinline__ void set(int i, const void* p, int64_t v) {
+    if (kType == 2) w[i] = __ldg(static_cast<const uint32_t*>(p) + v);
+    else w[i / 2] |= static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + v)) << 16 * (i & 1);
   }
-  __device__ __forceinline__ void load(const void* p, int64_t v0, int64_t v1) {
-    if (v0 + kDraftTile <= v1) {
-      const uint8_t* at = static_cast<const uint8_t*>(p) + place(v0, 0) * (kType == 2 ? 4 : 2);
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        if (kVec) {
-          const uint4 x = __ldcs(reinterpret_cast<const uint4*>(at) + 32 * j);
-          w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
-        } else {
-          w[j] = kType == 2 ? __ldcs(reinterpret_cast<const uint32_t*>(at) + 32 * j) : __ldcs(reinterpret_cast<const uint16_t*>(at) + 32 * j);
-        }
-      }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < (kType == 2 || !kVec ? 32 : 16); ++i) w[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int64_t v = place(v0, i / kEach) + i % kEach;
-      if (v < v1) one(p, v, i);
-    }
-  }
-  // Value i as nothing.
   __device__ __forceinline__ void clear(int i) {
-    if (kType == 2 || !kVec) w[i] = 0u;
+    if (kType == 2) w[i] = 0u;
     else w[i / 2] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
   }
   // Values 2 i and 2 i + 1.
   __device__ __forceinline__ uint64_t two(int i) const {
     if (kType == 2) return pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-    const uint32_t x = kVec ? w[i] : w[2 * i] | w[2 * i + 1] << 16;
-    const float2 f = unpack2<kType == 1>(x);
+    const float2 f = unpack2<kType == 1>(w[i]);
     return pair(f.x, f.y);
+  }
+  // Row p of V probabilities, from v0 on.  `off`: how many values before a multiple of
+  // 16 bytes p + v0 lies behind (uniform over the warp).
+  __device__ __forceinline__ void load(const uint8_t* p, int64_t v0, int64_t V, int off) {
+    constexpr int kBytes = 16 / kEach;
+    if (v0 >= off && v0 + kTile + (off ? kEach : 0) <= V) {
+      const uint4* at = reinterpret_cast<const uint4*>(p + (place(v0, 0) - off) * kBytes);
+#pragma unroll
+      for (int j = 0; j < kDraftLoads; ++j) {
+        const uint4 x = __ldcs(at + 32 * j);
+        w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+      }
+      if (off) {
+        // What follows a lane's 16 bytes is the next lane's, and the next load's first after the last.
+        const uint4 end = __ldg(at + 32 * (kDraftLoads - 1) + 1);
+        const int words = off * kBytes / 4, bits = off * kBytes % 4 * 8;
+#pragma unroll
+        for (int j = 0; j < kDraftLoads; ++j) {
+          uint32_t c[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            c[k] = w[4 * j + k];
+            const uint32_t mine = (threadIdx.x & 31) == 0 && j + 1 < kDraftLoads ? w[(4 * j + 4 + k) % (4 * kDraftLoads)] : c[k];
+            c[4 + k] = __shfl_sync(0xFFFFFFFFu, mine, (threadIdx.x + 1) & 31);
+          }
+          if (j + 1 == kDraftLoads && (threadIdx.x & 31) == 31) c[4] = end.x, c[5] = end.y, c[6] = end.z, c[7] = end.w;
+#pragma unroll
+          for (int k = 0; k < 6; ++k) c[k] = words & 2 ? c[k + 2] : c[k];
+#pragma unroll
+          for (int k = 0; k < 5; ++k) c[k] = words & 1 ? c[k + 1] : c[k];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[4 * j + k] = __funnelshift_r(c[k], c[k + 1], bits);
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * kDraftLoads; ++i) w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < kEach * kDraftLoads; ++i) {
+      const int64_t v = place(v0, i);
+      if (v >= 0 && v < V) set(i, p, v);
+    }
   }
 };
 
@@ -183,8 +203,9 @@ __device__ __forceinline__ FF from_lane(const FF& x, int lane) {
   return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
 }
 
-template <int kType, bool kVec>
+template <int kType>
 __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kernel(DraftParams P) {
+  constexpr int kBytes = kType == 2 ? 4 : 2;
   __shared__ FF tile_own[kDraftTiles], tile_sum[kDraftTiles], part[kDraftWarps], cta_sum[kDraftClusters];
   __shared__ uint32_t stop;
   __shared__ int first_over, last_some, owner_tile;
@@ -237,7 +258,6 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
   }
 
   // Sums of the weights of this CTA's part of the vocabulary, tile by tile.
-  constexpr int kBytes = kType == 2 ? 4 : 2;
   const uint8_t* pr = static_cast<const uint8_t*>(P.target) + (row0 + kept) * P.target_stride * kBytes;
   const uint8_t* qr = nullptr;
   int64_t out = -1;                                   // a token that counts for nothing
@@ -245,34 +265,37 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
     if (P.draft) qr = static_cast<const uint8_t*>(P.draft) + static_cast<int64_t>(a0 + kept) * P.draft_stride * kBytes;
     else out = P.drafts[a0 + kept];
   }
-  const int tile = kDraftTile << P.tile_shift;
-  const int all_tiles = (P.V + tile - 1) / tile, per = (all_tiles + ctas - 1) / ctas;
+  using L = Line<kType>;
+  const auto behind = [](const uint8_t* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) / kBytes; };
+  const int skip = behind(pr), tile = L::kTile << P.tile_shift;       // tile t begins at token t * tile - skip
+  const int all_tiles = static_cast<int>((static_cast<int64_t>(P.V) + skip + tile - 1) / tile), per = (all_tiles + ctas - 1) / ctas;
   const int t0 = min(static_cast<int>(rank) * per, all_tiles), tiles = min(per, all_tiles - t0);
   FF mine, total, upto;                               // upto: of the CTAs up to the one with this lane's rank
   for (int pass = 0;; ++pass) {
+    const int off = qr ? (behind(qr) - skip) & (L::kEach - 1) : 0;
     for (int t = warp; t < tiles; t += kDraftWarps) {
       Sums a, c;
-      int64_t v0 = static_cast<int64_t>(t0 + t) * tile;
-      const int64_t v1 = v0 + tile < P.V ? v0 + tile : P.V;
-      for (; v0 < v1; v0 += kDraftTile) {
-        Line<kType, kVec> p;
-        p.load(pr, v0, v1);
+      int64_t v0 = static_cast<int64_t>(t0 + t) * tile - skip;
+#pragma unroll 1
+      for (int k = 0; k < 1 << P.tile_shift; ++k, v0 += L::kTile) {
+        L p;
+        p.load(pr, v0, P.V, 0);
         if (qr) {
-          Line<kType, kVec> q;
-          q.load(qr, v0, v1);
+          L q;
+          q.load(qr, v0, P.V, off);
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
+          for (int i = 0; i < L::kEach * kDraftLoads / 2; i += 2) {
             a.add(p.two(i), q.two(i));
             c.add(p.two(i + 1), q.two(i + 1));
           }
         } else {
-          if (out >= v0 && out < v0 + kDraftTile) {
+          if (out >= v0 && out < v0 + L::kTile) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (p.place(v0, i / p.kEach) + i % p.kEach == out) p.clear(i);
+            for (int i = 0; i < L::kEach * kDraftLoads; ++i)
+              if (p.place(v0, i) == out) p.clear(i);
           }
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
+          for (int i = 0; i < L::kEach * kDraftLoads / 2; i += 2) {
             a.add(p.two(i));
             c.add(p.two(i + 1));
           }
@@ -349,7 +372,7 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
   const int t = owner_tile;
   if (t) before = before + tile_sum[t - 1];
   // Its probabilities in order, a few consecutive ones a thread.
-  const int64_t v0 = static_cast<int64_t>(t0 + t) * tile;
+  const int64_t v0 = static_cast<int64_t>(t0 + t) * tile - skip;
   const int64_t v1 = v0 + tile < P.V ? v0 + tile : P.V;
   for (int64_t k = v0; k < v1; k += 4 * kDraftThreads) {
     FF w[4], own = {0.0f, 0.0f};
@@ -357,7 +380,7 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
     float p[4], q[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool there = v + j < v1 && v + j != out;
+      const bool there = v + j >= 0 && v + j < v1 && v + j != out;
       p[j] = there ? prob<kType>(pr, v + j) : 0.0f;
       q[j] = there && qr ? prob<kType>(qr, v + j) : 0.0f;
     }

@@ -60,20 +60,33 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(CopyParams P) {
 
 // ---------------------------------------------------------------------------
 // Compact, in place: position i of a sequence takes token keep[i] >= i.  A cluster
-// takes one head of K or V of one sequence and goes over the positions upwards,
-// a chunk of 256 for each of its CTAs at a time.  The tokens of later chunks lie
-// behind what a chunk writes (keep ascends, so keep[j] >= j), so they may be read
-// at any time; those of the same and earlier chunks have been read when the
-// cluster passes its barrier, and then the chunk is written.
+// takes one head of K or V of one sequence (or half of its channels) and goes over
+// the positions upwards, a chunk of 256 (512) for each of its CTAs at a time.  The
+// tokens of later chunks lie behind what a chunk writes (keep ascends, so keep[j]
+// >= j), so they may be read at any time; those of the same and earlier chunks
+// have been read when all CTAs of the cluster have said so, and then the chunk is
+// written.
 //
-// A warp moves 32 positions of a chunk through its own part of shared memory:
+// A warp moves 32 (64) positions of a chunk through its own part of shared memory:
 // list, page table, and tokens of the chunks ahead are on their way while one is
 // written.
 // ---------------------------------------------------------------------------
 constexpr int kCompactThreads = 256;
-constexpr int kCompactChunk = 256;                // positions of a CTA at a time: 32 a warp, 8 x 16 bytes a lane
-constexpr int kCompactStages = 3;                 // chunks in shared memory
-constexpr int kCompactSmem = kCompactStages * kCompactChunk * 128;
+constexpr int kCompactCtas = 2;                         // of an SM
+constexpr int kCompactClusters = 8;                     // most CTAs of a cluster
+constexpr int kCompactStages = 2;                       // chunks in shared memory
+constexpr uint64_t kCompactTimeoutNs = 4000000000ull;   // of a wait
+constexpr unsigned kStatusTimeoutBit = 1u;              // of the device status word
+
+template <int kRow>         // bytes of a token's codes: 128, or 64
+struct CompactShape {
+  static constexpr int kEach = 128 / kRow;              // positions a lane
+  static constexpr int kLanes = kRow / 16;              // of a token's codes
+  static constexpr int kChunk = kCompactThreads * kEach;
+  static constexpr int kCodes = kChunk * kRow;
+  static constexpr int kStage = kCodes + kChunk * 9;    // and words that hold the scales, rows to write, bytes of the words
+  static constexpr int kSmem = kCompactStages * kStage;
+};
 
 struct CompactParams {
   CacheView c;
@@ -87,14 +100,20 @@ struct CompactParams {
 __device__ __forceinline__ void copy_async16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
+__device__ __forceinline__ void copy_async4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
 
-__global__ void __launch_bounds__(kCompactThreads, 2) kv_compact_kernel(CompactParams C) {
+template <int kRow>
+__global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kernel(CompactParams C) {
+  using Shape = CompactShape<kRow>;
+  constexpr int kEach = Shape::kEach, kLanes = Shape::kLanes;
   extern __shared__ __align__(128) uint8_t tokens[];
-  __shared__ uint8_t scale_of[kCompactThreads];
-  __shared__ int found;
+  __shared__ __align__(8) uint64_t bars[kCompactStages];
+  __shared__ int found, abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = cluster_size(), rank = cluster_rank();
-  const int h = blockIdx.y >> 1, kv = blockIdx.y & 1, b = blockIdx.z;
+  const int part = blockIdx.y & (kEach - 1), kv = blockIdx.y / kEach & 1, h = blockIdx.y / (2 * kEach), b = blockIdx.z;
   const int a0 = C.cu[b], a1 = C.cu[b + 1];
   const int len = row_len(C.P, b), n = a1 - a0;
   if (a0 < 0 || a1 > C.n || n < 0 || len < 0 || n > len) {
@@ -115,8 +134,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) kv_compact_kernel(CompactP
     __syncthreads();
     const int f = found;
     __syncthreads();
-    const int part = f == hi ? (hi - lo) / step * step : f - step + 1 - lo;
-    lo += part;
+    lo += f == hi ? (hi - lo) / step * step : f - step + 1 - lo;
     hi = f;
     if (step == 1) {
       lo = f;
@@ -133,97 +151,142 @@ __global__ void __launch_bounds__(kCompactThreads, 2) kv_compact_kernel(CompactP
     if (tid == 0) atomicOr(C.P.status, kPagedBadIndex);
     return;                                       // all CTAs of the cluster see the same
   }
-  uint8_t* codes = kv ? C.c.v : C.c.k;
+  uint8_t* codes = (kv ? C.c.v : C.c.k) + part * kRow;
   uint8_t* scales = kv ? C.c.vs : C.c.ks;
 
-  // The same number of steps in every CTA; step s is this lane's position lo + s * stride + ...
-  const int stride = kCompactChunk * ctas, steps = (n - lo + stride - 1) / stride;
-  const int first = lo + rank * kCompactChunk + tid;
-  struct Ahead {            // of one position: its token and the one before it, the pages of both
-    int t, before, from, to;
+  // The same number of steps in every CTA; a lane's positions in step s are first +
+  // s * stride, and 32 more.
+  const int stride = Shape::kChunk * ctas, steps = (n - lo + stride - 1) / stride;
+  const int first = lo + rank * Shape::kChunk + warp * (32 * kEach) + lane;
+  struct Ahead {            // of some positions: their tokens and the one before them, the pages of both
+    int t[kEach], before, from[kEach], to[kEach];
   };
   // Each of the three uses what the one before it loaded a step earlier: a value
   // looked at in the step that loads it would make the warp wait for it.
-  auto listed = [&](int s, Ahead& x) {            // its token
+  auto listed = [&](int s, Ahead& x) {            // the tokens
     const int64_t i = first + static_cast<int64_t>(s) * stride;
-    x.t = i < n ? __ldg(keep + i) : -1;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) x.t[k] = i + 32 * k < n ? __ldg(keep + i + 32 * k) : -1;
     x.before = lane == 0 && i > 0 && i < n ? __ldg(keep + i - 1) : -1;
   };
-  auto paged = [&](int s, Ahead& x) {             // its pages
+  auto paged = [&](int s, Ahead& x) {             // their pages
     const int64_t i = first + static_cast<int64_t>(s) * stride;
-    const int up = __shfl_up_sync(0xFFFFFFFFu, x.t, 1);
-    const bool ok = i < n && x.t >= i && x.t > (lane ? up : x.before) && x.t < len;
-    if (!ok && i < n) atomicOr(C.P.status, kPagedBadIndex);
-    if (!ok) x.t = -1;
-    x.from = ok ? __ldg(table + x.t / C.P.by_page) : -1;
-    x.to = ok ? __ldg(table + static_cast<int>(i) / C.P.by_page) : -1;
+    int before = x.before;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int up = __shfl_up_sync(0xFFFFFFFFu, x.t[k], 1), last = __shfl_sync(0xFFFFFFFFu, x.t[k], 31);
+      const bool there = i + 32 * k < n, ok = there && x.t[k] >= i + 32 * k && x.t[k] > (lane ? up : before) && x.t[k] < len;
+      if (!ok && there) atomicOr(C.P.status, kPagedBadIndex);
+      if (!ok) x.t[k] = -1;
+      x.from[k] = ok ? __ldg(table + x.t[k] / C.P.by_page) : -1;
+      x.to[k] = ok ? __ldg(table + static_cast<int>(i + 32 * k) / C.P.by_page) : -1;
+      before = last;
+    }
   };
   auto row_of = [&](int t, int p) { return (p * C.c.heads + h) * C.c.page + (t - t / C.P.by_page * C.c.page); };
-  const uint32_t mine = smem_addr(tokens) + warp * (32 * 128) + lane * 16;
-  int to[kCompactStages], scale[kCompactStages];
-  auto fetch = [&](int s, int stage, const Ahead& x) {            // its token's codes and scale on their way
-    int from = -1;
-    to[stage] = -1;
-    if (x.t >= 0) {
-      if (x.from >= 0 && x.from < C.c.pages && x.to >= 0 && x.to < C.c.pages) {
-        from = row_of(x.t, x.from);
-        to[stage] = row_of(first + s * stride, x.to);
-      } else {
-        atomicOr(C.P.status, kPagedBadIndex);
+  const uint32_t base = smem_addr(tokens);
+  auto codes_at = [&](int stage) { return base + stage * Shape::kStage + warp * 4096 + lane * 16; };
+  auto scale_at = [&](int stage) { return base + stage * Shape::kStage + Shape::kCodes + tid * 4; };
+  auto row_at = [&](int stage) { return scale_at(stage) + Shape::kChunk * 4; };
+  auto byte_at = [&](int stage) { return base + stage * Shape::kStage + Shape::kCodes + Shape::kChunk * 8 + tid; };
+  auto fetch = [&](int s, int stage, const Ahead& x) {            // the tokens' codes and scales on their way
+    const uint32_t at = codes_at(stage);
+    int from[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      int to = -1;
+      from[k] = -1;
+      if (x.t[k] >= 0) {
+        if (x.from[k] >= 0 && x.from[k] < C.c.pages && x.to[k] >= 0 && x.to[k] < C.c.pages) {
+          from[k] = row_of(x.t[k], x.from[k]);
+          to = row_of(first + s * stride + 32 * k, x.to[k]);
+        } else {
+          atomicOr(C.P.status, kPagedBadIndex);
+        }
       }
+      if (part == 0 && from[k] >= 0) copy_async4(scale_at(stage) + k * (kCompactThreads * 4), scales + (from[k] & ~3));
+      // the row to write, and which byte of its scale's word is meant
+      asm volatile("st.shared.s32 [%0], %1;" ::"r"(row_at(stage) + k * (kCompactThreads * 4)), "r"(to) : "memory");
+      if (part == 0) asm volatile("st.shared.u8 [%0], %1;" ::"r"(byte_at(stage) + k * kCompactThreads), "r"(from[k] & 3) : "memory");
     }
-    scale[stage] = from >= 0 ? __ldcg(scales + from) : 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int row = __shfl_sync(0xFFFFFFFFu, from, 4 * j + (lane >> 3));
-      if (row >= 0) copy_async16(mine + stage * (kCompactChunk * 128) + j * 512, codes + static_cast<int64_t>(row) * 128 + (lane & 7) * 16);
+      const int row = __shfl_sync(0xFFFFFFFFu, from[j * kEach / 8], (j * (32 / kLanes) + lane / kLanes) & 31);
+      if (row >= 0) copy_async16(at + j * 512, codes + static_cast<int64_t>(row) * 128 + (lane & (kLanes - 1)) * 16);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  Ahead x0, x1, x2;
-  listed(0, x0);
-  listed(1, x1);
-  listed(2, x2);
-  paged(0, x0);
-  paged(1, x1);
-  fetch(0, 0, x0);
-  fetch(1, 1, x1);
-  x0 = x2;
-  paged(2, x0);
-  listed(3, x1);
-  int s = 0;
-  while (s < steps) {
-#pragma unroll
-    for (int stage = 0; stage < kCompactStages; ++stage, ++s) {   // step s is in `stage`
-      if (s >= steps) break;
-      fetch(s + 2, (stage + 2) % kCompactStages, x0);
-      x0 = x1;
-      paged(s + 3, x0);
-      listed(s + 4, x1);
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-      scale_of[tid] = scale[stage];               // what this thread reads has arrived
-      __syncwarp();
-      if (ctas > 1) {
-        // Only reads have to be over, and those are: no fence for what was written.
-        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-        cluster_wait();
-      } else {
-        __syncthreads();
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int row = __shfl_sync(0xFFFFFFFFu, to[stage], 4 * j + (lane >> 3));
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(mine + stage * (kCompactChunk * 128) + j * 512));
-        if (row >= 0) *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(row) * 128 + (lane & 7) * 16) = v;
-      }
-      if (to[stage] >= 0) scales[to[stage]] = scale_of[tid];
-      __syncwarp();
+  // A stage's barrier counts the warps of all CTAs that have read its chunk.
+  if (tid < kCompactStages) mbar_init(smem_addr(&bars[tid]), kCompactThreads / 32 * ctas);
+  if (tid == 0) abort = 0;
+  fence_mbar_init();
+  __syncthreads();
+  cluster_arrive();
+  Ahead x0, x1;
+#pragma unroll 1
+  for (int s = 0; s < kCompactStages - 1; ++s) {
+    listed(s, x0);
+    paged(s, x0);
+    fetch(s, s, x0);
+  }
+  listed(kCompactStages - 1, x0);
+  listed(kCompactStages, x1);
+  paged(kCompactStages - 1, x0);
+  cluster_wait();
+  // This warp's part of a chunk has arrived in shared memory: the CTAs are told.
+  // Only reads have to be over, so nothing that was written is waited for.
+  auto has_read = [&](int stage) {
+    __syncwarp();
+    if (lane < ctas)
+      asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(&bars[stage], lane)) : "memory");
+  };
+  asm volatile("cp.async.wait_group %0;" ::"n"(kCompactStages - 2) : "memory");
+  has_read(0);
+  int stage = 0;                                  // of chunk s
+  uint32_t parity = 0;
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s) {
+    fetch(s + kCompactStages - 1, stage ? stage - 1 : kCompactStages - 1, x0);
+    x0 = x1;
+    paged(s + kCompactStages, x0);
+    listed(s + kCompactStages + 1, x1);
+    bool ok = paged_wait(smem_addr(&bars[stage]), parity, kCompactTimeoutNs, &abort);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (!ok) {
+      abort = 1;
+      atomicOr(C.P.status, kStatusTimeoutBit);
+      break;
     }
+    const uint32_t at = codes_at(stage);
+    int to[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      asm volatile("ld.shared.s32 %0, [%1];" : "=r"(to[k]) : "r"(row_at(stage) + k * (kCompactThreads * 4)));
+      if (part == 0 && to[k] >= 0) {
+        uint32_t byte, e;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(byte_at(stage) + k * kCompactThreads));
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(scale_at(stage) + k * (kCompactThreads * 4) + byte));
+        scales[to[k]] = static_cast<uint8_t>(e);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int row = __shfl_sync(0xFFFFFFFFu, to[j * kEach / 8], (j * (32 / kLanes) + lane / kLanes) & 31);
+      uint4 v;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at + j * 512));
+      if (row >= 0) *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(row) * 128 + (lane & (kLanes - 1)) * 16) = v;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kCompactStages - 2) : "memory");
+    const int next = stage + 1 < kCompactStages ? stage + 1 : 0;
+    if (s + 1 < steps) has_read(next);
+    __syncwarp();
+    if (next == 0) parity ^= 1u;
+    stage = next;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  cluster_arrive();                               // no CTA leaves while others may still tell it something
+  cluster_wait();
 }
 
 }  // namespace ovc

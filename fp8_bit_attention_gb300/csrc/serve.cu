@@ -68,7 +68,8 @@ ovc_status serve_init(int device) {
   if (cudaFuncSetAttribute(pages_reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(reserve_smem(kReserveRows))) != cudaSuccess ||
       cudaFuncSetAttribute(pages_reserve_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-      cudaFuncSetAttribute(kv_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCompactSmem) != cudaSuccess)
+      cudaFuncSetAttribute(kv_compact_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, CompactShape<128>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(kv_compact_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, CompactShape<64>::kSmem) != cudaSuccess)
     return OVC_ERR_CUDA;
   g_serve_init[device] = true;
   return OVC_OK;
@@ -159,9 +160,15 @@ ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const in
   C.n = static_cast<int32_t>(n);
   st = serve_init(dev->index);
   if (st != OVC_OK) return st;
-  const int ctas = clusters_for(p->rows * c->heads * 2, 2 * dev->sms, 8);
-  return launch_clusters(kv_compact_kernel, dim3(ctas, static_cast<unsigned>(2 * c->heads), static_cast<unsigned>(p->rows)),
-                         kCompactThreads, kCompactSmem, ctas, static_cast<cudaStream_t>(stream), C);
+  const int64_t units = p->rows * c->heads * 2;
+  // Half the channels a CTA where clusters of the largest size would leave SMs
+  // without two CTAs.
+  const bool halves = units * kCompactClusters < kCompactCtas * dev->sms;
+  const int parts = halves ? 2 : 1;
+  const int ctas = clusters_for(units * parts, kCompactCtas * dev->sms, kCompactClusters);
+  return launch_clusters(halves ? kv_compact_kernel<64> : kv_compact_kernel<128>,
+                         dim3(ctas, static_cast<unsigned>(units / p->rows * parts), static_cast<unsigned>(p->rows)), kCompactThreads,
+                         halves ? CompactShape<64>::kSmem : CompactShape<128>::kSmem, ctas, static_cast<cudaStream_t>(stream), C);
 }
 
 ovc_status ovc_verify_drafts(const ovc_drafts* d, int32_t* tokens, int32_t* accepted, void* stream) {
@@ -194,14 +201,9 @@ ovc_status ovc_verify_drafts(const ovc_drafts* d, int32_t* tokens, int32_t* acce
   const int most = clusters_for(1, (d->V + 4095) / 4096, kDraftClusters);
   int ctas = 1;                                  // as many as run at once
   while (ctas < most && d->B * ctas * 2 <= kDraftCtas * dev->sms) ctas *= 2;
-  while ((d->V + (int64_t{kDraftTile} << P.tile_shift) - 1) / (int64_t{kDraftTile} << P.tile_shift) > int64_t{kDraftTiles} * ctas)
-    ++P.tile_shift;
-  const int64_t bytes = d->dtype == OVC_FP32 ? 4 : 2;
-  const bool vec = at16(d->target) && d->target_stride * bytes % 16 == 0 &&
-                   (!d->draft || (at16(d->draft) && d->draft_stride * bytes % 16 == 0));
-  auto* fn = d->dtype == OVC_FP32   ? (vec ? verify_drafts_kernel<2, true> : verify_drafts_kernel<2, false>)
-             : d->dtype == OVC_FP16 ? (vec ? verify_drafts_kernel<1, true> : verify_drafts_kernel<1, false>)
-                                    : (vec ? verify_drafts_kernel<0, true> : verify_drafts_kernel<0, false>);
+  const int64_t tile = d->dtype == OVC_FP32 ? kDraftTile<2> : kDraftTile<0>;
+  while (d->V + 7 > (tile << P.tile_shift) * kDraftTiles * ctas) ++P.tile_shift;       // rows begin up to 7 tokens behind a tile
+  auto* fn = d->dtype == OVC_FP32 ? verify_drafts_kernel<2> : d->dtype == OVC_FP16 ? verify_drafts_kernel<1> : verify_drafts_kernel<0>;
   return launch_clusters(fn, dim3(static_cast<unsigned>(d->B * ctas)), kDraftThreads, 0, ctas, static_cast<cudaStream_t>(stream), P);
 }
 

@@ -9,8 +9,9 @@
 
 namespace ovc {
 
-constexpr int kDraftThreads = 256;
-constexpr int kDraftWarps = kDraftThreads / 32;
+// Threads of a CTA: without the draft's probabilities a thread holds half as much.
+template <bool kDraft>
+constexpr int kDraftThreads = kDraft ? 256 : 512;
 constexpr int kDraftLoads = 8;                   // of 16 bytes a lane and row
 template <int kType>
 constexpr int kDraftTile = 32 * kDraftLoads * (kType == 2 ? 4 : 8);   // probabilities whose weights a warp sums into one, or a power of two times that
@@ -134,9 +135,15 @@ struct Line {
     if (kType == 2) w[i] = __ldg(static_cast<const uint32_t*>(p) + v);
     else w[i / 2] |= static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + v)) << 16 * (i & 1);
   }
-  __device__ __forceinline__ void clear(int i) {
-    if (kType == 2) w[i] = 0u;
-    else w[i / 2] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+  // The value of token v, if it is in the tile from v0 on and this lane's, as nothing.
+  __device__ __forceinline__ void clear(int64_t v0, int64_t v) {
+    const int i = static_cast<int>(v - v0), at = i / kEach;
+    if (i < 0 || i >= kTile || (at & 31) != static_cast<int>(threadIdx.x & 31)) return;
+    const uint32_t keep = kType == 2 ? 0u : i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    const int word = at / 32 * 4 + (kType == 2 ? i & 3 : (i & 7) / 2);
+#pragma unroll
+    for (int k = 0; k < 4 * kDraftLoads; ++k)
+      if (k == word) w[k] &= keep;
   }
   // Values 2 i and 2 i + 1.
   __device__ __forceinline__ uint64_t two(int i) const {
@@ -144,38 +151,63 @@ struct Line {
     const float2 f = unpack2<kType == 1>(w[i]);
     return pair(f.x, f.y);
   }
-  // Row p of V probabilities, from v0 on.  `off`: how many values before a multiple of
-  // 16 bytes p + v0 lies behind (uniform over the warp).
-  __device__ __forceinline__ void load(const uint8_t* p, int64_t v0, int64_t V, int off) {
+  // Row p of V probabilities, from v0 on, where p + v0 is a multiple of 16 bytes;
+  // what does not fill 16 bytes at the row's ends is left out (edge()).
+  __device__ __forceinline__ void load(const uint8_t* p, int64_t v0, int64_t V) {
+    const uint4* at = reinterpret_cast<const uint4*>(p + place(v0, 0) * (16 / kEach));
+    if (v0 >= 0 && v0 + kTile <= V) {
+#pragma unroll
+      for (int j = 0; j < kDraftLoads; ++j) {
+        const uint4 x = __ldcs(at + 32 * j);
+        w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+      }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < kDraftLoads; ++j) {
+      const int64_t v = place(v0, j * kEach);
+      const uint4 x = v >= 0 && v + kEach <= V ? __ldcs(at + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+      w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+    }
+  }
+  // The token of this lane among those that load() leaves out of a tile, or -1.
+  __device__ __forceinline__ static int64_t edge(int64_t v0, int64_t V) {
+    const int lane = threadIdx.x & 31;
+    const int64_t first = v0 < 0 ? v0 + kEach : 0;                       // of the row's first whole 16 bytes (-kEach < v0)
+    if (lane < kEach) return lane < first && lane < V ? lane : -1;
+    const int64_t tail = V - (V - v0) % kEach, v = tail + lane - kEach;  // behind the last
+    return v0 + kTile > V && tail >= first && lane < 2 * kEach && v < V ? v : -1;
+  }
+  // The same, of a row that lies otherwise: p + v0 lies `off` values behind a
+  // multiple of 16 bytes (uniform over the warp, not 0).  Nothing is left out.
+  __device__ __forceinline__ void load_shifted(const uint8_t* p, int64_t v0, int64_t V, int off) {
     constexpr int kBytes = 16 / kEach;
-    if (v0 >= off && v0 + kTile + (off ? kEach : 0) <= V) {
+    if (v0 >= off && v0 + kTile + kEach <= V) {
       const uint4* at = reinterpret_cast<const uint4*>(p + (place(v0, 0) - off) * kBytes);
 #pragma unroll
       for (int j = 0; j < kDraftLoads; ++j) {
         const uint4 x = __ldcs(at + 32 * j);
         w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
       }
-      if (off) {
-        // What follows a lane's 16 bytes is the next lane's, and the next load's first after the last.
-        const uint4 end = __ldg(at + 32 * (kDraftLoads - 1) + 1);
-        const int words = off * kBytes / 4, bits = off * kBytes % 4 * 8;
+      // What follows a lane's 16 bytes is the next lane's, and the next load's first after the last.
+      const uint4 end = __ldg(at + 32 * (kDraftLoads - 1) + 1);
+      const int words = off * kBytes / 4, bits = off * kBytes % 4 * 8;
 #pragma unroll
-        for (int j = 0; j < kDraftLoads; ++j) {
-          uint32_t c[8];
+      for (int j = 0; j < kDraftLoads; ++j) {
+        uint32_t c[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            c[k] = w[4 * j + k];
-            const uint32_t mine = (threadIdx.x & 31) == 0 && j + 1 < kDraftLoads ? w[(4 * j + 4 + k) % (4 * kDraftLoads)] : c[k];
-            c[4 + k] = __shfl_sync(0xFFFFFFFFu, mine, (threadIdx.x + 1) & 31);
-          }
-          if (j + 1 == kDraftLoads && (threadIdx.x & 31) == 31) c[4] = end.x, c[5] = end.y, c[6] = end.z, c[7] = end.w;
-#pragma unroll
-          for (int k = 0; k < 6; ++k) c[k] = words & 2 ? c[k + 2] : c[k];
-#pragma unroll
-          for (int k = 0; k < 5; ++k) c[k] = words & 1 ? c[k + 1] : c[k];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[4 * j + k] = __funnelshift_r(c[k], c[k + 1], bits);
+        for (int k = 0; k < 4; ++k) {
+          c[k] = w[4 * j + k];
+          const uint32_t mine = (threadIdx.x & 31) == 0 && j + 1 < kDraftLoads ? w[(4 * j + 4 + k) % (4 * kDraftLoads)] : c[k];
+          c[4 + k] = __shfl_sync(0xFFFFFFFFu, mine, (threadIdx.x + 1) & 31);
         }
+        if (j + 1 == kDraftLoads && (threadIdx.x & 31) == 31) c[4] = end.x, c[5] = end.y, c[6] = end.z, c[7] = end.w;
+#pragma unroll
+        for (int k = 0; k < 6; ++k) c[k] = words & 2 ? c[k + 2] : c[k];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) c[k] = words & 1 ? c[k + 1] : c[k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[4 * j + k] = __funnelshift_r(c[k], c[k + 1], bits);
       }
       return;
     }
@@ -203,16 +235,17 @@ __device__ __forceinline__ FF from_lane(const FF& x, int lane) {
   return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
 }
 
-template <int kType>
-__global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kernel(DraftParams P) {
+template <int kType, bool kDraft>
+__global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_drafts_kernel(DraftParams P) {
+  constexpr int kThreads = kDraftThreads<kDraft>, kWarps = kThreads / 32;
   constexpr int kBytes = kType == 2 ? 4 : 2;
-  __shared__ FF tile_own[kDraftTiles], tile_sum[kDraftTiles], part[kDraftWarps], cta_sum[kDraftClusters];
+  __shared__ FF tile_own[kDraftTiles], tile_sum[kDraftTiles], part[kWarps], cta_sum[kDraftClusters];
   __shared__ uint32_t stop;
   __shared__ int first_over, last_some, owner_tile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
   const int b = blockIdx.x / ctas;
-  cluster_arrive();
+  cluster_begun();
 
   const int a0 = P.cu ? P.cu[b] : b * P.each, a1 = P.cu ? P.cu[b + 1] : a0 + P.each;
   if (a0 < 0 || a1 < a0 || a1 > P.N) {                // all CTAs of the cluster
@@ -230,7 +263,7 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
   // The first draft that does not stay: 2 i, or 2 i + 1 where there is none at i.
   if (tid == 0) stop = 2u * n + 1u;
   __syncthreads();
-  for (int i0 = 0; i0 < n; i0 += kDraftThreads) {
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + tid;
     if (i < n) {
       const int x = P.drafts[a0 + i];
@@ -240,19 +273,19 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
         if (x >= P.V) atomicOr(P.status, kPagedBadIndex);
       } else {
         const float p = prob<kType>(P.target, (row0 + i) * P.target_stride + x);
-        const float q = P.draft ? prob<kType>(P.draft, static_cast<int64_t>(a0 + i) * P.draft_stride + x) : 1.0f;
+        const float q = kDraft ? prob<kType>(P.draft, static_cast<int64_t>(a0 + i) * P.draft_stride + x) : 1.0f;
         // 24 by 24 bits: exact in 64
         if (!(static_cast<double>(u) * q < p)) atomicMin(&stop, 2u * i);
       }
     }
     __syncthreads();
-    if (stop < 2u * (i0 + kDraftThreads)) break;
+    if (stop < 2u * (i0 + kThreads)) break;
     __syncthreads();
   }
   const int kept = stop >> 1;
   const bool rejected = !(stop & 1u);
   if (rank == 0) {
-    for (int i = tid; i <= n; i += kDraftThreads)
+    for (int i = tid; i <= n; i += kThreads)
       if (i != kept) P.tokens[row0 + i] = i < kept ? P.drafts[a0 + i] : -1;
     if (tid == 0) P.accepted[b] = kept;
   }
@@ -262,7 +295,7 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
   const uint8_t* qr = nullptr;
   int64_t out = -1;                                   // a token that counts for nothing
   if (rejected) {
-    if (P.draft) qr = static_cast<const uint8_t*>(P.draft) + static_cast<int64_t>(a0 + kept) * P.draft_stride * kBytes;
+    if (kDraft) qr = static_cast<const uint8_t*>(P.draft) + static_cast<int64_t>(a0 + kept) * P.draft_stride * kBytes;
     else out = P.drafts[a0 + kept];
   }
   using L = Line<kType>;
@@ -272,34 +305,40 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
   const int t0 = min(static_cast<int>(rank) * per, all_tiles), tiles = min(per, all_tiles - t0);
   FF mine, total, upto;                               // upto: of the CTAs up to the one with this lane's rank
   for (int pass = 0;; ++pass) {
-    const int off = qr ? (behind(qr) - skip) & (L::kEach - 1) : 0;
-    for (int t = warp; t < tiles; t += kDraftWarps) {
+    const int off = kDraft && qr ? (behind(qr) - skip) & (L::kEach - 1) : 0;
+    for (int t = warp; t < tiles; t += kWarps) {
       Sums a, c;
       int64_t v0 = static_cast<int64_t>(t0 + t) * tile - skip;
 #pragma unroll 1
-      for (int k = 0; k < 1 << P.tile_shift; ++k, v0 += L::kTile) {
+      for (int k = 0; k < 1 << P.tile_shift && v0 < P.V; ++k, v0 += L::kTile) {
         L p;
-        p.load(pr, v0, P.V, 0);
-        if (qr) {
+        p.load(pr, v0, P.V);
+        float edge_p = 0.0f, edge_q = 0.0f;
+        if (v0 < 0 || v0 + L::kTile > P.V) {
+          const int64_t v = L::edge(v0, P.V);
+          if (v >= 0 && v != out) {
+            edge_p = prob<kType>(pr, v);
+            if (kDraft && qr) edge_q = prob<kType>(qr, v);
+          }
+        }
+        if (kDraft && qr) {
           L q;
-          q.load(qr, v0, P.V, off);
+          if (off) q.load_shifted(qr, v0, P.V, off);
+          else q.load(qr, v0, P.V);
 #pragma unroll
           for (int i = 0; i < L::kEach * kDraftLoads / 2; i += 2) {
             a.add(p.two(i), q.two(i));
             c.add(p.two(i + 1), q.two(i + 1));
           }
         } else {
-          if (out >= v0 && out < v0 + L::kTile) {
-#pragma unroll
-            for (int i = 0; i < L::kEach * kDraftLoads; ++i)
-              if (p.place(v0, i) == out) p.clear(i);
-          }
+          if (!kDraft && out >= 0) p.clear(v0, out);
 #pragma unroll
           for (int i = 0; i < L::kEach * kDraftLoads / 2; i += 2) {
             a.add(p.two(i));
             c.add(p.two(i + 1));
           }
         }
+        a.add(pair(edge_p, 0.0f), pair(edge_q, 0.0f));
       }
       FF w = a.sum() + c.sum();
 #pragma unroll
@@ -374,7 +413,7 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
   // Its probabilities in order, a few consecutive ones a thread.
   const int64_t v0 = static_cast<int64_t>(t0 + t) * tile - skip;
   const int64_t v1 = v0 + tile < P.V ? v0 + tile : P.V;
-  for (int64_t k = v0; k < v1; k += 4 * kDraftThreads) {
+  for (int64_t k = v0; k < v1; k += 4 * kThreads) {
     FF w[4], own = {0.0f, 0.0f};
     const int64_t v = k + 4 * tid;
     float p[4], q[4];
@@ -382,7 +421,7 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
     for (int j = 0; j < 4; ++j) {
       const bool there = v + j >= 0 && v + j < v1 && v + j != out;
       p[j] = there ? prob<kType>(pr, v + j) : 0.0f;
-      q[j] = there && qr ? prob<kType>(qr, v + j) : 0.0f;
+      q[j] = kDraft && there && qr ? prob<kType>(qr, v + j) : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -392,7 +431,7 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
     const FF in_warp = warp_scan<32>(own);
     if (lane == 31) part[warp] = in_warp;
     __syncthreads();
-    const FF parts = warp_scan<kDraftWarps>(lane < kDraftWarps ? part[lane] : FF{0.0f, 0.0f});
+    const FF parts = warp_scan<kWarps>(lane < kWarps ? part[lane] : FF{0.0f, 0.0f});
     const FF ahead = from_lane(parts, warp ? warp - 1 : 0);
     const FF up = warp ? before + ahead + in_warp : before + in_warp;
     // A thread within whose numbers it may exceed goes through them once more.
@@ -412,7 +451,7 @@ __global__ void __launch_bounds__(kDraftThreads, kDraftCtas) verify_drafts_kerne
     }
     __syncthreads();
     if (first_over != 0x7FFFFFFF) break;
-    before = before + from_lane(parts, kDraftWarps - 1);
+    before = before + from_lane(parts, kWarps - 1);
   }
   if (tid == 0) P.tokens[row0 + kept] = first_over != 0x7FFFFFFF ? first_over : last_some;
 }

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
       asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(&bars[stage], lane)) : "memory");
   };
   asm volatile("cp.async.wait_group %0;" ::"n"(kCompactStages - 2) : "memory");
-  has_read(0);
+  if (steps > 0) has_read(0);                     // all that is told is waited for
   int stage = 0;                                  // of chunk s
   uint32_t parity = 0;
 #pragma unroll 1
@@ -285,7 +285,10 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
-  cluster_arrive();                               // no CTA leaves while others may still tell it something
+  // No CTA leaves while others may still tell it something: the barrier's release
+  // orders what was told before it (a relaxed one does not, and an arrival at a CTA
+  // that has left faults).
+  cluster_arrive();
   cluster_wait();
 }
 

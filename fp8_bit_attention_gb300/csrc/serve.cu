@@ -203,8 +203,13 @@ ovc_status ovc_verify_drafts(const ovc_drafts* d, int32_t* tokens, int32_t* acce
   while (ctas < most && d->B * ctas * 2 <= kDraftCtas * dev->sms) ctas *= 2;
   const int64_t tile = d->dtype == OVC_FP32 ? kDraftTile<2> : kDraftTile<0>;
   while (d->V + 7 > (tile << P.tile_shift) * kDraftTiles * ctas) ++P.tile_shift;       // rows begin up to 7 tokens behind a tile
-  auto* fn = d->dtype == OVC_FP32 ? verify_drafts_kernel<2> : d->dtype == OVC_FP16 ? verify_drafts_kernel<1> : verify_drafts_kernel<0>;
-  return launch_clusters(fn, dim3(static_cast<unsigned>(d->B * ctas)), kDraftThreads, 0, ctas, static_cast<cudaStream_t>(stream), P);
+  const auto launch = [&](auto* with, auto* without) {
+    return launch_clusters(d->draft ? with : without, dim3(static_cast<unsigned>(d->B * ctas)),
+                           d->draft ? kDraftThreads<true> : kDraftThreads<false>, 0, ctas, static_cast<cudaStream_t>(stream), P);
+  };
+  if (d->dtype == OVC_FP32) return launch(verify_drafts_kernel<2, true>, verify_drafts_kernel<2, false>);
+  if (d->dtype == OVC_FP16) return launch(verify_drafts_kernel<1, true>, verify_drafts_kernel<1, false>);
+  return launch(verify_drafts_kernel<0, true>, verify_drafts_kernel<0, false>);
 }
 
 }  // extern "C"

@@ -95,14 +95,12 @@ __device__ __forceinline__ uint64_t sub_pairs(uint64_t a, uint64_t b) {
 struct Sums {
   uint64_t hi = 0, lo = 0;
 
-  // A NaN or negative p counts as nothing (fmaxf drops a NaN).
-  __device__ __forceinline__ void add(uint64_t p) {
-    const float2 x = unpair(p);
-    const uint64_t d = pair(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f));
+  __device__ __forceinline__ void add(uint64_t d) {
     const uint64_t s = add_pairs(hi, d), t = sub_pairs(s, hi);
     lo = add_pairs(lo, add_pairs(sub_pairs(hi, sub_pairs(s, t)), sub_pairs(d, t)));
     hi = s;
   }
+  // max(p - q, 0): fmaxf drops a NaN.
   __device__ __forceinline__ void add(uint64_t p, uint64_t q) {
     const uint64_t c = sub_pairs(p, q);
     const float2 x = unpair(c), y = unpair(sub_pairs(sub_pairs(p, c), q));
@@ -149,6 +147,15 @@ struct Line {
   __device__ __forceinline__ uint64_t two(int i) const {
     if (kType == 2) return pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     const float2 f = unpack2<kType == 1>(w[i]);
+    return pair(f.x, f.y);
+  }
+  // The same, NaN and what is negative as 0.
+  __device__ __forceinline__ uint64_t two_weights(int i) const {
+    if (kType == 2) return pair(fmaxf(__uint_as_float(w[2 * i]), 0.0f), fmaxf(__uint_as_float(w[2 * i + 1]), 0.0f));
+    uint32_t x;
+    if (kType == 1) asm("max.f16x2 %0, %1, %2;" : "=r"(x) : "r"(w[i]), "r"(0u));
+    else asm("max.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[i]), "r"(0u));
+    const float2 f = unpack2<kType == 1>(x);
     return pair(f.x, f.y);
   }
   // Row p of V probabilities, from v0 on, where p + v0 is a multiple of 16 bytes;
@@ -334,8 +341,8 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
           if (!kDraft && out >= 0) p.clear(v0, out);
 #pragma unroll
           for (int i = 0; i < L::kEach * kDraftLoads / 2; i += 2) {
-            a.add(p.two(i));
-            c.add(p.two(i + 1));
+            a.add(p.two_weights(i));
+            c.add(p.two_weights(i + 1));
           }
         }
         a.add(pair(edge_p, 0.0f), pair(edge_q, 0.0f));

@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
   constexpr int kThreads = kDraftThreads<kDraft>, kWarps = kThreads / 32;
   constexpr int kBytes = kType == 2 ? 4 : 2;
   __shared__ FF tile_own[kDraftTiles], tile_sum[kDraftTiles], part[kWarps], cta_sum[kDraftClusters];
+  __shared__ int again;
   __shared__ uint32_t stop;
   __shared__ int first_over, last_some, owner_tile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -255,17 +256,10 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
   cluster_begun();
 
   const int a0 = P.cu ? P.cu[b] : b * P.each, a1 = P.cu ? P.cu[b + 1] : a0 + P.each;
-  if (a0 < 0 || a1 < a0 || a1 > P.N) {                // all CTAs of the cluster
-    if (rank == 0 && tid == 0) {
-      P.accepted[b] = 0;
-      atomicOr(P.status, kPagedBadIndex);
-    }
-    __syncwarp();
-    cluster_wait();
-    return;
-  }
-  const int n = a1 - a0;
-  const int64_t row0 = static_cast<int64_t>(a0) + b;  // of the target's probabilities
+  // No CTA leaves before the last barrier, whatever it finds: others write to it.
+  const bool bad = a0 < 0 || a1 < a0 || a1 > P.N;
+  const int n = bad ? 0 : a1 - a0;
+  const int64_t row0 = bad ? 0 : static_cast<int64_t>(a0) + b;         // of the target's probabilities
 
   // The first draft that does not stay: 2 i, or 2 i + 1 where there is none at i.
   if (tid == 0) stop = 2u * n + 1u;
@@ -294,7 +288,10 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
   if (rank == 0) {
     for (int i = tid; i <= n; i += kThreads)
       if (i != kept) P.tokens[row0 + i] = i < kept ? P.drafts[a0 + i] : -1;
-    if (tid == 0) P.accepted[b] = kept;
+    if (tid == 0) {
+      P.accepted[b] = kept;
+      if (bad) atomicOr(P.status, kPagedBadIndex);
+    }
   }
 
   // Sums of the weights of this CTA's part of the vocabulary, tile by tile.
@@ -309,7 +306,7 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
   const auto behind = [](const uint8_t* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) / kBytes; };
   const int skip = behind(pr), tile = L::kTile << P.tile_shift;       // tile t begins at token t * tile - skip
   const int all_tiles = static_cast<int>((static_cast<int64_t>(P.V) + skip + tile - 1) / tile), per = (all_tiles + ctas - 1) / ctas;
-  const int t0 = min(static_cast<int>(rank) * per, all_tiles), tiles = min(per, all_tiles - t0);
+  const int t0 = min(static_cast<int>(rank) * per, all_tiles), tiles = bad ? 0 : min(per, all_tiles - t0);
   FF mine, total, upto;                               // upto: of the CTAs up to the one with this lane's rank
   for (int pass = 0;; ++pass) {
     const int off = kDraft && qr ? (behind(qr) - skip) & (L::kEach - 1) : 0;
@@ -370,13 +367,15 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
       if (lane < ctas)
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(&cta_sum[rank], lane)), "f"(mine.hi), "f"(mine.lo)
                      : "memory");
+      if (rank == 0 && lane < ctas)                   // whether there is another row to draw from
+        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(&again, lane)), "r"(static_cast<int>(!pass && (qr || out >= 0))) : "memory");
       __syncwarp();
     }
     cluster_arrive();
     cluster_wait();
     upto = warp_scan<kDraftClusters>(lane < ctas ? cta_sum[lane] : FF{0.0f, 0.0f});
     total = from_lane(upto, kDraftClusters - 1);
-    if (total.hi > 0.0f || (!qr && out < 0) || pass) break;
+    if (total.hi > 0.0f || !again) break;
     // Nothing is left of p - q: p itself.
     __syncwarp();
     cluster_arrive();
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
     out = -1;
   }
   if (!(total.hi > 0.0f)) {
-    if (rank == 0 && tid == 0) P.tokens[row0 + kept] = -1;
+    if (rank == 0 && tid == 0 && !bad) P.tokens[row0 + kept] = -1;
     return;
   }
 

@@ -115,11 +115,12 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   const int ctas = cluster_size(), rank = cluster_rank();
   const int part = blockIdx.y & (kEach - 1), kv = blockIdx.y / kEach & 1, h = blockIdx.y / (2 * kEach), b = blockIdx.z;
   const int a0 = C.cu[b], a1 = C.cu[b + 1];
-  const int len = row_len(C.P, b), n = a1 - a0;
-  if (a0 < 0 || a1 > C.n || n < 0 || len < 0 || n > len) {
-    if (tid == 0 && (len >= 0 || n != 0)) atomicOr(C.P.status, kPagedBadIndex);
-    return;                                       // all CTAs of the cluster
-  }
+  const int len = row_len(C.P, b);
+  // No CTA leaves before the last barrier, whatever it finds: others may still tell
+  // it something.
+  bool bad = a0 < 0 || a1 < a0 || a1 > C.n || len < 0 || a1 - a0 > len;
+  if (bad && tid == 0) atomicOr(C.P.status, kPagedBadIndex);
+  const int n = bad ? 0 : a1 - a0;
   const int32_t* keep = C.keep + h * C.keep_stride + a0;
   const int32_t* table = C.P.table + static_cast<int64_t>(b) * C.P.width;
 
@@ -141,22 +142,16 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
       break;
     }
   }
-  // Pages that would be written must be this row's own.
-  int bad = 0;
-  for (int c = lo / C.P.by_page + tid; lo < n && c <= (n - 1) / C.P.by_page; c += kCompactThreads) {
-    const int p = table[c];
-    bad |= p < 0 || p >= C.c.pages || C.P.refs[p] > 1;
-  }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) atomicOr(C.P.status, kPagedBadIndex);
-    return;                                       // all CTAs of the cluster see the same
-  }
+  // Pages that will be written must be this row's own: looked up here, and told
+  // when the first tokens are on their way.
+  const int written = lo < n ? (n - 1) / C.P.by_page + 1 : 0;     // the first column behind them
+  int column = lo / C.P.by_page + tid, page = column < written ? __ldg(table + column) : -1;
   uint8_t* codes = (kv ? C.c.v : C.c.k) + part * kRow;
   uint8_t* scales = kv ? C.c.vs : C.c.ks;
 
-  // The same number of steps in every CTA; a lane's positions in step s are first +
+  // The CTAs take the same number of steps; a lane's positions in step s are first +
   // s * stride, and 32 more.
-  const int stride = Shape::kChunk * ctas, steps = (n - lo + stride - 1) / stride;
+  const int stride = Shape::kChunk * ctas;
   const int first = lo + rank * Shape::kChunk + warp * (32 * kEach) + lane;
   struct Ahead {            // of some positions: their tokens and the one before them, the pages of both
     int t[kEach], before, from[kEach], to[kEach];
@@ -231,7 +226,12 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   }
   listed(kCompactStages - 1, x0);
   listed(kCompactStages, x1);
+  for (; column < written; column += kCompactThreads, page = column < written ? __ldg(table + column) : -1)
+    bad |= page < 0 || page >= C.c.pages || __ldg(C.P.refs + page) > 1;
   paged(kCompactStages - 1, x0);
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) atomicOr(C.P.status, kPagedBadIndex);
+  const int steps = bad ? 0 : (n - lo + stride - 1) / stride;
   cluster_wait();
   // This warp's part of a chunk has arrived in shared memory: the CTAs are told.
   // Only reads have to be over, so nothing that was written is waited for.

@@ -632,8 +632,8 @@ typedef struct {
  * max(p - q, 0) (q = 1 at x and 0 elsewhere without `draft`), from p where that is
  * zero everywhere; after the last, from its row of p: the least token t whose
  * running sum w_0 + ... + w_t exceeds sample_u times the sum of all.  The tokens
- * are then distributed as the target's own.  NaN probabilities count as 0; a row
- * that leaves nothing to draw from gives -1.
+ * are then distributed as the target's own.  A NaN rejects its draft and leaves
+ * its token without weight; a row that leaves nothing to draw from gives -1.
  * tokens [N + B] int32, in target's order: the drafts that stayed, the next
  * token, -1 for the rest.  accepted [B] int32: how many stayed.  Where cu_drafts
  * descends or leaves [0, N], that sequence's accepted is 0, its tokens are left as

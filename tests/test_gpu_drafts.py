@@ -94,6 +94,42 @@ def test_rows_of_any_alignment(dtype, offset, extra):
     c.check(*whole)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [3, 70, 2047, 2049, 9001])
+def test_rows_of_different_alignment(dtype, vocab):
+    """The draft's rows at every place relative to the target's."""
+    c = Case([2, 1], vocab, dtype, seed=vocab)
+    whole = c.run()
+    c.check(*whole)
+    q = c.q
+    for offset in range(9):
+        wide = torch.full((3, vocab + 16), 7.0, dtype=dtype, device="cuda")[:, offset:offset + vocab]
+        wide.copy_(q)
+        c.q = wide
+        got = c.run()
+        assert torch.equal(got[0], whole[0]) and torch.equal(got[1], whole[1])
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+def test_large_vocabularies_of_many_sequences(drafted):
+    """Tiles of several lines: one row of the target (and of the draft) for all, no two random numbers alike."""
+    vocab, batch = 2200003, 160
+    g = torch.Generator(device="cuda").manual_seed(13)
+    p, q = _probs(g, 1, vocab, torch.float32, 1.0, False), _probs(g, 1, vocab, torch.float32, 1.0, False)
+    us = torch.rand(batch, generator=g, device="cuda")
+    w = p[0].double().cpu().numpy()
+    if drafted:
+        x = torch.full((batch, 1), int((p[0] / q[0]).argmin()), dtype=torch.int32, device="cuda")
+        u = torch.full((batch, 1), 0.999, device="cuda")
+        tokens, accepted = ovc.verify_drafts(p.expand(2 * batch, -1), x, u, us, draft_probs=q.expand(batch, -1))
+        w = np.maximum(w - q[0].double().cpu().numpy(), 0.0)
+        cu = np.arange(batch + 1)
+    else:
+        cu = np.zeros(batch + 1, int)
+        tokens, accepted = ovc.verify_drafts(p.expand(batch, -1), _i32([]), _f32([]), us, cu_drafts=_i32(cu))
+    check_verified(tokens.cpu().numpy(), accepted.cpu().numpy(), [], cu, us.double().cpu().numpy(), [(0, w)] * batch)
+
+
 def test_equal_numbers_of_drafts_need_no_starts():
     c = Case([5] * 7, 777, torch.float32, seed=3)
     a = c.run()
@@ -178,10 +214,16 @@ def test_rows_that_leave_nothing(vocab):
     for draft_probs in (q, None):
         tokens, accepted = ovc.verify_drafts(p, _i32([2]), _f32([0.0]), _f32([0.5, 0.5]), draft_probs=draft_probs, cu_drafts=_i32([0, 1, 1]))
         assert tokens.tolist() == [-1, -1, -1] and accepted.tolist() == [0, 0]
-    p[1, 3], p[2, 1:4] = 0.2, float("nan")          # NaN counts for nothing
+    p[1, 3], p[2, 1:4] = 0.2, float("nan")          # a NaN leaves its token without weight
     p[2, 4] = 1e-30
     tokens, _ = ovc.verify_drafts(p[1:], _i32([]), _f32([]), _f32([0.9, 0.9]), cu_drafts=_i32([0, 0, 0]))
-    assert tokens.tolist() == [3, 4] and ovc.device_status() == 0
+    assert tokens.tolist() == [3, 4]
+    p = torch.full((2, vocab), 0.25, device="cuda")
+    q[0], q[0, 1], q[0, 2] = float("nan"), 0.125, 0.5
+    for x, u in ((2, 0.9), (0, 0.0)):               # rejected by its probabilities, or by a NaN among them
+        tokens, accepted = ovc.verify_drafts(p, _i32([[x]]), _f32([[u]]), _f32([0.99]), draft_probs=q)
+        assert tokens.tolist() == [1, -1] and accepted.tolist() == [0]
+    assert ovc.device_status() == 0
 
 
 def test_very_small_and_large_probabilities():

@@ -21,7 +21,7 @@ constexpr int kDraftCtas = 2;                    // of an SM
 
 struct DraftParams {
   const int32_t* cu;        // or nullptr: each drafts
-  int32_t each, B, N, V;
+  int32_t each, N, V;
   const int32_t* drafts;
   const void* target;
   const void* draft;        // or nullptr
@@ -242,6 +242,16 @@ __device__ __forceinline__ FF from_lane(const FF& x, int lane) {
   return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
 }
 
+// One cluster a sequence.  Every CTA finds the first draft that does not stay, sums
+// the weights of its part of that row tile by tile, and learns the other parts'
+// sums; the one whose part holds the drawn place looks for it in one tile again.
+// Bound by memory where rows are many and long: 64 x 131072 FP32 with the draft's
+// rows, 67 MB, 18.5 us, of which the sums take 10 to 12 (the memory's rate); before
+// them a chain of lookups (starts, draft, its probabilities, 2.5 us), after them the
+// exchange and the last tile (3 us).  256 x 100003 BF16 without them, 51 MB, 21 us:
+// 104 of 152 SMs have two CTAs, the others one.  1 x 32000: 7 us, the chain alone.
+// Tried: one 16-bit probability a load where rows are not aligned 28 us for the
+// latter; the running sums in FP64 30 and 41 us.
 template <int kType, bool kDraft>
 __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_drafts_kernel(DraftParams P) {
   constexpr int kThreads = kDraftThreads<kDraft>, kWarps = kThreads / 32;

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
   const int b = blockIdx.x / ctas;
-  cluster_begun();
+  if (ctas > 1) cluster_begun();
 
   const int a0 = P.cu ? P.cu[b] : b * P.each, a1 = P.cu ? P.cu[b + 1] : a0 + P.each;
   // No CTA leaves before the last barrier, whatever it finds: others write to it.
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
       }
       __syncwarp();
     }
-    cluster_wait();
+    if (ctas > 1) cluster_wait();
     if (warp == 0) {
       if (lane < ctas)
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(&cta_sum[rank], lane)), "f"(mine.hi), "f"(mine.lo)
@@ -381,14 +381,22 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
         asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(&again, lane)), "r"(static_cast<int>(!pass && (qr || out >= 0))) : "memory");
       __syncwarp();
     }
-    cluster_arrive();
-    cluster_wait();
+    if (ctas > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
     upto = warp_scan<kDraftClusters>(lane < ctas ? cta_sum[lane] : FF{0.0f, 0.0f});
     total = from_lane(upto, kDraftClusters - 1);
     if (total.hi > 0.0f || !again) break;
     // Nothing is left of p - q: p itself.
-    __syncwarp();
-    cluster_arrive();
+    if (ctas > 1) {
+      __syncwarp();
+      cluster_arrive();
+    } else {
+      __syncthreads();
+    }
     qr = nullptr;
     out = -1;
   }

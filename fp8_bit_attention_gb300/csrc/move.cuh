@@ -128,6 +128,12 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   const int part = blockIdx.y & (kEach - 1), kv = blockIdx.y / kEach & 1, h = blockIdx.y / (2 * kEach), b = blockIdx.z;
   const int a0 = C.cu[b], a1 = C.cu[b + 1];
   const int len = row_len(C.P, b);
+  // A stage's barrier counts the warps of all CTAs that have read its chunk.
+  if (tid < kCompactStages) mbar_init(smem_addr(&bars[tid]), kCompactThreads / 32 * ctas);
+  if (tid == 0) abort = 0;
+  fence_mbar_init();
+  __syncthreads();
+  cluster_arrive();
   // No CTA leaves before the last barrier, whatever it finds: others may still tell
   // it something.
   bool bad = a0 < 0 || a1 < a0 || a1 > C.n || len < 0 || a1 - a0 > len;
@@ -223,24 +229,17 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // A stage's barrier counts the warps of all CTAs that have read its chunk.
-  if (tid < kCompactStages) mbar_init(smem_addr(&bars[tid]), kCompactThreads / 32 * ctas);
-  if (tid == 0) abort = 0;
-  fence_mbar_init();
-  __syncthreads();
-  cluster_arrive();
-  Ahead x0, x1;
-#pragma unroll 1
-  for (int s = 0; s < kCompactStages - 1; ++s) {
-    listed(s, x0);
-    paged(s, x0);
-    fetch(s, s, x0);
-  }
-  listed(kCompactStages - 1, x0);
-  listed(kCompactStages, x1);
+  // All of the first lookups are on their way at once: lists, then pages.
+  static_assert(kCompactStages == 2, "chunks looked up ahead");
+  Ahead x, x0, x1;
+  listed(0, x);
+  listed(1, x0);
+  listed(2, x1);
+  paged(0, x);
+  paged(1, x0);
   for (; column < written; column += kCompactThreads, page = column < written ? __ldg(table + column) : -1)
     bad |= page < 0 || page >= C.c.pages || __ldg(C.P.refs + page) > 1;
-  paged(kCompactStages - 1, x0);
+  fetch(0, 0, x);
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(C.P.status, kPagedBadIndex);
   const int steps = bad ? 0 : (n - lo + stride - 1) / stride;

@@ -74,19 +74,21 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(CopyParams P) {
 // written.
 //
 // Reads and writes 258 bytes a token and head: 49152 tokens of one sequence x 8
-// heads, 203 MB, in 40 us (5.1 TB/s, 76% of the measured copy rate); half of 8
-// ragged sequences up to 32768 x 8 heads, 161 MB, in 38 us, where the longest
-// sequence's chain of chunks is what remains at the end.  A few tokens at the
-// sequences' ends: 9 us, the chain of lookups before the first token.
+// heads, 203 MB, in 40 us (5.1 TB/s, 76% of the measured copy rate), of which the
+// chunks take 30 (the memory's rate) and the chain of lookups before the first
+// token 7; half of 8 ragged sequences up to 32768 x 8 heads, 161 MB, in 36 us.
+// A few tokens at the sequences' ends: 7 us, that chain.
 // Tried: a hardware barrier of the cluster for each chunk instead of the counting
 // ones 55 and 47 us; values held in registers, not in shared memory 99 and 70 us.
 // ---------------------------------------------------------------------------
 constexpr int kCompactThreads = 256;
 constexpr int kCompactCtas = 2;                         // of an SM
+constexpr int kCompactSorted = 64;                      // most sequences that are put in order
 constexpr int kCompactClusters = 8;                     // most CTAs of a cluster
-// Chunks in shared memory; three leave room for a CTA less an SM: 46 against 38 us
-// for the 8 sequences above, 41 against 40 for the one.
-constexpr int kCompactStages = 2;
+// Chunks in shared memory.  Two, three (a CTA less an SM) and four (two less): 8
+// sequences of 16384, half kept, 53, 52 and 58 us, 32 of 4096 86, 70 and 80 us, the
+// ragged ones above 35, 36 and 51 us.
+constexpr int kCompactStages = 3;
 constexpr uint64_t kCompactTimeoutNs = 4000000000ull;   // of a wait
 constexpr unsigned kStatusTimeoutBit = 1u;              // of the device status word
 
@@ -122,10 +124,25 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   constexpr int kEach = Shape::kEach, kLanes = Shape::kLanes;
   extern __shared__ __align__(128) uint8_t tokens[];
   __shared__ __align__(8) uint64_t bars[kCompactStages];
-  __shared__ int found, abort;
+  __shared__ int found, abort, kept[kCompactSorted];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = cluster_size(), rank = cluster_rank();
-  const int part = blockIdx.y & (kEach - 1), kv = blockIdx.y / kEach & 1, h = blockIdx.y / (2 * kEach), b = blockIdx.z;
+  const int part = blockIdx.y & (kEach - 1), kv = blockIdx.y / kEach & 1, h = blockIdx.y / (2 * kEach);
+  // The longest sequences go first, so that they are not what remains at the end:
+  // 32 ragged sequences up to 16384, half kept, 94 us without, 83 us.
+  int b = blockIdx.z;
+  if (C.P.rows > 1 && C.P.rows <= kCompactSorted) {
+    if (tid < C.P.rows) kept[tid] = C.cu[tid + 1] - C.cu[tid];
+    __syncthreads();
+    if (tid < C.P.rows) {
+      int before = 0;
+      for (int j = 0; j < C.P.rows; ++j) before += kept[j] > kept[tid] || (kept[j] == kept[tid] && j < tid);
+      if (before == b) found = tid;
+    }
+    __syncthreads();
+    b = found;
+    __syncthreads();
+  }
   const int a0 = C.cu[b], a1 = C.cu[b + 1];
   const int len = row_len(C.P, b);
   // A stage's barrier counts the warps of all CTAs that have read its chunk.
@@ -230,16 +247,16 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // All of the first lookups are on their way at once: lists, then pages.
-  static_assert(kCompactStages == 2, "chunks looked up ahead");
-  Ahead x, x0, x1;
-  listed(0, x);
-  listed(1, x0);
-  listed(2, x1);
-  paged(0, x);
-  paged(1, x0);
+  Ahead x[kCompactStages + 1];
+#pragma unroll
+  for (int s = 0; s <= kCompactStages; ++s) listed(s, x[s]);
+#pragma unroll
+  for (int s = 0; s < kCompactStages; ++s) paged(s, x[s]);
   for (; column < written; column += kCompactThreads, page = column < written ? __ldg(table + column) : -1)
     bad |= page < 0 || page >= C.c.pages || __ldg(C.P.refs + page) > 1;
-  fetch(0, 0, x);
+#pragma unroll
+  for (int s = 0; s < kCompactStages - 1; ++s) fetch(s, s, x[s]);
+  Ahead x0 = x[kCompactStages - 1], x1 = x[kCompactStages];
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(C.P.status, kPagedBadIndex);
   const int steps = bad ? 0 : (n - lo + stride - 1) / stride;

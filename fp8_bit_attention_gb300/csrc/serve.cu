@@ -168,10 +168,15 @@ ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const in
   const int64_t units = p->rows * c->heads * 2;
   // Half the channels a CTA where clusters of the largest size would leave SMs
   // without two CTAs.  Whole and half: 49152 moved of one sequence of 65536, 8 heads,
-  // 45 and 40 us; 8 sequences up to 32768, half kept, 41 and 48 us.
+  // 45 and 40 us; 8 sequences up to 32768, half kept, 36 and 48 us.
   const bool halves = units * kCompactClusters < kCompactCtas * dev->sms;
   const int parts = halves ? 2 : 1;
-  const int ctas = clusters_for(units * parts, kCompactCtas * dev->sms, kCompactClusters);
+  // One CTA a unit where they fill the SMs; else more than run at once, as sequences
+  // may differ in length.  2, 4 and 6 CTAs: 8 ragged sequences up to 32768 x 8 heads
+  // 51, 36 and 41 us, 8 of 16384 50, 52 and 57 us.  1 and 2 CTAs, a few tokens of 16
+  // sequences 7.0 and 11.8 us.
+  const int64_t fit = units >= dev->sms ? 1 : 18 * dev->sms / 5 / (units * parts);
+  const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kCompactClusters, fit)));
   return launch_clusters(halves ? kv_compact_kernel<64> : kv_compact_kernel<128>,
                          dim3(ctas, static_cast<unsigned>(units / p->rows * parts), static_cast<unsigned>(p->rows)), kCompactThreads,
                          halves ? CompactShape<64>::kSmem : CompactShape<128>::kSmem, ctas, static_cast<cudaStream_t>(stream), C);

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   Ahead x0 = x[kCompactStages - 1], x1 = x[kCompactStages];
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(C.P.status, kPagedBadIndex);
-  const int steps = bad ? 0 : (n - lo + stride - 1) / stride;
+  const int steps = bad || lo >= n ? 0 : (n - lo - 1) / stride + 1;
   cluster_wait();
   // This warp's part of a chunk has arrived in shared memory: the CTAs are told.
   // Only reads have to be over, so nothing that was written is waited for.

@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(1024) pages_release_kernel(PagesView P, const 
 }
 
 // ---------------------------------------------------------------------------
-// Fork: a CTA a child, which also looks for itself in both lists.  960 children of
+// Fork: a CTA a child, which also looks for itself in both lists (at most 8192
+// entries each).  960 children of
 // 450 pages each 5.9 us (128 and 512 threads: 6.2 and 7.4), 32 children 3 us.
 // ---------------------------------------------------------------------------
 constexpr int kForkThreads = 256;
@@ -128,8 +129,8 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView P, c
 // the chunks' numbers of free pages are exchanged once, and then each free page
 // knows its rank among all, and by it the row and column that it goes to.
 //
-// Bound by its chain of steps, each a latency or a barrier: 64 rows, 32768 pages
-// 6.6 us; 1024 rows that all copy, 131072 pages 11 us; 93000 pages given out of
+// Bound by its chain of steps, each a latency or a barrier: 40 rows, 8192 pages
+// 6.6 us, 64 rows, 32768 pages 7.7 us; 1024 rows that all copy, 131072 pages 11 us; 93000 pages given out of
 // 600000 16 us (2.4 MB of refs read at least once: 0.4 us).
 // Tried: pages dealt out in contiguous parts, 57 us for the last (the lowest pages,
 // which are the ones given out, all in one CTA); a search in shared memory for each
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView P, c
 // ---------------------------------------------------------------------------
 constexpr int kReserveThreads = 1024;
 constexpr int kReserveWarps = kReserveThreads / 32;
-constexpr int kReserveRows = 8192;             // most rows of a call: their sums are held in shared memory
+constexpr int kReserveRows = 8192;             // most rows of a state: their sums are held in shared memory
 constexpr int kReserveClusters = 16;           // most CTAs
 constexpr int kReserveWords = 4;               // words of 32 pages of a warp in a block
 constexpr int kReserveBlock = kReserveWarps * kReserveWords * 32;  // pages that a CTA deals out together

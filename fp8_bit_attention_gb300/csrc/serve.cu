@@ -20,7 +20,7 @@ namespace {
 constexpr int64_t kMost = 0x7FFFFC00;
 
 bool pages_ok(const ovc_kv_pages* p) {
-  if (!p || p->rows < 1 || p->rows > kMost || p->pages < 1 || p->pages > kMost || p->width < 1) return false;
+  if (!p || p->rows < 1 || p->rows > kReserveRows || p->pages < 1 || p->pages > kMost || p->width < 1) return false;
   if (p->page < 16 || p->page > 1024 || p->page % 16) return false;
   return p->pages * p->page <= kMost && static_cast<int64_t>(p->width) * p->page <= kMost && at4(p->page_table) &&
          at4(p->kv_lens) && at16(p->refs);
@@ -84,7 +84,7 @@ extern "C" {
 
 ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int32_t* src, int32_t* dst, int32_t* tokens,
                                 void* stream) {
-  if (!pages_ok(p) || p->rows > kReserveRows || !at4(lens) || !at4(src) || !at4(dst) || !at4(tokens)) return OVC_ERR_INVALID_ARG;
+  if (!pages_ok(p) || !at4(lens) || !at4(src) || !at4(dst) || !at4(tokens)) return OVC_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   ovc_status st = device_state(&dev);
   if (st != OVC_OK) return st;
@@ -150,7 +150,7 @@ ovc_status ovc_kv_copy(const ovc_kv_cache* to, const ovc_kv_cache* from, const i
 
 ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const int32_t* keep, int64_t keep_stride,
                           const int32_t* cu_keep, int64_t n, void* stream) {
-  if (!cache_ok(c) || !pages_ok(p) || c->page != p->page || c->pages != p->pages || c->heads > 32767 || p->rows > 65535)
+  if (!cache_ok(c) || !pages_ok(p) || c->page != p->page || c->pages != p->pages || c->heads > 32767)
     return OVC_ERR_INVALID_ARG;
   if (!at4(keep) || !at4(cu_keep) || n < 1 || n > kMost || (keep_stride != 0 && keep_stride < n)) return OVC_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;

@@ -37,7 +37,8 @@ class KVPages:
     ``refs`` [pages], and the tokens of a page.  Row b's first
     ceil(kv_lens[b] / page) entries are its pages; ``refs[p]`` counts the entries
     that name page p (a program may add to it to keep a page), 0 says that it is
-    free.  The tensors are those that :func:`paged_attention` takes."""
+    free.  At most 8192 sequences; ``refs`` is 16-byte aligned.  The first two are
+    what :func:`paged_attention` takes."""
     page_table: torch.Tensor
     kv_lens: torch.Tensor
     refs: torch.Tensor
@@ -54,6 +55,8 @@ class KVPages:
             raise ValueError("refs must be 16-byte aligned")
         if self.page % 16 or not 16 <= self.page <= 1024:
             raise ValueError(f"page size {self.page} is not a multiple of 16 up to 1024")
+        if t.shape[0] > 8192:
+            raise ValueError(f"{t.shape[0]} sequences: at most 8192 are supported")
         if max(self.refs.shape[0], t.shape[1]) * self.page > 2 ** 31 - 1024:
             raise ValueError(f"{self.refs.shape[0]} pages, {t.shape[1]} a sequence, of {self.page} tokens are not supported")
         desc = _abi.OvcKVPages(t.shape[0], self.refs.shape[0], t.shape[1], self.page, *ptrs)
@@ -84,8 +87,8 @@ def kv_pages_reserve(pages: KVPages, lens: torch.Tensor, *, stream=None):
 
     Returns the copies that replaced pages ask for: pages, their successors and
     tokens, int32 [sequences] each (-1, -1, 0 for the others), as
-    :func:`kv_cache_copy` takes them, for the cache of each layer, before the
-    next change of `pages`.  At most 8192 sequences."""
+    :func:`kv_cache_copy` takes them, for the cache of each layer, before new
+    tokens are written to it and before the next change of `pages`."""
     dev = _device(pages.refs, lens, stream=stream)
     n = pages._rows
     pl = _ints(lens, (n,), "lens")

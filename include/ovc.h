@@ -536,8 +536,8 @@ ovc_status ovc_paged_attention(const ovc_rows* q, const ovc_kv_cache* c, const o
  *   refs        [pages] how many entries of the table name the page, and what the
  *               program adds itself to keep one from being given out; 0 is free;
  *               16-byte aligned
- * An empty state is page_table -1, kv_lens 0, refs 0.  pages*page and width*page
- * are below 2^31 - 1024.  The calls change the state in place and run one after
+ * An empty state is page_table -1, kv_lens 0, refs 0.  At most 8192 rows;
+ * pages*page and width*page are below 2^31 - 1024.  The calls change the state in place and run one after
  * the other; arrays of lengths and lists may be any others on the device.  Rows
  * whose kv_len the table cannot hold, and entries that name no page, are reported
  * as OVC_ERR_BAD_INDEX by ovc_get_device_status() and left alone. */
@@ -559,8 +559,9 @@ typedef struct {
  * need no more pages than are free: kv_lens says which did.
  * src, dst and tokens [rows] receive, for each row whose last page was replaced,
  * that page, its successor, and the tokens to copy (ovc_kv_copy, in the cache of
- * each layer, before the next of these calls); -1, -1, 0 for the others.
- * At most 8192 rows. */
+ * each layer, before any row writes new tokens there and before the next of these
+ * calls: a row that keeps the page may write over what it does not hold itself);
+ * -1, -1, 0 for the others. */
 ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int32_t* src, int32_t* dst, int32_t* tokens,
                                 void* stream);
 
@@ -596,7 +597,7 @@ ovc_status ovc_kv_copy(const ovc_kv_cache* to, const ovc_kv_cache* from, const i
  * sequence with another is reported and left as it was.  Positions that do not
  * ascend or lie outside are reported and not moved, the sequence's other tokens
  * then unspecified.  c->pages and c->page are those of `p`; n: the size of a list;
- * rows <= 65535, heads <= 32767. */
+ * heads <= 32767. */
 ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const int32_t* keep, int64_t keep_stride,
                           const int32_t* cu_keep, int64_t n, void* stream);
 

@@ -456,9 +456,9 @@ def test_refusals():
         ovc.kv_cache_compact(ovc.kv_cache(5, 2, 16), p, two, three)
     with pytest.raises(ValueError, match="CUDA device"):
         ovc.kv_pages_release(p, two.cpu())
-    for bad in (dict(page_size=20), dict(page_size=2048), dict(num_pages=0), dict(num_sequences=0)):
+    for bad in (dict(page_size=20), dict(page_size=2048), dict(num_pages=0), dict(num_sequences=0), dict(num_sequences=8193)):
         with pytest.raises(ValueError):
             ovc.kv_pages(**{**dict(num_pages=4, num_sequences=2, pages_per_sequence=2, page_size=16), **bad})
-    many = ovc.kv_pages(4, 8193, 1, 16)
-    with pytest.raises(ovc.OvcError):
-        ovc.kv_pages_reserve(many, many.kv_lens)
+    refs = torch.zeros(9, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="aligned"):
+        ovc.KVPages(p.page_table, p.kv_lens, refs[1:], 16)

@@ -82,7 +82,7 @@ def test_checked_tokens_lie_at_their_place():
 
 
 # ------------------------------------------------------------------- refusals
-BAD_PAGES = [dict(rows=0), dict(pages=0), dict(width=0), dict(page=8), dict(page=24), dict(page=2048), dict(page_table=0),
+BAD_PAGES = [dict(rows=0), dict(rows=8193), dict(pages=0), dict(width=0), dict(page=8), dict(page=24), dict(page=2048), dict(page_table=0),
              dict(kv_lens=0x20002), dict(refs=None), dict(refs=0x30004), dict(pages=1 << 27), dict(width=1 << 27), dict(rows=1 << 31)]
 
 
@@ -110,7 +110,6 @@ def test_bad_lists_are_refused(lib):  # noqa: F811
         assert lib.ovc_kv_compact(R(c), R(p), B(x), 0, B(0x2000), 5, None) == BAD
         assert lib.ovc_kv_compact(R(c), R(p), B(0x1000), 0, B(x), 5, None) == BAD
     assert lib.ovc_kv_copy(R(c), None, B(0x1000), B(0x2000), B(0x3002), 1, None) == BAD
-    assert lib.ovc_kv_pages_reserve(R(_pages(rows=8193)), B(0x1000), B(0x2000), B(0x3000), B(0x4000), None) == BAD
     for n in (0, -1, 4):
         assert lib.ovc_kv_pages_fork(R(p), B(0x1000), B(0x2000), n, None) == BAD
     for n in (0, -1, 1 << 31):
@@ -122,7 +121,6 @@ def test_bad_lists_are_refused(lib):  # noqa: F811
         assert lib.ovc_kv_copy(R(c), R(_cache(**other)), B(0x1000), B(0x2000), None, 1, None) == BAD
     for other in (dict(pages=5), dict(page=32), dict(heads=32768)):
         assert lib.ovc_kv_compact(R(_cache(**other)), R(p), B(0x1000), 0, B(0x2000), 5, None) == BAD
-    assert lib.ovc_kv_compact(R(c), R(_pages(rows=65536)), B(0x1000), 0, B(0x2000), 5, None) == BAD
     assert lib.ovc_kv_pages_release(None, B(0x1000), None) == BAD
     assert lib.ovc_kv_compact(None, R(p), B(0x1000), 0, B(0x2000), 5, None) == BAD
 

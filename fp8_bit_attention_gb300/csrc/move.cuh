@@ -159,35 +159,13 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   const int32_t* keep = C.keep + h * C.keep_stride + a0;
   const int32_t* table = C.P.table + static_cast<int64_t>(b) * C.P.width;
 
-  // The first position that does not stay: keep[i] - i never falls.
-  int lo = 0, hi = n;                             // it lies in [lo, hi]
-  while (lo < hi) {
-    const int step = (hi - lo + kCompactThreads - 1) / kCompactThreads;
-    if (tid == 0) found = hi;
-    __syncthreads();
-    const int i = lo + (tid + 1) * step - 1;      // the last of this thread's part
-    if (i < hi && __ldg(keep + i) != i) atomicMin(&found, i);
-    __syncthreads();
-    const int f = found;
-    __syncthreads();
-    lo += f == hi ? (hi - lo) / step * step : f - step + 1 - lo;
-    hi = f;
-    if (step == 1) {
-      lo = f;
-      break;
-    }
-  }
-  // Pages that will be written must be this row's own: looked up here, and told
-  // when the first tokens are on their way.
-  const int written = lo < n ? (n - 1) / C.P.by_page + 1 : 0;     // the first column behind them
-  int column = lo / C.P.by_page + tid, page = column < written ? __ldg(table + column) : -1;
   uint8_t* codes = (kv ? C.c.v : C.c.k) + part * kRow;
   uint8_t* scales = kv ? C.c.vs : C.c.ks;
 
   // The CTAs take the same number of steps; a lane's positions in step s are first +
   // s * stride, and 32 more.
   const int stride = Shape::kChunk * ctas;
-  const int first = lo + rank * Shape::kChunk + warp * (32 * kEach) + lane;
+  int first = rank * Shape::kChunk + warp * (32 * kEach) + lane;
   struct Ahead {            // of some positions: their tokens and the one before them, the pages of both
     int t[kEach], before, from[kEach], to[kEach];
   };
@@ -207,9 +185,10 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
       const int up = __shfl_up_sync(0xFFFFFFFFu, x.t[k], 1), last = __shfl_sync(0xFFFFFFFFu, x.t[k], 31);
       const bool there = i + 32 * k < n, ok = there && x.t[k] >= i + 32 * k && x.t[k] > (lane ? up : before) && x.t[k] < len;
       if (!ok && there) atomicOr(C.P.status, kPagedBadIndex);
-      if (!ok) x.t[k] = -1;
-      x.from[k] = ok ? __ldg(table + x.t[k] / C.P.by_page) : -1;
-      x.to[k] = ok ? __ldg(table + static_cast<int>(i + 32 * k) / C.P.by_page) : -1;
+      const bool moves = ok && x.t[k] != i + 32 * k;
+      if (!moves) x.t[k] = -1;
+      x.from[k] = moves ? __ldg(table + x.t[k] / C.P.by_page) : -1;
+      x.to[k] = moves ? __ldg(table + static_cast<int>(i + 32 * k) / C.P.by_page) : -1;
       before = last;
     }
   };
@@ -246,20 +225,59 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // All of the first lookups are on their way at once: lists, then pages.
+  // Where the work begins: at the first position that does not stay, which a search
+  // by 256 narrows down (keep[i] - i never falls), or a little before it.  The first
+  // lookups of the search, and of the work as if it began at 0, are on their way
+  // together: list; the rest of the search, and pages; refs, and tokens.
   Ahead x[kCompactStages + 1];
 #pragma unroll
   for (int s = 0; s <= kCompactStages; ++s) listed(s, x[s]);
+  int lo = 0, hi = n, step = 0, probe = 0, seen = 0;     // it lies in [lo, hi], and is lo in the end
+  auto look = [&] {
+    step = (hi - lo + kCompactThreads - 1) / kCompactThreads;
+    probe = lo + (tid + 1) * step - 1;            // the last of this thread's part
+    seen = probe < hi ? __ldg(keep + probe) : probe;
+  };
+  auto narrow = [&] {
+    if (tid == 0) found = hi;
+    __syncthreads();
+    if (seen != probe) atomicMin(&found, probe);
+    __syncthreads();
+    const int f = found;
+    __syncthreads();
+    lo = step == 1 ? f : f == hi ? lo + (hi - lo) / step * step : f - step + 1;
+    hi = f;
+  };
+  if (lo < hi) {
+    look();
+    narrow();
+  }
+  const int start = lo;
+  if (start > 0) {
+    first += start;
+#pragma unroll
+    for (int s = 0; s <= kCompactStages; ++s) listed(s, x[s]);
+  }
+  if (lo < hi) look();
+  const int columns = n > 0 ? (n - 1) / C.P.by_page + 1 : 0;
+  int column = start / C.P.by_page + tid, page = column < columns ? __ldg(table + column) : -1;
 #pragma unroll
   for (int s = 0; s < kCompactStages; ++s) paged(s, x[s]);
-  for (; column < written; column += kCompactThreads, page = column < written ? __ldg(table + column) : -1)
-    bad |= page < 0 || page >= C.c.pages || __ldg(C.P.refs + page) > 1;
+  while (lo < hi) {
+    narrow();
+    if (lo < hi) look();
+  }
+  // Pages that will be written must be this row's own.
+  for (; column < columns; column += kCompactThreads, page = column < columns ? __ldg(table + column) : -1) {
+    const bool shared = page < 0 || page >= C.c.pages || __ldg(C.P.refs + page) > 1;
+    bad |= shared && lo < n && column >= lo / C.P.by_page;
+  }
 #pragma unroll
   for (int s = 0; s < kCompactStages - 1; ++s) fetch(s, s, x[s]);
   Ahead x0 = x[kCompactStages - 1], x1 = x[kCompactStages];
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(C.P.status, kPagedBadIndex);
-  const int steps = bad || lo >= n ? 0 : (n - lo - 1) / stride + 1;
+  const int steps = bad || lo >= n ? 0 : (n - start - 1) / stride + 1;
   cluster_wait();
   // This warp's part of a chunk has arrived in shared memory: the CTAs are told.
   // Only reads have to be over, so nothing that was written is waited for.

@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
   const int b = blockIdx.x / ctas;
   if (ctas > 1) cluster_begun();
 
+  const float u = __ldg(P.sample_u + b);              // here, so that nothing waits for it later
   const int a0 = P.cu ? P.cu[b] : b * P.each, a1 = P.cu ? P.cu[b + 1] : a0 + P.each;
   // No CTA leaves before the last barrier, whatever it finds: others write to it.
   const bool bad = a0 < 0 || a1 < a0 || a1 > P.N;
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
     const int i = i0 + tid;
     if (i < n) {
       const int x = P.drafts[a0 + i];
-      const float u = P.accept_u[a0 + i];
+      const float luck = P.accept_u[a0 + i];
       if (x < 0 || x >= P.V) {
         atomicMin(&stop, 2u * i + 1u);
         if (x >= P.V) atomicOr(P.status, kPagedBadIndex);
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
         const float p = prob<kType>(P.target, (row0 + i) * P.target_stride + x);
         const float q = kDraft ? prob<kType>(P.draft, static_cast<int64_t>(a0 + i) * P.draft_stride + x) : 1.0f;
         // 24 by 24 bits: exact in 64
-        if (!(static_cast<double>(u) * q < p)) atomicMin(&stop, 2u * i);
+        if (!(static_cast<double>(luck) * q < p)) atomicMin(&stop, 2u * i);
       }
     }
     __syncthreads();
@@ -408,7 +409,6 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
   // The part of the vocabulary, tile and thread within which the running sum first
   // exceeds u * total, or, where rounding (or u >= 1) leaves none, the last that
   // holds any weight.
-  const float u = P.sample_u[b];
   FF goal = {u * total.hi, 0.0f};
   goal.lo = fmaf(u, total.hi, -goal.hi) + u * total.lo;
   const bool some = lane < ctas && cta_sum[lane].hi > 0.0f;

@@ -61,6 +61,12 @@ __device__ __forceinline__ FF operator+(const FF& a, const FF& b) {
   const float hi = s.hi + s.lo;                  // |lo| <= half a step of hi again
   return {hi, s.lo - (hi - s.hi)};
 }
+// The same with a lower part that may have grown to a few steps of the upper one.
+__device__ __forceinline__ FF near_sum(const FF& a, const FF& b) {
+  FF s = two_sum(a.hi, b.hi);
+  s.lo += a.lo + b.lo;
+  return s;
+}
 __device__ __forceinline__ bool above(const FF& a, const FF& b) { return (a.hi - b.hi) + (a.lo - b.lo) > 0.0f; }
 
 // max(p - q, 0), NaN: 0.  Where p >= q >= 0 the lower part makes it exact (Dekker,
@@ -110,9 +116,12 @@ struct Sums {
     lo = add_pairs(lo, add_pairs(add_pairs(sub_pairs(hi, sub_pairs(s, t)), sub_pairs(d, t)), e));
     hi = s;
   }
-  __device__ __forceinline__ FF sum() const {
-    const float2 h = unpair(hi), l = unpair(lo);
-    return FF{h.x, l.x} + FF{h.y, l.y};
+  // Both sums and those of c.
+  __device__ __forceinline__ FF sum(const Sums& c) const {
+    const uint64_t s = add_pairs(hi, c.hi), t = sub_pairs(s, hi);
+    const float2 h = unpair(s);
+    const float2 l = unpair(add_pairs(add_pairs(lo, c.lo), add_pairs(sub_pairs(hi, sub_pairs(s, t)), sub_pairs(c.hi, t))));
+    return near_sum({h.x, l.x}, {h.y, l.y});
   }
 };
 
@@ -328,13 +337,9 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
       for (int k = 0; k < 1 << P.tile_shift && v0 < P.V; ++k, v0 += L::kTile) {
         L p;
         p.load(pr, v0, P.V);
-        float edge_p = 0.0f, edge_q = 0.0f;
         if (v0 < 0 || v0 + L::kTile > P.V) {
           const int64_t v = L::edge(v0, P.V);
-          if (v >= 0 && v != out) {
-            edge_p = prob<kType>(pr, v);
-            if (kDraft && qr) edge_q = prob<kType>(qr, v);
-          }
+          if (v >= 0 && v != out) a.add(pair(prob<kType>(pr, v), 0.0f), pair(kDraft && qr ? prob<kType>(qr, v) : 0.0f, 0.0f));
         }
         if (kDraft && qr) {
           L q;
@@ -346,19 +351,18 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
             c.add(p.two(i + 1), q.two(i + 1));
           }
         } else {
-          if (!kDraft && out >= 0) p.clear(v0, out);
+          if (!kDraft && out >= v0 && out < v0 + L::kTile) p.clear(v0, out);
 #pragma unroll
           for (int i = 0; i < L::kEach * kDraftLoads / 2; i += 2) {
             a.add(p.two_weights(i));
             c.add(p.two_weights(i + 1));
           }
         }
-        a.add(pair(edge_p, 0.0f), pair(edge_q, 0.0f));
       }
-      FF w = a.sum() + c.sum();
+      FF w = a.sum(c);
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1)
-        w = w + FF{__shfl_xor_sync(0xFFFFFFFFu, w.hi, d), __shfl_xor_sync(0xFFFFFFFFu, w.lo, d)};
+        w = near_sum(w, FF{__shfl_xor_sync(0xFFFFFFFFu, w.hi, d), __shfl_xor_sync(0xFFFFFFFFu, w.lo, d)});
       if (lane == 0) tile_own[t] = w;
     }
     __syncthreads();

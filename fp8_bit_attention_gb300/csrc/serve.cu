@@ -92,9 +92,10 @@ ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int3
   if (st != OVC_OK) return st;
   int shift = 0;
   while (p->pages > (int64_t{kReserveBlock} << shift) * kReserveChunks) ++shift;
-  // 4, 8 and 16 CTAs: 600000 pages 41, 25 and 16 us; 131072 pages 12.3 and 11.0 us
-  // (one CTA 18.2).  8192 pages: one CTA 6.6, two 7.3 us.
-  const int ctas = clusters_for(1, (p->pages - 1) / (kReserveBlock * kReserveAhead) + 1, kReserveClusters);
+  // 4, 8 and 16 CTAs: 600000 pages 41, 25 and 16 us; 131072 pages 12.3, 11.1 and 10.8
+  // us (one CTA 18.2); 1, 2 and 4, 32768 pages: 8.1, 7.7 and 7.4 us; 8192 pages: one
+  // CTA 6.4, two 7.3 us.
+  const int ctas = clusters_for(1, (p->pages - 1) / (2 * kReserveBlock) + 1, kReserveClusters);
   return launch_clusters(pages_reserve_kernel, dim3(ctas), kReserveThreads, reserve_smem(static_cast<int>(p->rows)), ctas,
                          static_cast<cudaStream_t>(stream), view(p, dev), lens, ReserveOut{src, dst, tokens}, shift, reserve_hash(static_cast<int>(p->rows)));
 }

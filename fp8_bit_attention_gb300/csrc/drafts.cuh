@@ -255,10 +255,10 @@ __device__ __forceinline__ FF from_lane(const FF& x, int lane) {
 // the weights of its part of that row tile by tile, and learns the other parts'
 // sums; the one whose part holds the drawn place looks for it in one tile again.
 // Bound by memory where rows are many and long: 64 x 131072 FP32 with the draft's
-// rows, 67 MB, 18.5 us, of which the sums take 10 to 12 (the memory's rate); before
+// rows, 67 MB, 17.2 us, of which the sums take 10 to 11 (the memory's rate); before
 // them a chain of lookups (starts, draft, its probabilities, 2.5 us), after them the
-// exchange and the last tile (3 us).  256 x 100003 BF16 without them, 51 MB, 21 us:
-// 104 of 152 SMs have two CTAs, the others one.  1 x 32000: 7 us, the chain alone.
+// exchange and the last tile (3 us).  256 x 100003 BF16 without them, 51 MB, 20 us:
+// 104 of 152 SMs have two CTAs, the others one.  1 x 32000: 6.5 us, the chain alone.
 // Tried: one 16-bit probability a load where rows are not aligned 28 us for the
 // latter; the running sums in FP64 30 and 41 us.
 template <int kType, bool kDraft>

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(CopyParams P) {
 // Reads and writes 258 bytes a token and head: 49152 tokens of one sequence x 8
 // heads, 203 MB, in 40 us (5.1 TB/s, 76% of the measured copy rate), of which the
 // chunks take 30 (the memory's rate) and the chain of lookups before the first
-// token 7; half of 8 ragged sequences up to 32768 x 8 heads, 161 MB, in 36 us.
+// token 6; half of 8 ragged sequences up to 32768 x 8 heads, 161 MB, in 36 us.
 // A few tokens at the sequences' ends: 7 us, that chain.
 // Tried: a hardware barrier of the cluster for each chunk instead of the counting
 // ones 55 and 47 us; values held in registers, not in shared memory 99 and 70 us.

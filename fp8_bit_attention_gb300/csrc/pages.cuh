@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(PagesView P, c
 // knows its rank among all, and by it the row and column that it goes to.
 //
 // Bound by its chain of steps, each a latency or a barrier: 40 rows, 8192 pages
-// 6.4 us, 64 rows, 32768 pages 7.4 us; 1024 rows that all copy, 131072 pages 11 us; 93000 pages given out of
+// 6.4 us, 64 rows, 32768 pages 7.3 us; 1024 rows that all copy, 131072 pages 11 us; 93000 pages given out of
 // 600000 16 us (2.4 MB of refs read at least once: 0.4 us).
 // Tried: pages dealt out in contiguous parts, 57 us for the last (the lowest pages,
 // which are the ones given out, all in one CTA); a search in shared memory for each

@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   // s * stride, and 32 more.
   const int stride = Shape::kChunk * ctas;
   int first = rank * Shape::kChunk + warp * (32 * kEach) + lane;
+  int lo = 0;               // the first position that does not stay, once it is found
   struct Ahead {            // of some positions: their tokens and the one before them, the pages of both
     int t[kEach], before, from[kEach], to[kEach];
   };
@@ -206,7 +207,8 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
       int to = -1;
       from[k] = -1;
       if (x.t[k] >= 0) {
-        if (x.from[k] >= 0 && x.from[k] < C.c.pages && x.to[k] >= 0 && x.to[k] < C.c.pages) {
+        // (before lo: of a list that does not ascend; its page has not been looked at)
+        if (first + s * stride + 32 * k >= lo && x.from[k] >= 0 && x.from[k] < C.c.pages && x.to[k] >= 0 && x.to[k] < C.c.pages) {
           from[k] = row_of(x.t[k], x.from[k]);
           to = row_of(first + s * stride + 32 * k, x.to[k]);
         } else {
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   Ahead x[kCompactStages + 1];
 #pragma unroll
   for (int s = 0; s <= kCompactStages; ++s) listed(s, x[s]);
-  int lo = 0, hi = n, step = 0, probe = 0, seen = 0;     // it lies in [lo, hi], and is lo in the end
+  int hi = n, step = 0, probe = 0, seen = 0;             // it lies in [lo, hi], and is lo in the end
   auto look = [&] {
     step = (hi - lo + kCompactThreads - 1) / kCompactThreads;
     probe = lo + (tid + 1) * step - 1;            // the last of this thread's part

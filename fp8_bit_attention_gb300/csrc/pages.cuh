@@ -58,8 +58,9 @@ __device__ __forceinline__ int row_len(const PagesView& P, int b) {
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) pages_release_kernel(PagesView P, const int32_t* __restrict__ lens) {
   const int b = blockIdx.x;
-  const int to = lens[b], len = row_len(P, b);
-  if (to < 0 || to >= len) return;                   // uniform over the CTA
+  const int to = lens[b];
+  const int len = to < 0 ? -1 : row_len(P, b);
+  if (to >= len || to < 0) return;                   // uniform over the CTA
   const int end = pages_of(P, len);
   int32_t* row = P.table + static_cast<int64_t>(b) * P.width;
   for (int c0 = pages_of(P, to) + threadIdx.x; c0 < end; c0 += 4 * blockDim.x) {
@@ -83,8 +84,8 @@ __global__ void __launch_bounds__(1024) pages_release_kernel(PagesView P, const 
 
 // ---------------------------------------------------------------------------
 // Fork: a CTA a child, which also looks for itself in both lists (at most 8192
-// entries each).  960 children of
-// 450 pages each 5.9 us (128 and 512 threads: 6.2 and 7.4), 32 children 3 us.
+// entries each).  960 children of 450 pages each 5.9 us (128 and 512 threads: 6.2
+// and 7.4), 32 children 3 us.
 // ---------------------------------------------------------------------------
 constexpr int kForkThreads = 256;
 

@@ -145,6 +145,8 @@ def test_bad_rows_are_reported_and_left_alone():
     ovc.kv_pages_release(p, _i32([0, 0, 0, 0]))
     assert ovc.device_status() == BAD_INDEX
     assert p.kv_lens.tolist() == [0, 0, 60, 0] and p.refs.tolist() == [0, 0, 0, 1, 0, 0, 0, 0]
+    ovc.kv_pages_release(p, _i32([-1, -1, -1, -1]))      # rows that stay are not looked at
+    assert ovc.device_status() == 0
     p.kv_lens[0] = 5                         # a page that nobody holds
     p.page_table[0, 0] = 6
     ovc.kv_pages_release(p, _i32([0, 0, -1, 0]))
@@ -341,6 +343,27 @@ def test_bad_positions_are_reported(keep, cu):
     ovc.kv_cache_compact(c, p, _i32(keep), _i32(cu))
     assert ovc.device_status() == BAD_INDEX
     assert all(torch.equal(x[2:], y[2:]) for x, y in zip(_arrays(c), old))
+
+
+def test_a_bad_position_before_those_that_move():
+    """A long list that goes wrong among the positions that stay, at one that the
+    search for the first that moves does not look at: its page, which others hold
+    too, is not written."""
+    page, n, at, kept = 16, 66100, 258 * 100, 66000
+    table, refs = _held([n], page, 3)
+    keep = np.arange(kept)
+    keep[at + 101:] += 1
+    for wrong in range(at, at + 6):
+        bad = keep.copy()
+        bad[wrong] = wrong + 40
+        shared = table[0, wrong // page]
+        r = refs.copy()
+        r[shared] = 2
+        c, p = _filled(len(refs), 1, page, 4), _state(table, [n], r, page)
+        old = [x[shared].clone() for x in (c.k, c.v, c.k_scale, c.v_scale)]
+        ovc.kv_cache_compact(c, p, _i32(bad), _i32([0, kept]))
+        assert all(torch.equal(x[shared], y) for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), old))
+    ovc.device_status()
 
 
 # --------------------------------------------------------- streams and graphs

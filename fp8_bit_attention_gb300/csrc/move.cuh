@@ -86,8 +86,8 @@ constexpr int kCompactCtas = 2;                         // of an SM
 constexpr int kCompactSorted = 64;                      // most sequences that are put in order
 constexpr int kCompactClusters = 8;                     // most CTAs of a cluster
 // Chunks in shared memory.  Two, three (a CTA less an SM) and four (two less): 8
-// sequences of 16384, half kept, 53, 52 and 58 us, 32 of 4096 86, 70 and 80 us, the
-// ragged ones above 35, 36 and 51 us.
+// sequences of 16384, half kept, 61, 52 and 63 us, 32 of 4096 86, 71 and 84 us, the
+// ragged ones above 38, 36 and 45 us.
 constexpr int kCompactStages = 3;
 constexpr uint64_t kCompactTimeoutNs = 4000000000ull;   // of a wait
 constexpr unsigned kStatusTimeoutBit = 1u;              // of the device status word
@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   const int ctas = cluster_size(), rank = cluster_rank();
   const int part = blockIdx.y & (kEach - 1), kv = blockIdx.y / kEach & 1, h = blockIdx.y / (2 * kEach);
   // The longest sequences go first, so that they are not what remains at the end:
-  // 32 ragged sequences up to 16384, half kept, 94 us without, 83 us.
+  // 32 ragged sequences up to 16384, half kept, 94 us without, 83 us with it; a few
+  // tokens of 16 sequences 6.5 and 7.1 us.
   int b = blockIdx.z;
   if (C.P.rows > 1 && C.P.rows <= kCompactSorted) {
     if (tid < C.P.rows) kept[tid] = C.cu[tid + 1] - C.cu[tid];

@@ -169,13 +169,13 @@ ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const in
   const int64_t units = p->rows * c->heads * 2;
   // Half the channels a CTA where clusters of the largest size would leave SMs
   // without two CTAs.  Whole and half: 49152 moved of one sequence of 65536, 8 heads,
-  // 45 and 40 us; 8 sequences up to 32768, half kept, 36 and 48 us.
+  // 46 and 41 us; 8 sequences up to 32768, half kept, 36 and 38 us.
   const bool halves = units * kCompactClusters < kCompactCtas * dev->sms;
   const int parts = halves ? 2 : 1;
   // One CTA a unit where they fill the SMs; else more than run at once, as sequences
   // may differ in length.  2, 4 and 6 CTAs: 8 ragged sequences up to 32768 x 8 heads
-  // 51, 36 and 41 us, 8 of 16384 50, 52 and 57 us.  1 and 2 CTAs, a few tokens of 16
-  // sequences 7.0 and 11.8 us.
+  // 47, 36 and 40 us, 8 of 16384 49, 52 and 57 us.  1 and 2 CTAs, a few tokens of 16
+  // sequences 7.1 and 11.7 us.
   const int64_t fit = units >= dev->sms ? 1 : 18 * dev->sms / 5 / (units * parts);
   const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kCompactClusters, fit)));
   return launch_clusters(halves ? kv_compact_kernel<64> : kv_compact_kernel<128>,
@@ -211,8 +211,8 @@ ovc_status ovc_verify_drafts(const ovc_drafts* d, int32_t* tokens, int32_t* acce
   P.status = dev->status;
   const int most = clusters_for(1, (d->V + 4095) / 4096, kDraftClusters);
   // As many CTAs as run at once (about 8/9 of the places, as clusters leave some
-  // empty).  One, two and four times as many: 64 x 131072 FP32 18.5, 23.1 and 23.3
-  // us, 256 x 100003 BF16 without draft 21.2, 25.7 and 32.4 us.
+  // empty).  One, two and four times as many: 64 x 131072 FP32 17.2, 20.8 and 21.2
+  // us, 256 x 100003 BF16 without draft 20.0, 25.3 and 31.6 us.
   const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, int64_t{kDraftCtas} * dev->sms * 8 / 9 / d->B)));
   const int64_t tile = d->dtype == OVC_FP32 ? kDraftTile<2> : kDraftTile<0>;
   while (d->V + 7 > (tile << P.tile_shift) * kDraftTiles * ctas) ++P.tile_shift;       // rows begin up to 7 tokens behind a tile

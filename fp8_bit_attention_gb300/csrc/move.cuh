@@ -71,7 +71,10 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(CopyParams P) {
 //
 // A warp moves 32 (64) positions of a chunk through its own part of shared memory:
 // list, page table, and tokens of the chunks ahead are on their way while one is
-// written.
+// written.  That a chunk has been read is told with release at the cluster's scope,
+// which also waits for what was written before; so the warps tell it to one warp of
+// their CTA, by a barrier of the CTA, and that one tells the other CTAs and waits.
+// Told by each warp itself, for the two cases below: 47 and 44 us.
 //
 // Reads and writes 258 bytes a token and head: 49152 tokens of one sequence x 8
 // heads, 203 MB, in 40 us (5.1 TB/s, 76% of the measured copy rate), of which the
@@ -81,7 +84,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(CopyParams P) {
 // Tried: a hardware barrier of the cluster for each chunk instead of the counting
 // ones 55 and 47 us; values held in registers, not in shared memory 99 and 70 us.
 // ---------------------------------------------------------------------------
-constexpr int kCompactThreads = 256;
+constexpr int kCompactThreads = 256;                    // that move tokens
+constexpr int kCompactTeller = kCompactThreads / 32;    // the warp behind them, which tells the other CTAs
 constexpr int kCompactCtas = 2;                         // of an SM
 constexpr int kCompactSorted = 64;                      // most sequences that are put in order
 constexpr int kCompactClusters = 8;                     // most CTAs of a cluster
@@ -118,12 +122,33 @@ __device__ __forceinline__ void copy_async4(uint32_t to, const void* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
 
+// As paged_wait, of a barrier that other CTAs of the cluster arrive at.
+__device__ __forceinline__ bool told_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool told_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  if (__builtin_expect(told_try(bar, parity), 1)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!told_try(bar, parity))
+    if (*abort || globaltimer_ns() - t0 > kCompactTimeoutNs) return false;
+  return true;
+}
+
 template <int kRow>
-__global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kernel(CompactParams C) {
+__global__ void __launch_bounds__(kCompactThreads + 32, kCompactCtas) kv_compact_kernel(CompactParams C) {
   using Shape = CompactShape<kRow>;
   constexpr int kEach = Shape::kEach, kLanes = Shape::kLanes;
   extern __shared__ __align__(128) uint8_t tokens[];
-  __shared__ __align__(8) uint64_t bars[kCompactStages];
+  __shared__ __align__(8) uint64_t bars[kCompactStages], landed[kCompactStages];
   __shared__ int found, abort, kept[kCompactSorted];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = cluster_size(), rank = cluster_rank();
@@ -146,8 +171,12 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   }
   const int a0 = C.cu[b], a1 = C.cu[b + 1];
   const int len = row_len(C.P, b);
-  // A stage's barrier counts the warps of all CTAs that have read its chunk.
-  if (tid < kCompactStages) mbar_init(smem_addr(&bars[tid]), kCompactThreads / 32 * ctas);
+  // A stage's barriers: the warps of this CTA that have read its chunk, and the
+  // CTAs that have.
+  if (tid < kCompactStages) {
+    mbar_init(smem_addr(&landed[tid]), kCompactThreads / 32);
+    mbar_init(smem_addr(&bars[tid]), ctas);
+  }
   if (tid == 0) abort = 0;
   fence_mbar_init();
   __syncthreads();
@@ -165,7 +194,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
 
   // The CTAs take the same number of steps; a lane's positions in step s are first +
   // s * stride, and 32 more.
-  const int stride = Shape::kChunk * ctas;
+  const int stride = Shape::kChunk * ctas, mine = warp < kCompactTeller ? n : 0;
   int first = rank * Shape::kChunk + warp * (32 * kEach) + lane;
   int lo = 0;               // the first position that does not stay, once it is found
   struct Ahead {            // of some positions: their tokens and the one before them, the pages of both
@@ -176,8 +205,8 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   auto listed = [&](int s, Ahead& x) {            // the tokens
     const int64_t i = first + static_cast<int64_t>(s) * stride;
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) x.t[k] = i + 32 * k < n ? __ldg(keep + i + 32 * k) : -1;
-    x.before = lane == 0 && i > 0 && i < n ? __ldg(keep + i - 1) : -1;
+    for (int k = 0; k < kEach; ++k) x.t[k] = i + 32 * k < mine ? __ldg(keep + i + 32 * k) : -1;
+    x.before = lane == 0 && i > 0 && i < mine ? __ldg(keep + i - 1) : -1;
   };
   auto paged = [&](int s, Ahead& x) {             // their pages
     const int64_t i = first + static_cast<int64_t>(s) * stride;
@@ -185,7 +214,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
       const int up = __shfl_up_sync(0xFFFFFFFFu, x.t[k], 1), last = __shfl_sync(0xFFFFFFFFu, x.t[k], 31);
-      const bool there = i + 32 * k < n, ok = there && x.t[k] >= i + 32 * k && x.t[k] > (lane ? up : before) && x.t[k] < len;
+      const bool there = i + 32 * k < mine, ok = there && x.t[k] >= i + 32 * k && x.t[k] > (lane ? up : before) && x.t[k] < len;
       if (!ok && there) atomicOr(C.P.status, kPagedBadIndex);
       const bool moves = ok && x.t[k] != i + 32 * k;
       if (!moves) x.t[k] = -1;
@@ -216,6 +245,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
           atomicOr(C.P.status, kPagedBadIndex);
         }
       }
+      // (the word's other bytes may be written meanwhile: memory keeps bytes apart)
       if (part == 0 && from[k] >= 0) copy_async4(scale_at(stage) + k * (kCompactThreads * 4), scales + (from[k] & ~3));
       // the row to write, and which byte of its scale's word is meant
       asm volatile("st.shared.s32 [%0], %1;" ::"r"(row_at(stage) + k * (kCompactThreads * 4)), "r"(to) : "memory");
@@ -238,7 +268,7 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
   int hi = n, step = 0, probe = 0, seen = 0;             // it lies in [lo, hi], and is lo in the end
   auto look = [&] {
     step = (hi - lo + kCompactThreads - 1) / kCompactThreads;
-    probe = lo + (tid + 1) * step - 1;            // the last of this thread's part
+    probe = lo + (min(tid, kCompactThreads - 1) + 1) * step - 1;   // the last of this thread's part
     seen = probe < hi ? __ldg(keep + probe) : probe;
   };
   auto narrow = [&] {
@@ -276,36 +306,53 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
     bad |= shared && lo < n && column >= lo / C.P.by_page;
   }
 #pragma unroll
-  for (int s = 0; s < kCompactStages - 1; ++s) fetch(s, s, x[s]);
+  for (int s = 0; s < kCompactStages - 1; ++s)
+    if (mine) fetch(s, s, x[s]);
   Ahead x0 = x[kCompactStages - 1], x1 = x[kCompactStages];
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(C.P.status, kPagedBadIndex);
   const int steps = bad || lo >= n ? 0 : (n - start - 1) / stride + 1;
   cluster_wait();
-  // This warp's part of a chunk has arrived in shared memory: the CTAs are told.
-  // Only reads have to be over, so nothing that was written is waited for.
+  // A warp's part of a chunk has arrived in shared memory: its CTA is told, before
+  // the warp writes the chunk ahead of it, and by the last warp all CTAs are.  One CTA
+  // alone needs no more than its own barrier.
+  if (warp == kCompactTeller) {
+    uint32_t parity = 0;
+#pragma unroll 1
+    for (int s = 0, stage = 0; ctas > 1 && s < steps; ++s) {
+      const bool ok = paged_wait(smem_addr(&landed[stage]), parity, kCompactTimeoutNs, &abort);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (lane < ctas)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(&bars[stage], lane)) : "memory");
+      __syncwarp();
+      if (++stage == kCompactStages) stage = 0, parity ^= 1u;
+    }
+  }
   auto has_read = [&](int stage) {
     __syncwarp();
-    if (lane < ctas)
-      asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(&bars[stage], lane)) : "memory");
+    if (lane == 0) mbar_arrive(smem_addr(&landed[stage]));
   };
+  uint64_t* const all = ctas > 1 ? bars : landed;
   asm volatile("cp.async.wait_group %0;" ::"n"(kCompactStages - 2) : "memory");
-  if (steps > 0) has_read(0);                     // all that is told is waited for
+  if (steps > 0 && mine) has_read(0);                     // all that is told is waited for
   int stage = 0;                                  // of chunk s
   uint32_t parity = 0;
 #pragma unroll 1
-  for (int s = 0; s < steps; ++s) {
+  for (int s = 0; s < steps && mine; ++s) {
     fetch(s + kCompactStages - 1, stage ? stage - 1 : kCompactStages - 1, x0);
     x0 = x1;
     paged(s + kCompactStages, x0);
     listed(s + kCompactStages + 1, x1);
-    bool ok = paged_wait(smem_addr(&bars[stage]), parity, kCompactTimeoutNs, &abort);
+    bool ok = told_wait(smem_addr(&all[stage]), parity, &abort);
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (!ok) {
       abort = 1;
       atomicOr(C.P.status, kStatusTimeoutBit);
       break;
     }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kCompactStages - 2) : "memory");
+    const int next = stage + 1 < kCompactStages ? stage + 1 : 0;
+    if (s + 1 < steps) has_read(next);
     const uint32_t at = codes_at(stage);
     int to[kEach];
 #pragma unroll
@@ -325,9 +372,6 @@ __global__ void __launch_bounds__(kCompactThreads, kCompactCtas) kv_compact_kern
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at + j * 512));
       if (row >= 0) *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(row) * 128 + (lane & (kLanes - 1)) * 16) = v;
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kCompactStages - 2) : "memory");
-    const int next = stage + 1 < kCompactStages ? stage + 1 : 0;
-    if (s + 1 < steps) has_read(next);
     __syncwarp();
     if (next == 0) parity ^= 1u;
     stage = next;

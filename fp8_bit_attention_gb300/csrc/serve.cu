@@ -179,7 +179,7 @@ ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const in
   const int64_t fit = units >= dev->sms ? 1 : 18 * dev->sms / 5 / (units * parts);
   const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kCompactClusters, fit)));
   return launch_clusters(halves ? kv_compact_kernel<64> : kv_compact_kernel<128>,
-                         dim3(ctas, static_cast<unsigned>(units / p->rows * parts), static_cast<unsigned>(p->rows)), kCompactThreads,
+                         dim3(ctas, static_cast<unsigned>(units / p->rows * parts), static_cast<unsigned>(p->rows)), kCompactThreads + 32,
                          halves ? CompactShape<64>::kSmem : CompactShape<128>::kSmem, ctas, static_cast<cudaStream_t>(stream), C);
 }
 

@@ -301,6 +301,33 @@ def test_compaction_of_many_chunks_is_repeatable():
         assert all(torch.equal(x[table[0, i // page], :, i % page], y) for x, y in zip(_arrays(c), want))
 
 
+@pytest.mark.parametrize("rows, heads, most, page", [(5, 4, 40000, 64), (9, 5, 27000, 16), (11, 6, 16000, 48), (8, 9, 12000, 128),
+                                                     (10, 5, 24000, 64), (13, 7, 5000, 16), (70, 3, 4000, 32), (6, 3, 40000, 64)])
+@pytest.mark.parametrize("kind", ["some", "window", "late"])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_compaction_by_clusters_of_every_size(rows, heads, most, page, kind, per_head):
+    """Ragged rows of many chunks: 8, 6, 4, 3, 5 CTAs a sequence and head, one
+    (twice), and 7 with half of the channels each (on 152 SMs)."""
+    g = np.random.default_rng(rows)
+    lens = g.integers(1, most // 8, rows)
+    lens[::3] = g.integers(most // 2, most, len(lens[::3]))
+    lens[rows // 2] = most
+    table, refs = _held(lens, page, rows)
+    c = _filled(len(refs), heads, page, rows + 1)
+    p = _state(table, lens, refs, page)
+    keep, cu = _keep(lens, kind, heads if per_head else 1, 5)
+    all_keep = torch.tensor(np.broadcast_to(keep, (heads, keep.shape[1])), device="cuda")
+    of = torch.tensor(np.repeat(np.arange(rows), np.diff(cu)), device="cuda")
+    i = torch.arange(keep.shape[1], device="cuda") - torch.tensor(cu, device="cuda")[of]
+    pages, head = p.page_table.long(), torch.arange(heads, device="cuda").unsqueeze(1)
+    free = torch.tensor(np.nonzero(refs == 0)[0], device="cuda")
+    want = [(x[pages[of, all_keep // page], head, all_keep % page], x[free]) for x in (c.k, c.v, c.k_scale, c.v_scale)]
+    ovc.kv_cache_compact(c, p, _i32(keep if per_head else keep[0]), _i32(cu))
+    for x, (kept, unheld) in zip((c.k, c.v, c.k_scale, c.v_scale), want):
+        assert torch.equal(x[pages[of, i // page], head, i % page], kept) and torch.equal(x[free], unheld)
+    assert Pages(table, lens, refs, page).same_as(p) and ovc.device_status() == 0
+
+
 def test_lists_of_heads_may_be_views():
     n, heads, page = 100, 4, 16
     table, refs = _held([n], page, 1)

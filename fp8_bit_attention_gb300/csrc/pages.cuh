@@ -221,7 +221,7 @@ __device__ __forceinline__ int row_of_rank(const uint32_t* start, int b, int row
   return b;
 }
 
-__device__ __forceinline__ uint32_t capped_sum(uint32_t a, uint32_t b) { return min(a + b, 0x80000000u); }
+__device__ __forceinline__ uint32_t capped_sum(uint32_t a, uint32_t b) { return min(a + b, 0x7FFFFFFFu); }
 
 __global__ void __launch_bounds__(kReserveThreads, 1) pages_reserve_kernel(PagesView P, const int32_t* __restrict__ lens,
                                                                         ReserveOut out, int chunk_shift, uint32_t hash) {
@@ -315,8 +315,9 @@ __global__ void __launch_bounds__(kReserveThreads, 1) pages_reserve_kernel(Pages
     if (static_cast<int>(count) == P.refs[S.key[h]]) atomicMax(S.val + h, count << 16 | (b + 1));
   }
   __syncthreads();
-  // Sums over the rows, in order.  They stop at 2^31, more than any cache's pages:
-  // a start is exact below that, and beyond it nothing is granted.
+  // Sums over the rows, in order.  They stop at 2^31 - 1, more than any cache's pages
+  // (2^27), and two of them fit 32 bits: a start is exact below that, and beyond it
+  // nothing is granted.
   uint32_t carry = 0;
   for (int b0 = 0; b0 < P.rows; b0 += kReserveThreads) {
     const int b = b0 + tid;

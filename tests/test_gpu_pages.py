@@ -133,6 +133,19 @@ def test_a_row_may_hold_every_page():
     assert p.kv_lens.tolist() == [1, 1024 * (n - 1)] and p.page_table[0, 0] == n - 1 and ovc.device_status() == 0
 
 
+def test_wishes_beyond_32_bits():
+    """Rows that together want more than 2^32 pages: only the first fits."""
+    rows, n = 1026, 1 << 22
+    if torch.cuda.mem_get_info()[0] < 4 * rows * n + (8 << 30):
+        pytest.skip("needs 25 GB")
+    p = ovc.kv_pages(n, rows, n, 16)
+    src, dst, tokens = _reserve(p, np.full(rows, 16 * n))
+    assert (src == -1).all() and (dst == -1).all() and not tokens.any()
+    assert p.kv_lens[0] == 16 * n and not p.kv_lens[1:].any() and (p.refs == 1).all()
+    assert torch.equal(p.page_table[0], torch.arange(n, dtype=torch.int32, device="cuda"))
+    assert all((row == -1).all() for row in p.page_table[1:].split(128)) and ovc.device_status() == 0
+
+
 def test_bad_rows_are_reported_and_left_alone():
     def state():
         return _state([[0, 1, -1], [2, 77, -1], [3, -1, -1], [4, -1, -1]], [20, 20, 60, 16], [1, 1, 1, 1, 1, 0, 0, 0], 16)

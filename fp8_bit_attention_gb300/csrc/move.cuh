@@ -293,7 +293,17 @@ __global__ void __launch_bounds__(kCompactThreads + 32, kCompactCtas) kv_compact
   }
   if (lo < hi) look();
   const int columns = n > 0 ? (n - 1) / C.P.by_page + 1 : 0;
-  int column = start / C.P.by_page + tid, page = column < columns ? __ldg(table + column) : -1;
+  // Where the pages are looked at from: no head moves a token before it.  With a list
+  // a head, all clusters of a sequence decide alike whether it is left alone, each by
+  // every head's list: `from` lies a few of the search's steps before this head's
+  // start, so that most often the others begin to move behind it too.
+  const bool lists = C.keep_stride > 0;
+  int from = lists ? max(0, start - n / 64) : start;
+  bool before = false;
+  if (lists && from > 0)
+#pragma unroll 1
+    for (int k = tid; k < C.c.heads; k += blockDim.x) before |= __ldg(C.keep + k * C.keep_stride + a0 + from - 1) != from - 1;
+  int column = from / C.P.by_page + tid, page = column < columns ? __ldg(table + column) : -1;
 #pragma unroll
   for (int s = 0; s < kCompactStages; ++s) paged(s, x[s]);
   while (lo < hi) {
@@ -301,15 +311,32 @@ __global__ void __launch_bounds__(kCompactThreads + 32, kCompactCtas) kv_compact
     if (lo < hi) look();
   }
   // Pages that will be written must be this row's own.
-  for (; column < columns; column += kCompactThreads, page = column < columns ? __ldg(table + column) : -1) {
-    const bool shared = page < 0 || page >= C.c.pages || __ldg(C.P.refs + page) > 1;
-    bad |= shared && lo < n && column >= lo / C.P.by_page;
+  if (lists && from > 0 && __syncthreads_or(before)) {
+    column = tid;
+    page = column < columns ? __ldg(table + column) : -1;
   }
+  int last = -1;                                  // of this thread's columns, with a page that is not
+  for (; column < columns; column += kCompactThreads, page = column < columns ? __ldg(table + column) : -1)
+    if (page < 0 || page >= C.c.pages || __ldg(C.P.refs + page) > 1) last = column;
 #pragma unroll
   for (int s = 0; s < kCompactStages - 1; ++s)
     if (mine) fetch(s, s, x[s]);
   Ahead x0 = x[kCompactStages - 1], x1 = x[kCompactStages];
-  bad = __syncthreads_or(bad);
+  if (__builtin_expect(__syncthreads_or(last >= 0), 0)) {
+    if (tid == 0) found = -1;
+    __syncthreads();
+    if (last >= 0) atomicMax(&found, last);
+    __syncthreads();
+    // Positions ascend, so a head writes to a column up to that one exactly if the
+    // last position of it does not stay.  (A list that does not ascend may say
+    // otherwise: this head's own first that moves counts too.)
+    const int end = min(n, (found + 1) * C.c.page);
+    bad = lo < end;
+    if (lists)
+#pragma unroll 1
+      for (int k = tid; k < C.c.heads; k += blockDim.x) bad |= __ldg(C.keep + k * C.keep_stride + a0 + end - 1) != end - 1;
+    bad = __syncthreads_or(bad);
+  }
   if (bad && tid == 0) atomicOr(C.P.status, kPagedBadIndex);
   const int steps = bad || lo >= n ? 0 : (n - start - 1) / stride + 1;
   cluster_wait();

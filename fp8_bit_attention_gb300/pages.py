@@ -155,7 +155,7 @@ def kv_cache_compact(cache: KVCache, pages: KVPages, keep: torch.Tensor, cu_keep
     gives back the pages behind.
 
     Every page that is written must be the sequence's alone: one with a shared
-    page among them is left as it was and reported by :func:`device_status` (7);
+    page among them is left as it was, in all heads, and reported by :func:`device_status` (7);
     so are positions that do not ascend or lie outside, which are not moved."""
     dev = _device(cache.k, pages.refs, keep, cu_keep, stream=stream)
     if cache.pages != pages.refs.shape[0] or cache.page != pages.page:

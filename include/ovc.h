@@ -594,11 +594,11 @@ ovc_status ovc_kv_copy(const ovc_kv_cache* to, const ovc_kv_cache* from, const i
  * behind the kept tokens is left as it is or holds parts of moved tokens; pages and
  * kv_lens do not change (ovc_kv_pages_release with the new lengths, after every
  * layer's cache).  Every page that is written is this row's alone (refs 1): a
- * sequence with another is reported and left as it was.  Positions that do not
- * ascend or lie outside are not moved and reported (but for some among the first
- * that stay, which a search passes over), the sequence's other tokens then
- * unspecified.  c->pages and c->page are those of `p`; n: the size of a list;
- * heads <= 32767. */
+ * sequence with another, in any head, is reported and left as it was in all heads.
+ * Positions that do not ascend or lie outside are not moved and reported (but for
+ * some among the first that stay, which a search passes over), the sequence's other
+ * tokens then unspecified.  c->pages and c->page are those of `p`; n: the size of a
+ * list; heads <= 32767. */
 ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const int32_t* keep, int64_t keep_stride,
                           const int32_t* cu_keep, int64_t n, void* stream);
 

@@ -372,6 +372,54 @@ def test_shared_pages_are_not_written():
     assert ovc.device_status() == BAD_INDEX and _holds(c, old)
 
 
+@pytest.mark.parametrize("heads, length, page", [(3, 44, 16), (1, 90, 16), (2, 300, 48), (8, 700, 16), (5, 3001, 64), (9, 5000, 1024),
+                                                 (2, 40000, 16), (300, 100, 16), (4, 20000, 128)])
+@pytest.mark.parametrize("pairs", [1, 4, 20])
+def test_a_sequence_with_shared_pages_is_left_alone_in_all_heads(heads, length, page, pairs):
+    """A list for each head.  The second row of each pair shares whole pages of the
+    first's and drops seven tokens a head: behind them in all heads, within them in
+    one, in some or in all, or only at the end, where nothing moves."""
+    pairs = max(1, min(pairs, 900000 // (heads * length)))
+    g = np.random.default_rng(heads + length)
+    held = -(-length // page)
+    table = np.arange(2 * pairs * held).reshape(2 * pairs, held)
+    keep, refused = [], []
+    for i in range(pairs):
+        shared = [held, held // 2, 1, held - 1][i % 4] if held > 1 else 1
+        table[2 * i + 1, :shared] = table[2 * i, :shared]
+        end = shared * page
+        inside = {0: [], 1: [int(g.integers(heads))], 2: g.choice(heads, heads // 2, replace=False), 3: range(heads)}[int(g.integers(4))]
+        behind = np.arange(min(end, length - 7), length)
+        lists = []
+        for h in range(heads):
+            drop = g.choice(min(end, length) if h in inside else behind, 7, replace=False)
+            if h not in inside and g.random() < 0.3:
+                drop = np.arange(length - 7, length)
+            lists.append(np.delete(np.arange(length), drop))
+        lists = np.stack(lists)
+        kept = -(-(length - 7) // page)                       # columns of the kept tokens
+        moved = [np.nonzero(k != np.arange(length - 7))[0] for k in lists]
+        refused.append(any(len(m) and m[0] // page < min(shared, kept) for m in moved))
+        keep += [np.broadcast_to(np.arange(length), (heads, length)), lists]
+    pages, refs = 2 * pairs * held, np.bincount(table.ravel(), minlength=2 * pairs * held)
+    cu = np.r_[0, np.cumsum([k.shape[1] for k in keep])]
+    c, p = _filled(pages, heads, page, 1), _state(table, [length] * (2 * pairs), refs, page)
+    old = [x.clone() for x in (c.k, c.v, c.k_scale, c.v_scale)]
+    ovc.kv_cache_compact(c, p, _i32(np.concatenate(keep, 1)), _i32(cu))
+    assert ovc.device_status() == (BAD_INDEX if any(refused) else 0)
+    changed = np.zeros(pages, bool)
+    head, i = torch.arange(heads, device="cuda").unsqueeze(1), torch.arange(length - 7, device="cuda")
+    for b, no in enumerate(refused):
+        if not no:
+            row, k = p.page_table[2 * b + 1].long(), torch.tensor(keep[2 * b + 1], device="cuda")
+            own = refs[table[2 * b + 1]] == 1
+            changed[table[2 * b + 1][own]] = True
+            for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), old):
+                assert torch.equal(x[row[i // page], head, i % page], y[row[k // page], head, k % page])
+    same = torch.tensor(np.nonzero(~changed)[0], device="cuda")
+    assert all(torch.equal(x[same], y[same]) for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), old))
+
+
 @pytest.mark.parametrize("keep, cu", [([0, 2, 2, 5], [0, 4, 4]), ([0, 3, 2], [0, 3, 3]), ([0, 30], [0, 2, 2]), ([-1, 3], [0, 2, 2]),
                                       ([0, 1], [0, 3, 3]), ([0, 1], [1, 0, 0]), ([0, 1], [-1, 0, 0]), (list(range(1, 25)), [0, 24, 24])], ids=str)
 def test_bad_positions_are_reported(keep, cu):

@@ -554,9 +554,10 @@ typedef struct {
  * pages that it lacks; where its last page is partly filled and others hold it
  * too (refs > 1), it gets a page in its place as well, so that what it writes next
  * is its own.  If all holders of such a page (refs of them) grow in this call,
- * the highest row keeps it.  The lowest free pages are taken, in the order of
- * rows and then of columns.  A row grows only if the rows up to and including it
- * need no more pages than are free: kv_lens says which did.
+ * the highest row keeps it; if more rows than refs says, those are reported and
+ * stay.  The lowest free pages are taken, in the order of rows and then of columns.
+ * A row grows only if the rows up to and including it need no more pages than are
+ * free: kv_lens says which did.
  * src, dst and tokens [rows] receive, for each row whose last page was replaced,
  * that page, its successor, and the tokens to copy (ovc_kv_copy, in the cache of
  * each layer, before any row writes new tokens there and before the next of these
@@ -567,7 +568,7 @@ ovc_status ovc_kv_pages_reserve(const ovc_kv_pages* p, const int32_t* lens, int3
 
 /* Let rows shrink to lens[b] tokens (not smaller, negative: it stays): pages
  * that hold none of them are given back (refs - 1, entry -1).  Giving back a page
- * that nobody holds is reported. */
+ * that nobody holds is reported, and leaves its refs as they were. */
 ovc_status ovc_kv_pages_release(const ovc_kv_pages* p, const int32_t* lens, void* stream);
 
 /* Row children[i] becomes a second holder of what row parents[i] holds, for

@@ -166,6 +166,20 @@ def test_bad_rows_are_reported_and_left_alone():
     assert ovc.device_status() == BAD_INDEX and p.refs[6] == 0
 
 
+def test_pages_with_too_few_holders_are_reported():
+    """More entries name a page than refs counts: given back, or left for one of their
+    own, by more rows than hold it, its count stays 0, or as it is."""
+    rows = 500
+    p = _state(np.zeros((rows, 1), int), [5] * rows, [rows - 100, 0], 16)
+    ovc.kv_pages_release(p, _i32([0] * rows))
+    assert ovc.device_status() == BAD_INDEX and p.refs.tolist() == [0, 0]
+    assert not p.kv_lens.any() and (p.page_table == -1).all()
+    p = _state([[0, 1, -1], [0, 1, -1], [2, 1, -1], [3, -1, -1]], [20, 20, 20, 10], [2, 2, 1, 1, 0, 0, 0, 0, 0], 16)
+    src, dst, tokens = _reserve(p, [24, 24, 34, 40])
+    assert ovc.device_status() == BAD_INDEX and p.kv_lens.tolist() == [20, 20, 20, 40] and p.refs.tolist() == [2, 2, 1, 1, 1, 1, 0, 0, 0]
+    assert (src == -1).all() and (dst == -1).all() and not tokens.any() and p.page_table.tolist()[2:] == [[2, 1, -1], [3, 4, 5]]
+
+
 @pytest.mark.parametrize("parents, children, done", [([0, 0], [2, 2], []), ([0, 2], [2, 3], [3]), ([0, 1], [1, 2], [2]),
                                                      ([0, 9], [2, 3], [2]), ([0, -1], [2, -1], [2]), ([0, -1], [2, 3], [2]),
                                                      ([0, 0], [2, 4], [2]), ([0, 3], [2, 3], [2]), ([4, 0], [2, 3], [3])], ids=str)

@@ -251,6 +251,31 @@ __device__ __forceinline__ FF from_lane(const FF& x, int lane) {
   return {__shfl_sync(0xFFFFFFFFu, x.hi, lane), __shfl_sync(0xFFFFFFFFu, x.lo, lane)};
 }
 
+// Whether sequence b's starts are sound.
+__device__ __forceinline__ bool starts_ok(const DraftParams& P, int a0, int a1) { return a0 >= 0 && a1 >= a0 && a1 <= P.N; }
+
+// -1 for the rows of no sequence, by the first CTA of sequence b: those before the
+// first sequence, those behind the last, and what a run of sequences whose starts are
+// not sound leaves between its neighbours, by the first of the run.
+__device__ __forceinline__ void leave_unnamed(const DraftParams& P, int b, int batch, int a0, int a1, int* next) {
+  const int tid = threadIdx.x, threads = blockDim.x, rows = P.N + batch;
+  const bool ok = starts_ok(P, a0, a1);
+  int from = b ? a0 + b : 0, to = ok ? a0 + b : rows;
+  if (!ok) {
+    if (b && !starts_ok(P, P.cu[b - 1], a0)) return;
+    if (tid == 0) *next = batch;
+    __syncthreads();
+    for (int k = b + 1; k < batch; k += threads) {
+      if (k + tid < batch && starts_ok(P, P.cu[k + tid], P.cu[k + tid + 1])) atomicMin(next, k + tid);
+      if (__syncthreads_or(*next < batch)) break;
+    }
+    if (*next < batch) to = P.cu[*next] + *next;
+  }
+  for (int i = from + tid; i < to; i += threads) P.tokens[i] = -1;
+  if (ok && b == batch - 1)
+    for (int i = a1 + batch + tid; i < rows; i += threads) P.tokens[i] = -1;
+}
+
 // One cluster a sequence.  Every CTA finds the first draft that does not stay, sums
 // the weights of its part of that row tile by tile, and learns the other parts'
 // sums; the one whose part holds the drawn place looks for it in one tile again.
@@ -277,9 +302,14 @@ __global__ void __launch_bounds__(kDraftThreads<kDraft>, kDraftCtas) verify_draf
   const float u = __ldg(P.sample_u + b);              // here, so that nothing waits for it later
   const int a0 = P.cu ? P.cu[b] : b * P.each, a1 = P.cu ? P.cu[b + 1] : a0 + P.each;
   // No CTA leaves before the last barrier, whatever it finds: others write to it.
-  const bool bad = a0 < 0 || a1 < a0 || a1 > P.N;
+  const bool bad = !starts_ok(P, a0, a1);
   const int n = bad ? 0 : a1 - a0;
   const int64_t row0 = bad ? 0 : static_cast<int64_t>(a0) + b;         // of the target's probabilities
+
+  if (rank == 0 && P.cu) {
+    const int batch = gridDim.x / ctas;
+    if (bad || (b == 0 && a0 > 0) || (b == batch - 1 && a1 < P.N)) leave_unnamed(P, b, batch, a0, a1, &again);
+  }
 
   // The first draft that does not stay: 2 i, or 2 i + 1 where there is none at i.
   if (tid == 0) stop = 2u * n + 1u;

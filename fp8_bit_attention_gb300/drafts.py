@@ -51,9 +51,11 @@ def verify_drafts(target_probs: torch.Tensor, drafts: torch.Tensor, accept_u: to
     whose running sum exceeds ``sample_u`` times the total.
 
     Returns int32 ``tokens`` [N + B], in the order of ``target_probs``: the drafts
-    that stayed, the next token (-1 if its row leaves nothing), -1 for the rest;
-    and ``accepted`` [B], how many stayed, so that a sequence whose drafts are in
-    its cache goes on with ``kv_lens - n + accepted`` tokens."""
+    that stayed, the next token (-1 if its row leaves nothing), -1 for the rest and
+    for rows of no sequence; and ``accepted`` [B], how many stayed, so that a
+    sequence whose drafts are in its cache goes on with ``kv_lens - n + accepted``
+    tokens.  A sequence whose starts descend or leave [0, N] has no rows and accepts
+    0; :func:`device_status` reports it (7)."""
     dev = _device(target_probs, drafts, accept_u, sample_u, draft_probs, cu_drafts, stream=stream)
     dtype = _TYPES.get(target_probs.dtype)
     if dtype is None:
@@ -85,7 +87,9 @@ def verify_drafts(target_probs: torch.Tensor, drafts: torch.Tensor, accept_u: to
         # two tensors: views of a new one take the host longer than allocating them
         tokens = torch.empty(n + batch, dtype=torch.int32, device=dev)
         accepted = torch.empty(batch, dtype=torch.int32, device=dev)
-        if batch:
+        if not batch:
+            tokens.fill_(-1)
+        else:
             check(lib().ovc_verify_drafts(_byref(desc), tokens.data_ptr(), accepted.data_ptr(), s), "ovc_verify_drafts")
         return tokens, accepted
 

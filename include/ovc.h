@@ -638,9 +638,10 @@ typedef struct {
  * are then distributed as the target's own.  A NaN rejects its draft and leaves
  * its token without weight; a row that leaves nothing to draw from gives -1.
  * tokens [N + B] int32, in target's order: the drafts that stayed, the next
- * token, -1 for the rest.  accepted [B] int32: how many stayed.  Where cu_drafts
- * descends or leaves [0, N], that sequence's accepted is 0, its tokens are left as
- * they were, and it is reported.
+ * token, -1 for the rest, and for rows of no sequence (before cu_drafts[0], behind
+ * the last).  accepted [B] int32: how many stayed.  Where cu_drafts descends or
+ * leaves [0, N], that sequence has no rows, its accepted is 0, and it is reported;
+ * rows that sequences beside it then share hold the tokens of one, or -1.
  * u * q < p is exact and sums hold 48 bits (FP32 pairs, then FP64): a result
  * differs from exact arithmetic's only where sample_u lies within about V * 2^-46
  * of a border. The same inputs give the same tokens. */

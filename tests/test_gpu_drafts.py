@@ -250,6 +250,34 @@ def test_bad_drafts_and_starts_are_reported():
         assert accepted[bad] == 0 and ovc.device_status() == 0
 
 
+@pytest.mark.parametrize("cu", [[0, 3, 2], [-1, 2, 4], [0, 2, 5], [1, 2, 4], [2, 2, 2], [0, 2, 3], [0, 0, 0], [5, 2, 4], [0, 4, 3], [3, 2, 1],
+                                [0, -1, -1, 1, 3, 9, 4, 4], [2, 2, 7, 2, 3, -5], [9, 9, 9, 9], [-1, 0, 0, 4], [3, 4, 5], [4], [1, 3],
+                                [-1] * 700 + [2, 3] + [9] * 700, [0] * 3 + [-7] * 1400 + [3, 4, 4], [-1] * 600], ids=lambda x: str(x[:9]))
+@pytest.mark.parametrize("vocab", [50, 40000])
+def test_rows_of_no_sequence_hold_no_token(cu, vocab):
+    """Starts that do not begin at 0, do not reach N, or are none."""
+    n, batch = 4, len(cu) - 1
+    c = Case([n], vocab, torch.float32, seed=14)
+    p = c.p.repeat(-(-(n + batch) // (n + 1)), 1)[:n + batch].contiguous()
+    us = torch.rand(batch, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    starts = _i32(cu)
+    ovc.device_status()
+    held = [torch.full((n + batch,), 12345, dtype=torch.int32, device="cuda") for _ in range(4)]
+    del held                                            # what a new tensor is likely to hold
+    tokens, accepted = ovc.verify_drafts(p, c.drafts, c.u, us, draft_probs=c.q, cu_drafts=starts)
+    good = [b for b in range(batch) if 0 <= cu[b] <= cu[b + 1] <= n]
+    assert ovc.device_status() == (0 if len(good) == batch else BAD_INDEX)
+    rows = sorted(r for b in good for r in range(cu[b] + b, cu[b + 1] + b + 1))
+    assert len(rows) == len(set(rows))
+    got, kept = tokens.cpu().numpy(), accepted.cpu().numpy()
+    assert (np.delete(got, rows) == -1).all() and not np.delete(kept, good).any()
+    host = [x.double().cpu().numpy() for x in (p, c.q, c.u, us)]
+    drafts = c.drafts.cpu().numpy()
+    for b in good[:8] + good[-8:]:
+        want = verify(host[0][b:], host[1], drafts, cu[b:b + 2], host[2], None)
+        check_verified(got[b:], kept[b:], drafts, cu[b:b + 2], host[3][b:], want)
+
+
 def test_long_strides():
     """Rows beyond 32-bit offsets."""
     wide = torch.empty((3, 1 << 31), dtype=torch.bfloat16, device="cuda")[:, :1000]

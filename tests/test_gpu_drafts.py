@@ -110,6 +110,18 @@ def test_rows_of_different_alignment(dtype, vocab):
         assert torch.equal(got[0], whole[0]) and torch.equal(got[1], whole[1])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch", [33, 36, 42, 50, 60, 80, 100, 140])
+@pytest.mark.parametrize("lookup", [False, True])
+def test_clusters_of_every_size(dtype, batch, lookup):
+    """8, 7, 6, 5, 4, 3, 2 CTAs and one a sequence (on 152 SMs), each with drafts, in
+    any number, or none."""
+    counts = [1 + b % 2 if b % 5 else 0 for b in range(batch)]
+    c = Case(counts, 33001 + batch, dtype, lookup=lookup, sharp=0.5, cut=batch % 4 == 0, seed=batch)
+    c.check(*c.run())
+    assert ovc.device_status() == 0
+
+
 @pytest.mark.parametrize("drafted", [False, True])
 def test_large_vocabularies_of_many_sequences(drafted):
     """Tiles of several lines: one row of the target (and of the draft) for all, no two random numbers alike."""

@@ -516,6 +516,43 @@ def test_captured_step_follows_new_lengths_and_lists():
     ovc.device_status()
 
 
+def test_captured_compactions_at_the_same_time():
+    """Two graphs, of caches of their own, on two streams, replayed as lists change:
+    many chunks, several CTAs a sequence and head."""
+    rows, heads, page, most = 5, 4, 64, 30000
+    g = np.random.default_rng(1)
+    parts = []
+    for i in range(2):
+        lens = g.integers(most // 2, most, rows)
+        table, refs = _held(lens, page, i)
+        s = {"p": _state(table, lens, refs, page), "c": _filled(len(refs), heads, page, i), "lens": lens, "refs": refs, "table": table,
+             "keep": _i32(np.zeros((heads, int(lens.sum())))), "cu": _i32(np.zeros(rows + 1)), "stream": torch.cuda.Stream(),
+             "graph": torch.cuda.CUDAGraph()}
+        ovc.kv_cache_compact(s["c"], s["p"], s["keep"], s["cu"])
+        with torch.cuda.graph(s["graph"]):
+            ovc.kv_cache_compact(s["c"], s["p"], s["keep"], s["cu"])
+        parts.append(s)
+    for step in range(4):
+        for s in parts:
+            keep, cu = _keep(s["lens"], ["some", "window", "late", "some"][step], heads, step)
+            s["keep"][:, :keep.shape[1]].copy_(_i32(keep))
+            s["cu"].copy_(_i32(cu))
+            of = torch.tensor(np.repeat(np.arange(rows), np.diff(cu)), device="cuda")
+            k, i = torch.tensor(keep, device="cuda"), torch.arange(keep.shape[1], device="cuda") - _i32(cu).long()[of]
+            t, head = s["p"].page_table.long(), torch.arange(heads, device="cuda").unsqueeze(1)
+            s["at"] = (t[of, i // page], head, i % page)
+            s["want"] = [x[t[of, k // page], head, k % page] for x in (s["c"].k, s["c"].v, s["c"].k_scale, s["c"].v_scale)]
+        torch.cuda.synchronize()
+        for s in parts:
+            with torch.cuda.stream(s["stream"]):
+                s["graph"].replay()
+        torch.cuda.synchronize()
+        for s in parts:
+            assert all(torch.equal(x[s["at"]], y) for x, y in zip((s["c"].k, s["c"].v, s["c"].k_scale, s["c"].v_scale), s["want"]))
+            assert Pages(s["table"], s["lens"], s["refs"], page).same_as(s["p"])
+        assert ovc.device_status() == 0
+
+
 def test_calls_on_a_stream_and_side_by_side():
     side = torch.cuda.Stream()
     states = []

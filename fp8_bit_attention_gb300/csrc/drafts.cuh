@@ -46,6 +46,15 @@ __device__ __forceinline__ float prob(const void* p, int64_t i) {
 // would move the borders between tokens by more than the least of them are wide,
 // and the FP64 units (2 additions a cycle and SM) would take several times as long
 // as the memory.
+//
+// What sums are off by at most, in units of 2^-48 (half a step, squared) of the total:
+// a lane's K weights in each of its four sums K^2 / 2 + 4 K (the lower part grows by a
+// step's half with each, and is rounded each time); the 7 merges up to a tile's sum
+// 14 (K + 8); its place among the tiles and CTAs 2 K + 45, and 3 for every 32 tiles; the
+// last search 66.  A running sum against u times the total: K^2 + 40 K + 380.  K = 2 j + 1
+// where a lane loads j times 16 bytes of 16-bit weights (V > 256 (j - 1) - 8), j + 1 of
+// FP32 (V > 128 (j - 1) - 4), 16 * 2^s + 1 at most in tiles of 2^s lines (V > 2^19 *
+// 2^s): less than 4 (V + 128) for every V.
 struct FF {
   float hi, lo;
 };

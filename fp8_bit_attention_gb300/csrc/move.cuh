@@ -77,10 +77,10 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(CopyParams P) {
 // Told by each warp itself, for the two cases below: 47 and 44 us.
 //
 // Reads and writes 258 bytes a token and head: 49152 tokens of one sequence x 8
-// heads, 203 MB, in 40 us (5.1 TB/s, 76% of the measured copy rate), of which the
-// chunks take 30 (the memory's rate) and the chain of lookups before the first
-// token 6; half of 8 ragged sequences up to 32768 x 8 heads, 161 MB, in 36 us.
-// A few tokens at the sequences' ends: 7 us, that chain.
+// heads, 203 MB, in 42 us (4.9 TB/s, 73% of the measured copy rate), of which the
+// chunks take 35 and the chain of lookups before the first token 6; half of 8 ragged
+// sequences up to 32768 x 8 heads, 161 MB, in 38 us.  A few tokens at the sequences'
+// ends: 7.5 us, that chain.
 // Tried: a hardware barrier of the cluster for each chunk instead of the counting
 // ones 55 and 47 us; values held in registers, not in shared memory 99 and 70 us.
 // ---------------------------------------------------------------------------
@@ -90,8 +90,8 @@ constexpr int kCompactCtas = 2;                         // of an SM
 constexpr int kCompactSorted = 64;                      // most sequences that are put in order
 constexpr int kCompactClusters = 8;                     // most CTAs of a cluster
 // Chunks in shared memory.  Two, three (a CTA less an SM) and four (two less): 8
-// sequences of 16384, half kept, 61, 52 and 63 us, 32 of 4096 86, 71 and 84 us, the
-// ragged ones above 38, 36 and 45 us.
+// sequences of 16384, half kept, 56, 54 and 69 us, three quarters of 32 of 4096 73, 71
+// and 88 us, the ragged ones above 40, 38 and 50 us.
 constexpr int kCompactStages = 3;
 constexpr uint64_t kCompactTimeoutNs = 4000000000ull;   // of a wait
 constexpr unsigned kStatusTimeoutBit = 1u;              // of the device status word
@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(kCompactThreads + 32, kCompactCtas) kv_compact
   const int ctas = cluster_size(), rank = cluster_rank();
   const int part = blockIdx.y & (kEach - 1), kv = blockIdx.y / kEach & 1, h = blockIdx.y / (2 * kEach);
   // The longest sequences go first, so that they are not what remains at the end:
-  // 32 ragged sequences up to 16384, half kept, 94 us without, 83 us with it; a few
-  // tokens of 16 sequences 6.5 and 7.1 us.
+  // 32 ragged sequences up to 16384, half kept, 95 us without, 83 us with it, the 8
+  // ragged ones 43 and 38 us; a few tokens of 16 sequences 6.8 and 7.5 us.
   int b = blockIdx.z;
   if (C.P.rows > 1 && C.P.rows <= kCompactSorted) {
     if (tid < C.P.rows) kept[tid] = C.cu[tid + 1] - C.cu[tid];

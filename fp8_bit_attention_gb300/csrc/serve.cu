@@ -105,9 +105,10 @@ ovc_status ovc_kv_pages_release(const ovc_kv_pages* p, const int32_t* lens, void
   DeviceState* dev = nullptr;
   const ovc_status st = device_state(&dev);
   if (st != OVC_OK) return st;
-  // A CTA a row.  Wide ones where all rows run at once and may drop many pages; 256
-  // and 1024 threads: 256 rows dropping up to 2048 pages 5.5 and 3.8 us, 960 rows
-  // dropping 450 each 7.4 and 10.1 us.
+  // A CTA a row.  Wide ones where all rows run at once and may drop many pages.  128,
+  // 256, 512 and 1024 threads: 256 rows dropping up to 2048 pages 13.2, 8.1, 5.5 and
+  // 4.8 us; 960 rows dropping 450 each 9.1, 7.4, 8.1 and 11.3 us; 64 rows dropping one
+  // or none 3.3, 3.3, 3.2 and 3.5 us.
   const int threads = p->width <= 128 ? 128 : p->width <= 512 || p->rows > 2 * dev->sms ? 256 : 1024;
   pages_release_kernel<<<static_cast<unsigned>(p->rows), threads, 0, static_cast<cudaStream_t>(stream)>>>(view(p, dev), lens);
   return launched();
@@ -169,13 +170,14 @@ ovc_status ovc_kv_compact(const ovc_kv_cache* c, const ovc_kv_pages* p, const in
   const int64_t units = p->rows * c->heads * 2;
   // Half the channels a CTA where clusters of the largest size would leave SMs
   // without two CTAs.  Whole and half: 49152 moved of one sequence of 65536, 8 heads,
-  // 46 and 41 us; 8 sequences up to 32768, half kept, 36 and 38 us.
+  // 49 and 42 us; 8 sequences up to 32768, half kept, 38 and 40 us.
   const bool halves = units * kCompactClusters < kCompactCtas * dev->sms;
   const int parts = halves ? 2 : 1;
   // One CTA a unit where they fill the SMs; else more than run at once, as sequences
   // may differ in length.  2, 4 and 6 CTAs: 8 ragged sequences up to 32768 x 8 heads
-  // 47, 36 and 40 us, 8 of 16384 49, 52 and 57 us.  1 and 2 CTAs, a few tokens of 16
-  // sequences 7.1 and 11.7 us.
+  // 50, 38 and 44 us, 8 of 16384 50, 54 and 59 us.  1 and 2 CTAs: three quarters of 32
+  // sequences of 4096 71 and 82 us, half of 32 ragged ones up to 16384 83 and 89 us, a
+  // few tokens of 16 sequences 7.5 and 13 us.
   const int64_t fit = units >= dev->sms ? 1 : 18 * dev->sms / 5 / (units * parts);
   const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kCompactClusters, fit)));
   return launch_clusters(halves ? kv_compact_kernel<64> : kv_compact_kernel<128>,

@@ -642,9 +642,10 @@ typedef struct {
  * the last).  accepted [B] int32: how many stayed.  Where cu_drafts descends or
  * leaves [0, N], that sequence has no rows, its accepted is 0, and it is reported;
  * rows that sequences beside it then share hold the tokens of one, or -1.
- * u * q < p is exact and sums hold 48 bits (FP32 pairs, then FP64): a result
- * differs from exact arithmetic's only where sample_u lies within about V * 2^-46
- * of a border. The same inputs give the same tokens. */
+ * u * q < p is exact and sums hold 48 bits (pairs of FP32 numbers): a result
+ * differs from exact arithmetic's only where sample_u lies within (V + 128) * 2^-46
+ * of a border (sums below 2^-100: within FP32's least number of it).  The same inputs
+ * give the same tokens. */
 ovc_status ovc_verify_drafts(const ovc_drafts* d, int32_t* tokens, int32_t* accepted, void* stream);
 
 #ifdef __cplusplus

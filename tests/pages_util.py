@@ -136,12 +136,14 @@ def verify(p, q, drafts, cu, accept_u, sample_u):
 def check_verified(tokens, accepted, drafts, cu, sample_u, want):
     """The outputs against :func:`verify`'s.  The drawn token t has a weight, and
     u * total lies between the sums before and up to it, where sums may be off by
-    V * 2^-46 of the total: one lane of 32 adds m <= V / 32 weights in a pair of
-    FP32 numbers, m at most 32, or 32 * 2^s from V = 2^19 * 2^s on.  The k-th
-    addition loses 2^-24 of the pair's lower part, at most k * 2^-24 of the sum, and
-    as much again for the weight's own lower part: (m^2 + m) / 2 * 2^-47 in all, at
-    most V * 2^-47 for these m.  The FP64 sums over lanes, tiles and parts, and those
-    here, are off by less than V * 2^-51 together, and a product by 2^-53."""
+    V * 2^-46 of the total.  The kernel's sums are pairs of FP32 numbers at every
+    level; drafts.cuh derives K^2 + 40 K + 380 units of 2^-48 for a running sum and
+    the total together, with K <= 3 up to V = 248: less than 4 V units from V = 128
+    on, with what the FP64 sums here are off by (V * 2^-52).  Below that one tile has
+    sums of few lanes, and adding 0 is exact: K = 3 weights a sum 17, merges within
+    the lane and over l lanes 2 (4 m + m (m + 1) / 2), m = 2 + log2(l), the search
+    24 + 3 log2(l), a product 3: 105 of 124 at V = 31.  Shorter rows are held to the
+    same, tighter than the kernel's bound of (V + 128) * 2^-46."""
     for b, (i, w) in enumerate(want):
         a, n = cu[b], cu[b + 1] - cu[b]
         got = tokens[a + b:a + b + n + 1]

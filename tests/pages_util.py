@@ -142,7 +142,7 @@ def check_verified(tokens, accepted, drafts, cu, sample_u, want):
     on, with what the FP64 sums here are off by (V * 2^-52).  Below that one tile has
     sums of few lanes, and adding 0 is exact: K = 3 weights a sum 17, merges within
     the lane and over l lanes 2 (4 m + m (m + 1) / 2), m = 2 + log2(l), the search
-    24 + 3 log2(l), a product 3: 105 of 124 at V = 31.  Shorter rows are held to the
+    24 + 3 log2(l), a product 3: 123 of 124 at V = 31, l = 8.  Shorter rows are held to the
     same, tighter than the kernel's bound of (V + 128) * 2^-46."""
     for b, (i, w) in enumerate(want):
         a, n = cu[b], cu[b + 1] - cu[b]
